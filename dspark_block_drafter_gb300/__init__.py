@@ -10,8 +10,13 @@ include/dspark.h).  This package is its thin Python binding:
 Importing the package does not load the library; the first call does, and fails
 loudly if the library has not been built.
 """
-from ._abi import (DSPARK_BF16, DSPARK_F32, DSPARK_OK, DSparkError, check,  # noqa: F401
-                   dspark_config, dspark_device_status, dspark_head, dspark_last_error,
-                   dspark_num_slots, dspark_outputs, dspark_propose,
-                   dspark_propose_workspace_size, dspark_status_string, dspark_tree_verify,
-                   dspark_verify, dspark_wait_selftest, lib)
+from ._abi import (DSPARK_BF16, DSPARK_F32, DSPARK_LOSS_MEAN, DSPARK_LOSS_SUM,  # noqa: F401
+                   DSPARK_OK, DSparkError, check, dspark_block_norm,
+                   dspark_block_norm_backward, dspark_block_norm_workspace_size,
+                   dspark_clip_grads, dspark_clip_grads_workspace_size, dspark_config,
+                   dspark_device_status, dspark_grad, dspark_head, dspark_head_loss,
+                   dspark_head_loss_workspace_size, dspark_last_error, dspark_loss_config,
+                   dspark_loss_outputs, dspark_norm_config, dspark_num_slots,
+                   dspark_outputs, dspark_propose, dspark_propose_workspace_size,
+                   dspark_status_string, dspark_tree_verify, dspark_verify,
+                   dspark_wait_selftest, lib)

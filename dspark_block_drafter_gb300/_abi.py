@@ -22,6 +22,8 @@ DSPARK_ERR_DEVICE = 5
 DSPARK_ERR_TIMEOUT = 6
 DSPARK_F32 = 0
 DSPARK_BF16 = 1
+DSPARK_LOSS_SUM = 0
+DSPARK_LOSS_MEAN = 1
 
 c_i32 = ctypes.c_int32
 c_ptr = ctypes.c_void_p
@@ -42,6 +44,26 @@ class dspark_head(ctypes.Structure):
 class dspark_outputs(ctypes.Structure):
     _fields_ = [("draft", c_ptr), ("n_draft", c_ptr), ("topk_ids", c_ptr),
                 ("topk_vals", c_ptr), ("conf", c_ptr), ("logits", c_ptr)]
+
+
+class dspark_loss_config(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("H", c_i32), ("V", c_i32), ("r", c_i32), ("dtype", c_i32),
+                ("reduction", c_i32), ("vocab_pieces", c_i32), ("loss_scale", ctypes.c_float)]
+
+
+class dspark_loss_outputs(ctypes.Structure):
+    _fields_ = [("loss", c_ptr), ("total", c_ptr), ("n_rows", c_ptr), ("d_hidden", c_ptr),
+                ("d_lm_head", c_ptr), ("d_markov_w1", c_ptr), ("d_markov_w2", c_ptr)]
+
+
+class dspark_norm_config(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("H", c_i32), ("dtype", c_i32), ("gate_span", c_i32),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
+
+
+class dspark_grad(ctypes.Structure):
+    _fields_ = [("in_", c_ptr), ("out", c_ptr), ("n", ctypes.c_int64), ("dtype", c_i32)]
 
 
 class DSparkError(RuntimeError):
@@ -87,6 +109,20 @@ SIGNATURES = {
     "dspark_pass_stats": (c_i32, [c_ptr, c_ptr, ctypes.POINTER(c_i32), ctypes.POINTER(c_i32),
                                   ctypes.POINTER(c_i32)]),
     "dspark_wait_selftest": (c_i32, [c_ptr, ctypes.c_size_t, ctypes.c_int64, c_i32, c_ptr]),
+    "dspark_head_loss_workspace_size": (ctypes.c_size_t, [
+        ctypes.POINTER(dspark_loss_config), ctypes.POINTER(dspark_head),
+        ctypes.POINTER(dspark_loss_outputs)]),
+    "dspark_head_loss": (c_i32, [ctypes.POINTER(dspark_loss_config),
+                                 ctypes.POINTER(dspark_head), c_ptr, c_ptr, c_ptr, c_ptr,
+                                 ctypes.POINTER(dspark_loss_outputs), c_ptr, ctypes.c_size_t,
+                                 c_ptr]),
+    "dspark_block_norm": (c_i32, [ctypes.POINTER(dspark_norm_config)] + [c_ptr] * 8),
+    "dspark_block_norm_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(dspark_norm_config)]),
+    "dspark_block_norm_backward": (c_i32, [ctypes.POINTER(dspark_norm_config)] + [c_ptr] * 13
+                                   + [ctypes.c_size_t, c_ptr]),
+    "dspark_clip_grads_workspace_size": (ctypes.c_size_t, [c_i32, ctypes.POINTER(dspark_grad)]),
+    "dspark_clip_grads": (c_i32, [c_i32, ctypes.POINTER(dspark_grad), ctypes.c_float, c_ptr,
+                                  c_ptr, ctypes.c_size_t, c_ptr]),
     "dspark_status_string": (ctypes.c_char_p, [c_i32]),
     "dspark_last_error": (ctypes.c_char_p, []),
 }
@@ -220,6 +256,53 @@ def dspark_wait_selftest(workspace: int, workspace_bytes: int, budget_cycles: in
                          pre_abort: bool = False, stream: int = 0) -> int:
     return lib().dspark_wait_selftest(workspace, workspace_bytes, budget_cycles,
                                       int(pre_abort), stream)
+
+
+def dspark_head_loss_workspace_size(cfg: dspark_loss_config, head: dspark_head,
+                                    out: dspark_loss_outputs) -> int:
+    return lib().dspark_head_loss_workspace_size(ctypes.byref(cfg), ctypes.byref(head),
+                                                 ctypes.byref(out))
+
+
+def dspark_head_loss(cfg: dspark_loss_config, head: dspark_head, hidden: int,
+                     prev: int | None, labels: int, weights: int | None,
+                     out: dspark_loss_outputs, workspace: int, workspace_bytes: int,
+                     stream: int = 0) -> int:
+    return lib().dspark_head_loss(ctypes.byref(cfg), ctypes.byref(head), hidden, prev, labels,
+                                  weights, ctypes.byref(out), workspace, workspace_bytes,
+                                  stream)
+
+
+def dspark_block_norm(cfg: dspark_norm_config, x: int, y: int | None, gate: int | None,
+                      w_post: int | None, w_pre: int, x_out: int | None, h: int,
+                      stream: int = 0) -> int:
+    return lib().dspark_block_norm(ctypes.byref(cfg), x, y, gate, w_post, w_pre, x_out, h,
+                                   stream)
+
+
+def dspark_block_norm_workspace_size(cfg: dspark_norm_config) -> int:
+    return lib().dspark_block_norm_workspace_size(ctypes.byref(cfg))
+
+
+def dspark_block_norm_backward(cfg: dspark_norm_config, x: int, y: int | None,
+                               gate: int | None, w_post: int | None, w_pre: int, d_h: int,
+                               d_x_out: int | None, d_x: int, d_y: int | None,
+                               d_gate: int | None, d_w_post: int | None, d_w_pre: int,
+                               workspace: int, workspace_bytes: int, stream: int = 0) -> int:
+    return lib().dspark_block_norm_backward(ctypes.byref(cfg), x, y, gate, w_post, w_pre, d_h,
+                                            d_x_out, d_x, d_y, d_gate, d_w_post, d_w_pre,
+                                            workspace, workspace_bytes, stream)
+
+
+def dspark_clip_grads_workspace_size(count: int, grads) -> int:
+    """``grads``: a ctypes array of dspark_grad."""
+    return lib().dspark_clip_grads_workspace_size(count, grads)
+
+
+def dspark_clip_grads(count: int, grads, max_norm: float, norm: int, workspace: int,
+                      workspace_bytes: int, stream: int = 0) -> int:
+    return lib().dspark_clip_grads(count, grads, max_norm, norm, workspace, workspace_bytes,
+                                   stream)
 
 
 def dspark_status_string(status: int) -> str:

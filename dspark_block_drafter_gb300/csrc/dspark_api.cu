@@ -9,17 +9,18 @@
 #include "../../include/dspark.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "status.h"
 
 namespace dspark {
 
 static thread_local std::string g_last_error;
 
-static dspark_status fail(dspark_status s, const std::string& msg) {
+dspark_status fail(dspark_status s, const std::string& msg) {
   g_last_error = msg;
   return s;
 }
 
-static dspark_status cuda_fail(cudaError_t e, const char* where) {
+dspark_status cuda_fail(cudaError_t e, const char* where) {
   g_last_error = std::string(where) + ": " + cudaGetErrorString(e);
   return DSPARK_ERR_CUDA;
 }

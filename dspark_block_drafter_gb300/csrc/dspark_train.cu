@@ -1,0 +1,336 @@
+// The C ABI of the head's training operators: argument validation, workspace carve-up and
+// kernel dispatch.
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "../../include/dspark.h"
+#include "common.cuh"
+#include "kernels.h"
+#include "loss.h"
+#include "status.h"
+#include "train.h"
+
+namespace dspark {
+
+static constexpr size_t kAlign = 256;
+static constexpr int kMaxLossRows = 1 << 20;
+
+static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+static dspark_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws || !aligned(ws, kAlign))
+    return fail(DSPARK_ERR_WORKSPACE, "workspace must be non-NULL and 256-byte aligned");
+  if (have < need)
+    return fail(DSPARK_ERR_WORKSPACE,
+                "workspace too small: need " + std::to_string(need) + " bytes");
+  return DSPARK_OK;
+}
+
+// ------------------------------------------------------------------ head loss
+static dspark_status validate_loss(const dspark_loss_config* c, const dspark_head* h,
+                                   const dspark_loss_outputs* o) {
+  if (!c) return fail(DSPARK_ERR_INVALID_ARG, "config is NULL");
+  if (!h) return fail(DSPARK_ERR_INVALID_ARG, "head is NULL");
+  if (!o) return fail(DSPARK_ERR_INVALID_ARG, "outputs is NULL");
+  if (c->T < 1 || c->H < 1 || c->V < 1 || c->r < 0)
+    return fail(DSPARK_ERR_INVALID_ARG, "T, H and V must be >= 1, r >= 0");
+  if (c->dtype != DSPARK_F32 && c->dtype != DSPARK_BF16)
+    return fail(DSPARK_ERR_INVALID_ARG, "dtype must be DSPARK_F32 or DSPARK_BF16");
+  if (c->reduction != DSPARK_LOSS_SUM && c->reduction != DSPARK_LOSS_MEAN)
+    return fail(DSPARK_ERR_INVALID_ARG, "reduction must be DSPARK_LOSS_SUM or DSPARK_LOSS_MEAN");
+  if (c->vocab_pieces < 0) return fail(DSPARK_ERR_INVALID_ARG, "vocab_pieces must be >= 0");
+  if (!std::isfinite(c->loss_scale))
+    return fail(DSPARK_ERR_INVALID_ARG, "loss_scale must be finite");
+  if (!h->lm_head) return fail(DSPARK_ERR_INVALID_ARG, "lm_head is required");
+  if (c->r > 0 && (!h->markov_w1 || !h->markov_w2))
+    return fail(DSPARK_ERR_INVALID_ARG, "markov_w1 and markov_w2 are required when r > 0");
+  if (c->r == 0 && (o->d_markov_w1 || o->d_markov_w2))
+    return fail(DSPARK_ERR_INVALID_ARG, "r = 0: there are no Markov weights to differentiate");
+  if (h->V_head < 1 || h->V_head > c->V)
+    return fail(DSPARK_ERR_INVALID_ARG, "V_head must be in [1, V]");
+  if (!h->d2t && h->V_head != c->V)
+    return fail(DSPARK_ERR_INVALID_ARG, "without d2t, V_head must equal V");
+  if (c->r > 512) return fail(DSPARK_ERR_UNSUPPORTED, "Markov rank above 512");
+  if (c->T > kMaxLossRows) return fail(DSPARK_ERR_UNSUPPORTED, "more than 2^20 rows");
+  if (c->H > (1 << 20) || c->V > (1 << 28))
+    return fail(DSPARK_ERR_UNSUPPORTED, "sizes too large");
+  if (c->dtype == DSPARK_BF16) {
+    if (c->H % 8 != 0)
+      return fail(DSPARK_ERR_UNSUPPORTED, "bf16 path needs H % 8 == 0 (16-byte rows)");
+    if (h->V_head % 8 != 0)
+      return fail(DSPARK_ERR_UNSUPPORTED, "bf16 path needs V_head % 8 == 0 (16-byte rows)");
+    if (!aligned(h->lm_head, 16) || (c->r > 0 && !aligned(h->markov_w2, 16)))
+      return fail(DSPARK_ERR_INVALID_ARG, "bf16 weights must be 16-byte aligned");
+  }
+  return DSPARK_OK;
+}
+
+// Sizes and workspace regions (offsets from `ws`, which is NULL when only the size is
+// wanted); returns the bytes used.
+static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
+                        const dspark_loss_outputs* o, char* ws, LossPlan* p) {
+  *p = LossPlan{};
+  p->T = c->T; p->H = c->H; p->V = c->V; p->Vh = h->V_head; p->r = c->r;
+  p->dtype = c->dtype; p->reduction = c->reduction; p->loss_scale = c->loss_scale;
+  p->Hp = (int)align_up((size_t)c->H, 64);
+  p->rp = (int)align_up((size_t)c->r, 64);
+  p->Kx = p->Hp + p->rp;
+  p->Tp = (int)align_up((size_t)c->T, 256);
+  p->lm_head = h->lm_head; p->w1 = h->markov_w1; p->w2 = h->markov_w2;
+  p->bias = h->lm_bias; p->d2t = h->d2t;
+  p->loss = o->loss; p->total = o->total; p->n_rows = o->n_rows;
+  p->d_hidden = o->d_hidden; p->d_lm_head = o->d_lm_head;
+  p->d_w1 = o->d_markov_w1; p->d_w2 = o->d_markov_w2;
+  p->grads = o->d_hidden || o->d_lm_head || o->d_markov_w1 || o->d_markov_w2;
+
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char* at = ws + off;
+    off = align_up(off + bytes, kAlign);
+    return (void*)at;
+  };
+  const size_t Tp = (size_t)p->Tp, Vh = (size_t)p->Vh, es = c->dtype == DSPARK_F32 ? 4 : 2;
+  p->ctrl = (uint32_t*)take(256);
+  p->tok = (int32_t*)take(4 * Tp);
+  p->lab = (int32_t*)take(4 * Tp);
+  p->prevc = (int32_t*)take(4 * Tp);
+  p->pos = (int32_t*)take(4 * Tp);
+  p->wrow = (float*)take(4 * Tp);
+  p->zlab = (float*)take(4 * Tp);
+  p->lse = (float*)take(4 * Tp);
+  if (h->lm_bias) {
+    p->vlist = (int32_t*)take(4 * Vh);
+    p->vinv = (int32_t*)take(4 * Vh);
+    p->biasc = (float*)take(4 * Vh);
+    p->vchunk = (int*)take(4 * (size_t)emit_chunks(p->Vh));
+  }
+  p->x = take(es * Tp * p->Kx);
+  p->stat_cols = 64;
+  p->n_stat = (p->Vh + p->stat_cols - 1) / p->stat_cols;
+  p->stat = (float2*)take(sizeof(float2) * Tp * p->n_stat);
+  if (p->grads) {
+    const int most = (p->Vh + 255) / 256;
+    const size_t qs = 4;
+    int pieces = c->vocab_pieces;
+    if (pieces == 0) {
+      // keep the whole vocabulary's numerators while they take no more than 8 GiB (a
+      // second computation of the logits costs a third more products)
+      const size_t all = Tp * align_up(Vh, 256) * qs, limit = (size_t)8 << 30;
+      pieces = (int)std::min<size_t>((all + limit - 1) / limit, (size_t)most);
+    }
+    pieces = std::min(pieces, most);
+    p->piece_cols = (most + pieces - 1) / pieces * 256;
+    p->pieces = (p->Vh + p->piece_cols - 1) / p->piece_cols;
+    p->ldq = (size_t)p->piece_cols;
+    p->q = take(qs * Tp * p->ldq);
+    if (p->d_hidden || p->d_w1) {
+      p->splits = loss_simt_splits(p->T, p->Kx, p->piece_cols);
+      p->dxp = (float*)take(sizeof(float) * p->splits * Tp * p->Kx);
+    }
+  }
+  return off;
+}
+
+static cudaError_t run_loss(const LossPlan& p) {
+  cudaError_t e = launch_loss_plan(p);
+  if (e != cudaSuccess) return e;
+  const bool keep = p.grads && p.pieces == 1;
+  e = launch_loss_logits_simt(p, 0, p.Vh, true, keep);
+  if (e == cudaSuccess) e = launch_loss_rows(p);
+  if (e != cudaSuccess || !p.grads) return e;
+  const bool dx = p.d_hidden || p.d_w1, dw = p.d_lm_head || p.d_w2;
+  for (int c = 0; c < p.pieces; ++c) {
+    const int v0 = c * p.piece_cols, v1 = std::min(p.Vh, v0 + p.piece_cols);
+    if (!keep) e = launch_loss_logits_simt(p, v0, v1, false, true);
+    if (e == cudaSuccess) e = launch_loss_dz(p, v0, v1);
+    if (e == cudaSuccess && dx) e = launch_loss_dx_simt(p, v0, v1, c == 0);
+    if (e == cudaSuccess && dw) e = launch_loss_dw_simt(p, v0, v1);
+    if (e != cudaSuccess) return e;
+  }
+  return dx ? launch_loss_dx(p) : cudaSuccess;
+}
+
+// ------------------------------------------------------------------ block norm
+static dspark_status validate_norm(const dspark_norm_config* c) {
+  if (!c) return fail(DSPARK_ERR_INVALID_ARG, "config is NULL");
+  if (c->T < 1 || c->H < 1 || c->gate_span < 1)
+    return fail(DSPARK_ERR_INVALID_ARG, "T, H and gate_span must be >= 1");
+  if (c->dtype != DSPARK_F32 && c->dtype != DSPARK_BF16)
+    return fail(DSPARK_ERR_INVALID_ARG, "dtype must be DSPARK_F32 or DSPARK_BF16");
+  if (!(c->eps > 0.f) || !std::isfinite(c->eps) || !std::isfinite(c->residual_scale) ||
+      !std::isfinite(c->weight_offset))
+    return fail(DSPARK_ERR_INVALID_ARG,
+                "eps must be positive, residual_scale and weight_offset finite");
+  if (c->H > kNormMaxH) return fail(DSPARK_ERR_UNSUPPORTED, "H above 8192");
+  return DSPARK_OK;
+}
+
+static dspark_status check_norm_inputs(const void* x, const void* y, const void* gate,
+                                       const void* w_post, const void* w_pre) {
+  if (!x || !w_pre) return fail(DSPARK_ERR_INVALID_ARG, "x and w_pre are required");
+  if (!y && (gate || w_post))
+    return fail(DSPARK_ERR_INVALID_ARG, "gate and w_post act on y: they need it");
+  return DSPARK_OK;
+}
+
+static size_t plan_norm(const dspark_norm_config* c, char* ws, NormArgs* a) {
+  size_t off = 0;
+  auto take = [&](size_t floats) {
+    char* at = ws + off;
+    off = align_up(off + 4 * floats, kAlign);
+    return (float*)at;
+  };
+  const size_t units = (size_t)c->T;
+  a->w_part = take(2 * std::min(units, (size_t)norm_max_ctas(c->H)) * c->H);
+  const int parts = norm_span_parts(c->T, c->gate_span);
+  a->gate_part = nullptr;
+  if (parts > 1) {
+    const size_t rows = ((size_t)c->T + c->gate_span - 1) / c->gate_span;
+    a->gate_part = take(rows * parts * c->H);
+  }
+  return off;
+}
+
+static void fill_norm(const dspark_norm_config* c, NormArgs* a) {
+  a->T = c->T; a->H = c->H; a->dtype = c->dtype; a->span = c->gate_span;
+  a->eps = c->eps; a->scale = c->residual_scale; a->offset = c->weight_offset;
+}
+
+// ------------------------------------------------------------------ clipping
+static dspark_status validate_clip(int32_t count, const dspark_grad* g) {
+  if (count < 1 || !g) return fail(DSPARK_ERR_INVALID_ARG, "at least one gradient is needed");
+  if (count > (1 << 20)) return fail(DSPARK_ERR_UNSUPPORTED, "more than 2^20 gradients");
+  for (int i = 0; i < count; ++i) {
+    if (g[i].n < 0 || (g[i].n > 0 && (!g[i].in || !g[i].out)))
+      return fail(DSPARK_ERR_INVALID_ARG,
+                  "gradient " + std::to_string(i) + ": n must be >= 0, in and out non-NULL");
+    if (g[i].dtype != DSPARK_F32 && g[i].dtype != DSPARK_BF16)
+      return fail(DSPARK_ERR_INVALID_ARG, "gradient " + std::to_string(i) +
+                                              ": dtype must be DSPARK_F32 or DSPARK_BF16");
+    const size_t es = g[i].dtype == DSPARK_F32 ? 4 : 2;
+    if (!aligned(g[i].in, es) || !aligned(g[i].out, es))
+      return fail(DSPARK_ERR_INVALID_ARG,
+                  "gradient " + std::to_string(i) + ": in and out must be element aligned");
+    if (g[i].n > (1ll << 38)) return fail(DSPARK_ERR_UNSUPPORTED, "a gradient above 2^38 elements");
+  }
+  return DSPARK_OK;
+}
+
+}  // namespace dspark
+
+using namespace dspark;
+
+static_assert(sizeof(dspark_loss_config) == 32, "dspark_loss_config layout");
+static_assert(sizeof(dspark_loss_outputs) == 56, "dspark_loss_outputs layout");
+static_assert(sizeof(dspark_norm_config) == 28, "dspark_norm_config layout");
+static_assert(sizeof(dspark_grad) == 32, "dspark_grad layout");
+
+extern "C" {
+
+size_t dspark_head_loss_workspace_size(const dspark_loss_config* cfg, const dspark_head* head,
+                                       const dspark_loss_outputs* out) {
+  if (validate_loss(cfg, head, out) != DSPARK_OK) return 0;
+  LossPlan p;
+  return plan_loss(cfg, head, out, nullptr, &p);
+}
+
+dspark_status dspark_head_loss(const dspark_loss_config* cfg, const dspark_head* head,
+                               const void* hidden, const int32_t* prev, const int32_t* labels,
+                               const float* weights, const dspark_loss_outputs* out,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  dspark_status st = validate_loss(cfg, head, out);
+  if (st != DSPARK_OK) return st;
+  if (!hidden || !labels || (cfg->r > 0 && !prev))
+    return fail(DSPARK_ERR_INVALID_ARG, "hidden, labels and (for r > 0) prev are required");
+  if (!out->loss || !out->total)
+    return fail(DSPARK_ERR_INVALID_ARG, "outputs loss and total are required");
+  LossPlan p;
+  const size_t need = plan_loss(cfg, head, out, (char*)workspace, &p);
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st != DSPARK_OK) return st;
+  p.hidden = hidden;
+  p.prev = prev;
+  p.labels = labels;
+  p.weights = weights;
+  p.stream = (cudaStream_t)stream;
+  const cudaError_t e = run_loss(p);
+  if (e != cudaSuccess) return cuda_fail(e, "head loss");
+  return DSPARK_OK;
+}
+
+dspark_status dspark_block_norm(const dspark_norm_config* cfg, const void* x, const void* y,
+                                const void* gate, const void* w_post, const void* w_pre,
+                                void* x_out, void* h, void* stream) {
+  dspark_status st = validate_norm(cfg);
+  if (st == DSPARK_OK) st = check_norm_inputs(x, y, gate, w_post, w_pre);
+  if (st != DSPARK_OK) return st;
+  if (!h) return fail(DSPARK_ERR_INVALID_ARG, "h is required");
+  NormArgs a{};
+  fill_norm(cfg, &a);
+  a.x = x; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre;
+  a.x_out = x_out;
+  a.h = h;
+  a.stream = (cudaStream_t)stream;
+  const cudaError_t e = launch_block_norm(a);
+  if (e != cudaSuccess) return cuda_fail(e, "block norm kernel");
+  return DSPARK_OK;
+}
+
+size_t dspark_block_norm_workspace_size(const dspark_norm_config* cfg) {
+  if (validate_norm(cfg) != DSPARK_OK) return 0;
+  NormArgs a{};
+  return plan_norm(cfg, nullptr, &a);
+}
+
+dspark_status dspark_block_norm_backward(const dspark_norm_config* cfg, const void* x,
+                                         const void* y, const void* gate, const void* w_post,
+                                         const void* w_pre, const void* d_h,
+                                         const void* d_x_out, void* d_x, void* d_y,
+                                         void* d_gate, void* d_w_post, void* d_w_pre,
+                                         void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+  dspark_status st = validate_norm(cfg);
+  if (st == DSPARK_OK) st = check_norm_inputs(x, y, gate, w_post, w_pre);
+  if (st != DSPARK_OK) return st;
+  if (!d_h || !d_x || !d_w_pre)
+    return fail(DSPARK_ERR_INVALID_ARG, "d_h, d_x and d_w_pre are required");
+  if (!y != !d_y || !gate != !d_gate || !w_post != !d_w_post)
+    return fail(DSPARK_ERR_INVALID_ARG,
+                "d_y, d_gate and d_w_post go with y, gate and w_post: both or neither");
+  NormArgs a{};
+  fill_norm(cfg, &a);
+  const size_t need = plan_norm(cfg, (char*)workspace, &a);
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st != DSPARK_OK) return st;
+  a.x = x; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre;
+  a.d_h = d_h; a.d_x_out = d_x_out; a.d_x = d_x; a.d_y = d_y; a.d_gate = d_gate;
+  a.d_w_post = d_w_post; a.d_w_pre = d_w_pre;
+  a.stream = (cudaStream_t)stream;
+  const cudaError_t e = launch_block_norm_backward(a);
+  if (e != cudaSuccess) return cuda_fail(e, "block norm gradient kernels");
+  return DSPARK_OK;
+}
+
+size_t dspark_clip_grads_workspace_size(int32_t count, const dspark_grad* grads) {
+  if (validate_clip(count, grads) != DSPARK_OK) return 0;
+  return align_up(sizeof(double) * clip_partials(count), kAlign);
+}
+
+dspark_status dspark_clip_grads(int32_t count, const dspark_grad* grads, float max_norm,
+                                float* norm, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  dspark_status st = validate_clip(count, grads);
+  if (st != DSPARK_OK) return st;
+  if (!(max_norm >= 0.f)) return fail(DSPARK_ERR_INVALID_ARG, "max_norm must be >= 0");
+  if (!norm) return fail(DSPARK_ERR_INVALID_ARG, "norm is required");
+  st = check_workspace(workspace, workspace_bytes,
+                       align_up(sizeof(double) * clip_partials(count), kAlign));
+  if (st != DSPARK_OK) return st;
+  const cudaError_t e = launch_clip_grads(count, grads, max_norm, norm, (double*)workspace,
+                                          (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "gradient clipping kernels");
+  return DSPARK_OK;
+}
+
+}  // extern "C"

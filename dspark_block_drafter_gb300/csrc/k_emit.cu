@@ -165,6 +165,16 @@ cudaError_t launch_emit_count(const float* bias, int V, int* count, cudaStream_t
   return cudaGetLastError();
 }
 
+int emit_chunks(int V) { return (V + kChunk - 1) / kChunk; }
+
+cudaError_t launch_emit_rows(const float* bias, int V, int* chunk_count, int32_t* list,
+                             int* chunks, cudaStream_t stream) {
+  *chunks = emit_chunks(V);
+  emit_chunk_counts<<<*chunks, 256, 0, stream>>>(bias, V, chunk_count);
+  emit_list<<<*chunks, kScanThreads, 0, stream>>>(bias, V, chunk_count, list);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_prepare_compact(const void* lm_head, const float* bias, const void* w1,
                                    const void* w2, int V, int H, int r, int n_emit, int n_pad,
                                    void* prepared, cudaStream_t stream) {
@@ -172,9 +182,9 @@ cudaError_t launch_prepare_compact(const void* lm_head, const float* bias, const
   char* base = (char*)prepared;
   int32_t* list = (int32_t*)(base + l.list);
   int* cc = (int*)(base + l.chunk_count);
-  const int chunks = (V + kChunk - 1) / kChunk;
-  emit_chunk_counts<<<chunks, 256, 0, stream>>>(bias, V, cc);
-  emit_list<<<chunks, kScanThreads, 0, stream>>>(bias, V, cc, list);
+  int chunks = 0;
+  cudaError_t e = launch_emit_rows(bias, V, cc, list, &chunks, stream);
+  if (e != cudaSuccess) return e;
   if (n_pad > n_emit) emit_pad<<<1, 32, 0, stream>>>(list, n_emit, n_pad);
   const int cpr = H / 8;                                  // 16-byte chunks of a bf16 row
   const size_t rows_total = (size_t)n_pad * cpr;
@@ -187,7 +197,7 @@ cudaError_t launch_prepare_compact(const void* lm_head, const float* bias, const
                                (__nv_bfloat16*)(base + l.w2));
   emit_gather_bias<<<(n_pad + 255) / 256, 256, 0, stream>>>(bias, list, n_emit, n_pad,
                                                             (float*)(base + l.bias));
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the pruned chain's preparation of the compact head
   e = launch_prepare_head(w1, base + l.w2, V, r, n_pad, base + l.prepared, stream);

@@ -1,0 +1,244 @@
+// The training loss of the head: its three products on the CUDA cores, in fp32.
+//
+//   logits  z[i][j]  = X[i] . [lm_head[j] | markov_w2[:, j]] + bias[j]
+//   dX      dx[i][c] = sum_j q[i][j] [lm_head | markov_w2^T][j][c]
+//   dW      [d_lm_head | d_markov_w2^T][j][c] = scale * sum_i q[i][j] X[i][c]
+//
+// i: compact rows, j: compact head rows, c: columns of X.  One 64 x 64 tile per CTA, 16
+// deep, four by four results per thread; operands pass through shared memory with the
+// index that is contiguous in memory spread over a warp's lanes.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "loss.h"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kTile = 64, kDepth = 16;
+
+// s[k][m] = at(m, k) for a 64 x 16 tile; `along_k`: k is the contiguous index in memory.
+template <typename F>
+__device__ __forceinline__ void load_tile(float (*s)[kTile + 4], bool along_k, F at) {
+#pragma unroll
+  for (int e = threadIdx.x; e < kTile * kDepth; e += 256) {
+    const int k = along_k ? e % kDepth : e / kTile;
+    const int m = along_k ? e / kDepth : e % kTile;
+    s[k][m] = at(m, k);
+  }
+}
+
+// acc[a][b] += sum_k A(4 ty + a, k) B(4 tx + b, k) over `depth`
+template <typename FA, typename FB>
+__device__ __forceinline__ void tile_product(float (&acc)[4][4], int depth, bool a_along_k,
+                                             FA a_at, FB b_tile) {
+  __shared__ __align__(16) float sa[kDepth][kTile + 4], sb[kDepth][kTile + 4];
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  for (int k0 = 0; k0 < depth; k0 += kDepth) {
+    __syncthreads();
+    load_tile(sa, a_along_k, [&](int m, int k) { return a_at(m, k0 + k); });
+    b_tile(sb, k0);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) {
+      float a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = sa[k][4 * ty + j];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = sb[k][4 * tx + j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+  }
+}
+
+// Columns [v0, v1) of the logits: their statistics per 64-column tile and the labels'
+// logits (`stats`), and the logits themselves (`store`).
+template <typename E>
+__global__ void __launch_bounds__(256)
+loss_logits(const LossPlan p, int v0, int v1, bool stats, bool store) {
+  const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
+  const int m0 = blockIdx.y * kTile, j0 = v0 + blockIdx.x * kTile;
+  if (m0 >= n_tok || j0 >= n_voc) return;
+  const E* x = (const E*)p.x;
+  const E* w = (const E*)p.lm_head;
+  const E* w2 = (const E*)p.w2;
+  __shared__ int s_row[kTile];
+  if (threadIdx.x < kTile)
+    s_row[threadIdx.x] = j0 + (int)threadIdx.x < n_voc ? loss_head_row(p, j0 + threadIdx.x) : -1;
+  __syncthreads();
+  float acc[4][4] = {};
+  tile_product(
+      acc, p.Kx, true,
+      [&](int m, int k) { return to_f32(x[(size_t)(m0 + m) * p.Kx + k]); },
+      [&](float (*sb)[kTile + 4], int k0) {
+        if (k0 < p.Hp)
+          load_tile(sb, true, [&](int n, int k) {
+            const int row = s_row[n], h = k0 + k;
+            return row >= 0 && h < p.H ? to_f32(w[(size_t)row * p.H + h]) : 0.f;
+          });
+        else
+          load_tile(sb, false, [&](int n, int k) {
+            const int row = s_row[n], c = k0 - p.Hp + k;
+            return row >= 0 && c < p.r ? to_f32(w2[(size_t)c * p.Vh + row]) : 0.f;
+          });
+      });
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int i = m0 + 4 * ty + a;
+    float m = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int j = j0 + 4 * tx + b;
+      float z = acc[a][b];
+      if (j < n_voc && p.vlist) z += p.biasc[j];
+      acc[a][b] = z;
+      if (j < n_voc) {
+        // (a NaN logit stays NaN in the maximum)
+        m = z != z || m != m ? m + z : fmaxf(m, z);
+        if (store && i < n_tok) ((float*)p.q)[(size_t)i * p.ldq + (j - v0)] = z;
+        if (stats && i < n_tok && j == p.lab[i]) p.zlab[i] = z;
+      }
+    }
+    if (!stats) continue;
+    // the row's 16 threads are 16 lanes of one warp
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      const float y = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+      m = y != y || m != m ? m + y : fmaxf(m, y);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (j0 + 4 * tx + b < n_voc && m > -INFINITY) s += expf(acc[a][b] - m);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (m != m) s = m;                        // (NaN for the whole row)
+    if (tx == 0 && i < n_tok) p.stat[(size_t)i * p.n_stat + j0 / kTile] = make_float2(m, s);
+  }
+}
+
+// dX of vocabulary columns [v0, v1): split blockIdx.z of their range.
+template <typename E>
+__global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1, bool first) {
+  const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
+  const int m0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
+  if (m0 >= n_tok) return;
+  const int share = ((v1 - v0 + (int)gridDim.z - 1) / (int)gridDim.z + kDepth - 1) / kDepth * kDepth;
+  const int ja = v0 + (int)blockIdx.z * share, jb = min(n_voc, ja + share);
+  const float* q = (const float*)p.q;
+  const E* w = (const E*)p.lm_head;
+  const E* w2 = (const E*)p.w2;
+  float acc[4][4] = {};
+  if (jb > ja)
+    tile_product(
+        acc, jb - ja, true,
+        [&](int m, int k) {
+          const int j = ja + k;
+          return m0 + m < n_tok && j < jb ? q[(size_t)(m0 + m) * p.ldq + (j - v0)] : 0.f;
+        },
+        [&](float (*sb)[kTile + 4], int k0) {
+          const bool head = c0 < p.Hp;
+          load_tile(sb, !head, [&](int n, int k) {
+            const int j = ja + k0 + k, c = c0 + n;
+            if (j >= jb) return 0.f;
+            const int row = loss_head_row(p, j);
+            if (head) return c < p.H ? to_f32(w[(size_t)row * p.H + c]) : 0.f;
+            return c - p.Hp < p.r ? to_f32(w2[(size_t)(c - p.Hp) * p.Vh + row]) : 0.f;
+          });
+        });
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  float* dx = p.dxp + (size_t)blockIdx.z * p.Tp * p.Kx;
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int i = m0 + 4 * ty + a, c = c0 + 4 * tx + b;
+      if (i >= n_tok) continue;
+      float* d = dx + (size_t)i * p.Kx + c;
+      *d = first ? acc[a][b] : *d + acc[a][b];
+    }
+}
+
+// dW of vocabulary columns [v0, v1).
+template <typename E>
+__global__ void __launch_bounds__(256) loss_dw(const LossPlan p, int v0, int v1) {
+  const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
+  const int j0 = v0 + blockIdx.y * kTile, c0 = blockIdx.x * kTile;
+  const bool head = c0 < p.Hp;
+  if (j0 >= n_voc || (head ? !p.d_lm_head : !p.d_w2)) return;
+  const float* q = (const float*)p.q;
+  const E* x = (const E*)p.x;
+  float acc[4][4] = {};
+  tile_product(
+      acc, n_tok, false,
+      [&](int m, int k) {
+        const int j = j0 + m;
+        return j < n_voc && k < n_tok ? q[(size_t)k * p.ldq + (j - v0)] : 0.f;
+      },
+      [&](float (*sb)[kTile + 4], int k0) {
+        load_tile(sb, false, [&](int n, int k) {
+          return k0 + k < n_tok ? to_f32(x[(size_t)(k0 + k) * p.Kx + c0 + n]) : 0.f;
+        });
+      });
+  const float scale = __uint_as_float(p.ctrl[kLossScale]);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int j = j0 + 4 * ty + a, c = c0 + 4 * tx + b;
+      if (j >= n_voc) continue;
+      const int row = loss_head_row(p, j);
+      const float g = acc[a][b] * scale;
+      if (head) {
+        if (c < p.H) ((E*)p.d_lm_head)[(size_t)row * p.H + c] = (E)g;
+      } else if (c - p.Hp < p.r) {
+        ((E*)p.d_w2)[(size_t)(c - p.Hp) * p.Vh + row] = (E)g;
+      }
+    }
+}
+
+}  // namespace
+
+// Splits of the vocabulary for dX: enough CTAs to fill the GPU when rows are few.
+int loss_simt_splits(int T, int Kx, int cols) {
+  const int tiles = ((T + kTile - 1) / kTile) * (Kx / kTile);
+  return std::max(1, std::min({(304 + tiles - 1) / tiles, (cols + 255) / 256, 64}));
+}
+
+cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stats, bool store) {
+  const dim3 grid((v1 - v0 + kTile - 1) / kTile, (p.T + kTile - 1) / kTile);
+  if (p.dtype == 0)
+    loss_logits<float><<<grid, 256, 0, p.stream>>>(p, v0, v1, stats, store);
+  else
+    loss_logits<__nv_bfloat16><<<grid, 256, 0, p.stream>>>(p, v0, v1, stats, store);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first) {
+  const dim3 grid(p.Kx / kTile, (p.T + kTile - 1) / kTile, p.splits);
+  if (p.dtype == 0)
+    loss_dx<float><<<grid, 256, 0, p.stream>>>(p, v0, v1, first);
+  else
+    loss_dx<__nv_bfloat16><<<grid, 256, 0, p.stream>>>(p, v0, v1, first);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1) {
+  const dim3 grid(p.Kx / kTile, (v1 - v0 + kTile - 1) / kTile);
+  if (p.dtype == 0)
+    loss_dw<float><<<grid, 256, 0, p.stream>>>(p, v0, v1);
+  else
+    loss_dw<__nv_bfloat16><<<grid, 256, 0, p.stream>>>(p, v0, v1);
+  return cudaGetLastError();
+}
+
+}  // namespace dspark

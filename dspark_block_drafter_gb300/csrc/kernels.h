@@ -44,6 +44,11 @@ struct CompactLayout {
 };
 CompactLayout plan_compact(int V, int H, int r, int n_pad);
 cudaError_t launch_emit_count(const float* bias, int V, int* count, cudaStream_t stream);
+// The emittable rows in increasing order into list[], their counts per chunk of the bias
+// into chunk_count[emit_chunks(V)].
+int emit_chunks(int V);
+cudaError_t launch_emit_rows(const float* bias, int V, int* chunk_count, int32_t* list,
+                             int* chunks, cudaStream_t stream);
 cudaError_t launch_prepare_compact(const void* lm_head, const float* bias, const void* w1,
                                    const void* w2, int V, int H, int r, int n_emit, int n_pad,
                                    void* prepared, cudaStream_t stream);

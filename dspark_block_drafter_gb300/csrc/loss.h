@@ -1,0 +1,78 @@
+// The training loss of the head: the call's plan (sizes, inputs, outputs, workspace
+// regions) and the kernels' host launchers.
+//
+// A call first compacts its rows (those with a label the head can emit) and, for a head in
+// the bias form, its vocabulary (the rows that are not masked).  Everything after works on
+// the compact rows i < n_tok and compact head rows j < n_voc; both counts stay on the
+// device.  The operand rows of the logits are X[i] = [hidden | markov_w1[prev]], each part
+// padded with zeros to a multiple of 64, so that the Markov term is part of the one
+// product z = X . [lm_head | markov_w2^T]^T and its gradients are columns of the others'.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace dspark {
+
+// Words of the control block at the head of the workspace (word 0: the error word).
+enum : int {
+  kLossTok = 1,      // compact rows
+  kLossVoc = 2,      // compact head rows
+  kLossScale = 3,    // float: loss_scale / D, the factor of every gradient
+  kLossDone = 4,     // row CTAs whose loss is written
+};
+
+struct LossPlan {
+  int T, H, V, Vh, r, dtype, reduction;
+  float loss_scale;
+  int Hp, rp, Kx, Tp;          // padded sizes: multiples of 64, Kx = Hp + rp, Tp of 256
+  // inputs
+  const void *hidden, *lm_head, *w1, *w2;
+  const float *bias, *weights;
+  const int32_t *d2t, *prev, *labels;
+  // outputs (NULL where not asked for)
+  float *loss, *total;
+  int32_t* n_rows;
+  void *d_hidden, *d_lm_head, *d_w1, *d_w2;
+  // workspace
+  uint32_t* ctrl;
+  int32_t *tok, *lab, *prevc, *pos;   // [Tp] compact rows: row, label's compact head row,
+                                      // prev; [T] row -> compact row or -1
+  float* wrow;                        // [Tp] w_t of the compact rows
+  int32_t *vlist, *vinv;              // bias form: compact head row -> head row [Vh], and
+                                      // the inverse or -1
+  int* vchunk;                        // counts per chunk of the bias
+  float* biasc;                       // [Vh] bias of the compact head rows
+  void* x;                            // [Tp][Kx]
+  float2* stat;                       // [Tp][n_stat] per vocabulary tile: the maximum of
+                                      // z, and the sum of exp(z - maximum)
+  int n_stat, stat_cols;
+  float *zlab, *lse;                  // [Tp]
+  void* q;                            // [Tp][ldq]
+  size_t ldq;
+  int pieces, piece_cols;             // pieces of the vocabulary, columns of each
+  float* dxp;                         // [splits][Tp][Kx] partial gradients of X
+  int splits;
+  bool grads;                         // any gradient asked for
+  cudaStream_t stream;
+};
+
+// compact -> head row, for kernels that read the head's own arrays
+__device__ __forceinline__ int loss_head_row(const LossPlan& p, int j) {
+  return p.vlist ? p.vlist[j] : j;
+}
+
+// k_loss_rows.cu: everything but the products
+cudaError_t launch_loss_plan(const LossPlan& p);         // compaction, X, zeroed outputs
+cudaError_t launch_loss_rows(const LossPlan& p);         // lse, losses, total
+cudaError_t launch_loss_dz(const LossPlan& p, int v0, int v1);   // q from stored logits
+cudaError_t launch_loss_dx(const LossPlan& p);           // d_hidden and d_w1 from dxp
+
+// k_loss_simt.cu: the products on the CUDA cores
+int loss_simt_splits(int T, int Kx, int cols);
+cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stats, bool store);
+cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first);
+cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1);
+
+}  // namespace dspark

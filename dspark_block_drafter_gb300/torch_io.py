@@ -47,8 +47,8 @@ def make_config(B, L_in, H, V, r, top_k, sample_from_anchor, conf_min, dtype,
 class Head:
     """Device copies of a drafter head and the matching dspark_head struct."""
     lm_head: torch.Tensor
-    markov_w1: torch.Tensor
-    markov_w2: torch.Tensor
+    markov_w1: Optional[torch.Tensor]      # None: no Markov term (dspark_head_loss, r = 0)
+    markov_w2: Optional[torch.Tensor]
     lm_bias: Optional[torch.Tensor] = None
     d2t: Optional[torch.Tensor] = None
     w_conf: Optional[torch.Tensor] = None
@@ -170,3 +170,189 @@ def device_status(workspace: torch.Tensor, stream=None) -> int:
 
 def pass_stats(workspace: torch.Tensor, stream=None) -> dict:
     return _abi.dspark_pass_stats(workspace.data_ptr(), _stream(stream))
+
+
+# ------------------------------------------------------------------ training the head
+_TORCH_DT = {_abi.DSPARK_F32: torch.float32, _abi.DSPARK_BF16: torch.bfloat16}
+_REDUCTION = {"sum": _abi.DSPARK_LOSS_SUM, "mean": _abi.DSPARK_LOSS_MEAN}
+
+
+def _checked(name: str, t: Optional[torch.Tensor], shape, dtype) -> Optional[int]:
+    """The address of a dense tensor of the given shape and type (None stays None)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def make_loss_config(T, H, V, r, dtype, reduction="mean", loss_scale=1.0,
+                     vocab_pieces=0) -> _abi.dspark_loss_config:
+    return _abi.dspark_loss_config(T=T, H=H, V=V, r=r,
+                                   dtype=_DT[dtype] if isinstance(dtype, str) else int(dtype),
+                                   reduction=_REDUCTION[reduction],
+                                   vocab_pieces=int(vocab_pieces),
+                                   loss_scale=float(loss_scale))
+
+
+@dataclasses.dataclass
+class LossOutputs:
+    loss: torch.Tensor
+    total: torch.Tensor
+    n_rows: Optional[torch.Tensor] = None
+    d_hidden: Optional[torch.Tensor] = None
+    d_lm_head: Optional[torch.Tensor] = None
+    d_markov_w1: Optional[torch.Tensor] = None
+    d_markov_w2: Optional[torch.Tensor] = None
+
+    @classmethod
+    def allocate(cls, cfg, head: Head, d_hidden=True, d_lm_head=True, d_markov=True,
+                 device="cuda"):
+        e = dict(dtype=_TORCH_DT[cfg.dtype], device=device)
+        f32 = dict(dtype=torch.float32, device=device)
+        markov = d_markov and cfg.r > 0
+        return cls(torch.empty(cfg.T, **f32), torch.empty(1, **f32),
+                   torch.empty(1, dtype=torch.int32, device=device),
+                   torch.empty(cfg.T, cfg.H, **e) if d_hidden else None,
+                   torch.empty(head.V_head, cfg.H, **e) if d_lm_head else None,
+                   torch.empty(cfg.V, cfg.r, **e) if markov else None,
+                   torch.empty(cfg.r, head.V_head, **e) if markov else None)
+
+    def struct(self) -> _abi.dspark_loss_outputs:
+        return _abi.dspark_loss_outputs(
+            loss=_ptr(self.loss), total=_ptr(self.total), n_rows=_ptr(self.n_rows),
+            d_hidden=_ptr(self.d_hidden), d_lm_head=_ptr(self.d_lm_head),
+            d_markov_w1=_ptr(self.d_markov_w1), d_markov_w2=_ptr(self.d_markov_w2))
+
+
+def loss_workspace_for(cfg, head: Head, out: LossOutputs, device="cuda") -> torch.Tensor:
+    n = _abi.dspark_head_loss_workspace_size(cfg, head.struct(), out.struct())
+    if n == 0:
+        _abi.check(_abi.DSPARK_ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def head_loss(cfg, head: Head, hidden, prev, labels, out: LossOutputs, workspace,
+              weights=None, stream=None) -> None:
+    """dspark_head_loss on torch tensors; raises DSparkError on a non-OK status."""
+    e, f32, i32 = _TORCH_DT.get(cfg.dtype), torch.float32, torch.int32
+    V, r, vh = cfg.V, cfg.r, head.V_head
+    for name, t, shape, dt in (
+            ("lm_head", head.lm_head, (vh, cfg.H), e), ("lm_bias", head.lm_bias, (vh,), f32),
+            ("d2t", head.d2t, (vh,), i32), ("markov_w1", head.markov_w1, (V, r), e),
+            ("markov_w2", head.markov_w2, (r, vh), e), ("loss", out.loss, (cfg.T,), f32),
+            ("total", out.total, (1,), f32), ("n_rows", out.n_rows, (1,), i32),
+            ("d_hidden", out.d_hidden, (cfg.T, cfg.H), e),
+            ("d_lm_head", out.d_lm_head, (vh, cfg.H), e),
+            ("d_markov_w1", out.d_markov_w1, (V, r), e),
+            ("d_markov_w2", out.d_markov_w2, (r, vh), e)):
+        _checked(name, t, shape, dt)
+    _abi.check(_abi.dspark_head_loss(
+        cfg, head.struct(), _checked("hidden", hidden, (cfg.T, cfg.H), e),
+        _checked("prev", prev, (cfg.T,), i32) if r > 0 else None,
+        _checked("labels", labels, (cfg.T,), i32),
+        _checked("weights", weights, (cfg.T,), f32), out.struct(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def make_norm_config(T, H, dtype, eps=1e-6, residual_scale=1.0, weight_offset=0.0,
+                     gate_span=1) -> _abi.dspark_norm_config:
+    return _abi.dspark_norm_config(T=T, H=H,
+                                   dtype=_DT[dtype] if isinstance(dtype, str) else int(dtype),
+                                   gate_span=int(gate_span), eps=float(eps),
+                                   residual_scale=float(residual_scale),
+                                   weight_offset=float(weight_offset))
+
+
+@dataclasses.dataclass
+class NormGrads:
+    d_x: torch.Tensor
+    d_y: Optional[torch.Tensor]
+    d_gate: Optional[torch.Tensor]
+    d_w_post: Optional[torch.Tensor]
+    d_w_pre: torch.Tensor
+
+    @classmethod
+    def allocate(cls, cfg, gate=True, w_post=True, y=True, device="cuda"):
+        e = dict(dtype=_TORCH_DT[cfg.dtype], device=device)
+        rows = (cfg.T + cfg.gate_span - 1) // cfg.gate_span
+        return cls(torch.empty(cfg.T, cfg.H, **e),
+                   torch.empty(cfg.T, cfg.H, **e) if y else None,
+                   torch.empty(rows, cfg.H, **e) if gate else None,
+                   torch.empty(cfg.H, **e) if w_post else None, torch.empty(cfg.H, **e))
+
+
+def norm_workspace_for(cfg, device="cuda") -> torch.Tensor:
+    n = _abi.dspark_block_norm_workspace_size(cfg)
+    if n == 0:
+        _abi.check(_abi.DSPARK_ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _norm_shapes(cfg):
+    rows = (cfg.T + cfg.gate_span - 1) // cfg.gate_span if cfg.gate_span > 0 else 0
+    return (cfg.T, cfg.H), (rows, cfg.H), (cfg.H,), _TORCH_DT.get(cfg.dtype)
+
+
+def block_norm(cfg, x, y, w_pre, h, x_out=None, gate=None, w_post=None, stream=None) -> None:
+    """dspark_block_norm on torch tensors; raises DSparkError on a non-OK status."""
+    row, gat, vec, e = _norm_shapes(cfg)
+    _abi.check(_abi.dspark_block_norm(
+        cfg, _checked("x", x, row, e), _checked("y", y, row, e),
+        _checked("gate", gate, gat, e), _checked("w_post", w_post, vec, e),
+        _checked("w_pre", w_pre, vec, e), _checked("x_out", x_out, row, e),
+        _checked("h", h, row, e), _stream(stream)))
+
+
+def block_norm_backward(cfg, x, y, w_pre, d_h, out: NormGrads, workspace, d_x_out=None,
+                        gate=None, w_post=None, stream=None) -> None:
+    """dspark_block_norm_backward on torch tensors; raises DSparkError on a non-OK status."""
+    row, gat, vec, e = _norm_shapes(cfg)
+    _abi.check(_abi.dspark_block_norm_backward(
+        cfg, _checked("x", x, row, e), _checked("y", y, row, e),
+        _checked("gate", gate, gat, e), _checked("w_post", w_post, vec, e),
+        _checked("w_pre", w_pre, vec, e), _checked("d_h", d_h, row, e),
+        _checked("d_x_out", d_x_out, row, e), _checked("d_x", out.d_x, row, e),
+        _checked("d_y", out.d_y, row, e), _checked("d_gate", out.d_gate, gat, e),
+        _checked("d_w_post", out.d_w_post, vec, e), _checked("d_w_pre", out.d_w_pre, vec, e),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+class GradList:
+    """The gradients of one clip_grads call and where their clipped values go (``outs``;
+    None: in place).  Holds the tensors, so that the addresses stay valid."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError("outs must have one tensor for each gradient")
+        dt = {v: k for k, v in _TORCH_DT.items()}
+        self.array = (_abi.dspark_grad * len(self.grads))()
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.dtype not in dt:
+                raise ValueError(f"gradient {i}: float32 or bfloat16, not {g.dtype}")
+            _checked(f"gradient {i}", g, g.shape, g.dtype)
+            _checked(f"outs[{i}]", o, g.shape, g.dtype)
+            self.array[i] = _abi.dspark_grad(in_=g.data_ptr(), out=o.data_ptr(), n=g.numel(),
+                                             dtype=dt[g.dtype])
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def clip_workspace_for(grads: GradList, device="cuda") -> torch.Tensor:
+    n = _abi.dspark_clip_grads_workspace_size(len(grads), grads.array)
+    if n == 0:
+        _abi.check(_abi.DSPARK_ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def clip_grads(grads: GradList, max_norm, norm, workspace, stream=None) -> None:
+    """dspark_clip_grads on torch tensors; raises DSparkError on a non-OK status."""
+    _abi.check(_abi.dspark_clip_grads(len(grads), grads.array, float(max_norm),
+                                      _checked("norm", norm, (1,), torch.float32),
+                                      workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(),
+                                      _stream(stream)))

@@ -399,6 +399,171 @@ dspark_status dspark_noalloc_device_status(void* stream);
 dspark_status dspark_wait_selftest(void* workspace, size_t workspace_bytes,
                                    int64_t budget_cycles, int32_t pre_abort, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Training the head.  dspark_block_norm makes the head's inputs from a drafter block's
+ * output, dspark_head_loss scores teacher-forced slots and gives the gradients of
+ * everything their logits are made of, dspark_block_norm_backward carries them through
+ * the norm, and dspark_clip_grads bounds the step.  (The pages describe the head these
+ * calls train, not its training: the operators are this library's own.)
+ * ------------------------------------------------------------------------------- */
+
+typedef enum dspark_reduction {
+  DSPARK_LOSS_SUM = 0,   /* total = loss_scale * sum_t w_t loss_t */
+  DSPARK_LOSS_MEAN = 1   /* that over the sum of w_t of the rows that carry a loss */
+} dspark_reduction;
+
+/* Sizes and knobs of dspark_head_loss. */
+typedef struct dspark_loss_config {
+  int32_t T;             /* rows (slots of all blocks), >= 1 */
+  int32_t H;             /* hidden size, >= 1 (multiple of 8 for bf16) */
+  int32_t V;             /* vocabulary: token ids are in [0, V) */
+  int32_t r;             /* Markov rank, 1 .. 512; 0: a head without the Markov term */
+  int32_t dtype;         /* dspark_dtype of hidden, the head's weights and the gradients */
+  int32_t reduction;     /* dspark_reduction */
+  int32_t vocab_pieces;  /* the gradients are computed over the vocabulary in this many
+                            pieces, >= 1; 0: chosen by size.  One piece keeps the
+                            softmax numerators of the whole vocabulary in the workspace
+                            (2 bytes each for bf16, 4 for fp32); with more, only a piece's
+                            are held, and each piece's logits are computed a second time.
+                            At most ceil(V_head / 256) pieces are made.  No effect when no
+                            gradient is asked for: nothing is kept then. */
+  float loss_scale;      /* factor of the total and of every gradient; finite */
+} dspark_loss_config;
+
+/* Outputs of dspark_head_loss (device memory).  Gradients are of `total`, have the
+   config's dtype and are overwritten, not added to. */
+typedef struct dspark_loss_outputs {
+  float* loss;           /* required [T]: the negative log-likelihood of each row's label;
+                            0 for a row that carries no loss */
+  float* total;          /* required [1]; 0 when no row carries a loss */
+  int32_t* n_rows;       /* [1] rows that carry a loss; or NULL */
+  void* d_hidden;        /* [T, H] (0 for rows without a loss); or NULL */
+  void* d_lm_head;       /* [V_head, H]; or NULL (a frozen lm_head) */
+  void* d_markov_w1;     /* [V, r]; or NULL */
+  void* d_markov_w2;     /* [r, V_head]; or NULL */
+} dspark_loss_outputs;
+
+/* Bytes of device workspace dspark_head_loss needs for this config, head and set of
+   requested gradients; 0 on invalid input.  256-byte aligned; needs no initialisation. */
+size_t dspark_head_loss_workspace_size(const dspark_loss_config* cfg,
+                                       const dspark_head* head,
+                                       const dspark_loss_outputs* out);
+
+/*
+ * dspark_head_loss -- softmax cross entropy of the Markov-corrected logits over the
+ * head's vocabulary, with its gradients:
+ *
+ *   z[t, v] = hidden[t] . lm_head[v] + lm_bias[v] + markov_w1[prev[t]] . markov_w2[:, v]
+ *   loss[t] = log sum_v exp z[t, v] - z[t, label[t]]
+ *
+ * hidden  device [T, H] dtype.  Rows of blocks [B, L_in, H] are passed as T = B * L_in
+ *         (in the 1+N layout with a negative label at slot 0)
+ * prev    device [T] int32: the token before each slot, in [0, V); NULL when r = 0
+ * labels  device [T] int32: the target token of each slot.  A negative label, or a token
+ *         the head cannot emit (absent from d2t, or masked by lm_bias <= -1e8), marks a
+ *         row without a loss: nothing of that row is read into any result
+ * weights device [T] fp32 >= 0, or NULL (all 1): w_t
+ *
+ * The head's lm_head, lm_bias, d2t, V_head, markov_w1 and markov_w2 are read (the last
+ * two NULL when r = 0); w_conf, b_conf and prepared are not.  Masked head rows take no
+ * part: their probability is 0, their gradients are 0, and their weights are not read.
+ * lm_bias itself gets no gradient.  A label at or above V, or a prev outside [0, V) on a
+ * row with a loss, drops the row and raises the error word (dspark_device_status).
+ *
+ * bf16: products on the tensor cores with fp32 accumulation; the softmax statistics,
+ * losses and sums are fp32 or wider; the gradient of the logits is rounded to bf16 once
+ * before the two gradient products, each gradient once on output.  No atomics decide an
+ * order of summation: the same call gives the same bits.  Not reentrant on one
+ * workspace.  Can be captured into a CUDA graph.
+ */
+dspark_status dspark_head_loss(const dspark_loss_config* cfg, const dspark_head* head,
+                               const void* hidden, const int32_t* prev,
+                               const int32_t* labels, const float* weights,
+                               const dspark_loss_outputs* out, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Sizes and knobs of dspark_block_norm and its gradient. */
+typedef struct dspark_norm_config {
+  int32_t T;             /* rows (tokens), >= 1 */
+  int32_t H;             /* features, 1 .. 8192 */
+  int32_t dtype;         /* dspark_dtype of every tensor */
+  int32_t gate_span;     /* consecutive rows that share one gate row, >= 1 */
+  float eps;             /* > 0 */
+  float residual_scale;  /* s below; finite */
+  float weight_offset;   /* added to the norm weights (1 for weights stored about 0) */
+} dspark_norm_config;
+
+/*
+ * dspark_block_norm -- the norms around the end of a drafter block:
+ *
+ *   u = y / rms(y) * (weight_offset + w_post)       (u = y when w_post is NULL)
+ *   x_out = x + s * gate * u                        (gate = 1 when NULL)
+ *   h = x_out / rms(x_out) * (weight_offset + w_pre),   rms(a) = sqrt(mean(a^2) + eps)
+ *
+ * x, y    device [T, H]: the residual stream and the block's output.  y NULL: x_out = x
+ * gate    device [ceil(T / gate_span), H] or NULL
+ * w_post, w_pre device [H]; w_pre is required
+ * x_out   device [T, H] or NULL: the stream after the block (the head's conf_hidden);
+ *         may be x itself
+ * h       device [T, H]: the head's hidden; may be y itself
+ *
+ * Arithmetic in fp32; h is computed from x_out before its rounding.
+ */
+dspark_status dspark_block_norm(const dspark_norm_config* cfg, const void* x, const void* y,
+                                const void* gate, const void* w_post, const void* w_pre,
+                                void* x_out, void* h, void* stream);
+
+/* Bytes of device workspace dspark_block_norm_backward needs; 0 on invalid input. */
+size_t dspark_block_norm_workspace_size(const dspark_norm_config* cfg);
+
+/*
+ * dspark_block_norm_backward -- the gradients of dspark_block_norm, from its inputs:
+ *
+ * d_h     device [T, H]: the gradient of h       d_x_out device [T, H] or NULL: of x_out
+ * d_x     device [T, H]                          d_y     device [T, H]; NULL with y
+ * d_gate  device, gate's shape (summed over the rows that share a gate row); NULL with gate
+ * d_w_post, d_w_pre device [H]: summed over the rows; d_w_post NULL with w_post
+ *
+ * Every gradient is overwritten, and must not overlap an input or another one.  The
+ * sums over rows are taken in a fixed order.
+ */
+dspark_status dspark_block_norm_backward(const dspark_norm_config* cfg, const void* x,
+                                         const void* y, const void* gate,
+                                         const void* w_post, const void* w_pre,
+                                         const void* d_h, const void* d_x_out, void* d_x,
+                                         void* d_y, void* d_gate, void* d_w_post,
+                                         void* d_w_pre, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* One gradient of dspark_clip_grads. */
+typedef struct dspark_grad {
+  const void* in;        /* device [n] */
+  void* out;             /* device [n]: in itself, or memory that overlaps no gradient */
+  int64_t n;             /* elements, >= 0 */
+  int32_t dtype;         /* dspark_dtype */
+} dspark_grad;
+
+/* Bytes of device workspace dspark_clip_grads needs for `count` gradients; 0 on invalid
+   input. */
+size_t dspark_clip_grads_workspace_size(int32_t count, const dspark_grad* grads);
+
+/*
+ * dspark_clip_grads -- the global norm of a list of gradients, and the clipped list:
+ *
+ *   norm = sqrt(sum over all elements of in^2),   out = in * min(1, max_norm / (norm + 1e-6))
+ *
+ * grads    host [count]: read during the call only
+ * max_norm >= 0
+ * norm     device [1] fp32
+ *
+ * Squares are summed in fp32 within a thread and in fp64 above, in a fixed order.  When
+ * the norm is not finite, out = in: the norm says so, and the caller skips the step.
+ * Where out is in and the factor is 1 nothing is written.
+ */
+dspark_status dspark_clip_grads(int32_t count, const dspark_grad* grads, float max_norm,
+                                float* norm, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
 /* Static description of a status code. */
 const char* dspark_status_string(int32_t status);
 
