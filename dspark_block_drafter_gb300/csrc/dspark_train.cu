@@ -62,6 +62,8 @@ static dspark_status validate_loss(const dspark_loss_config* c, const dspark_hea
       return fail(DSPARK_ERR_UNSUPPORTED, "bf16 path needs V_head % 8 == 0 (16-byte rows)");
     if (!aligned(h->lm_head, 16) || (c->r > 0 && !aligned(h->markov_w2, 16)))
       return fail(DSPARK_ERR_INVALID_ARG, "bf16 weights must be 16-byte aligned");
+    if (!aligned(o->d_lm_head, 16))
+      return fail(DSPARK_ERR_INVALID_ARG, "bf16 d_lm_head must be 16-byte aligned");
   }
   return DSPARK_OK;
 }
@@ -91,6 +93,7 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
     return (void*)at;
   };
   const size_t Tp = (size_t)p->Tp, Vh = (size_t)p->Vh, es = c->dtype == DSPARK_F32 ? 4 : 2;
+  const bool tc = c->dtype == DSPARK_BF16;
   p->ctrl = (uint32_t*)take(256);
   p->tok = (int32_t*)take(4 * Tp);
   p->lab = (int32_t*)take(4 * Tp);
@@ -104,28 +107,34 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
     p->vinv = (int32_t*)take(4 * Vh);
     p->biasc = (float*)take(4 * Vh);
     p->vchunk = (int*)take(4 * (size_t)emit_chunks(p->Vh));
+    if (tc) {
+      p->wc = take(es * Vh * p->H);
+      p->w2c = take(es * Vh * p->r);
+    }
   }
   p->x = take(es * Tp * p->Kx);
-  p->stat_cols = 64;
+  p->stat_cols = tc ? 128 : 64;
   p->n_stat = (p->Vh + p->stat_cols - 1) / p->stat_cols;
   p->stat = (float2*)take(sizeof(float2) * Tp * p->n_stat);
   if (p->grads) {
     const int most = (p->Vh + 255) / 256;
-    const size_t qs = 4;
     int pieces = c->vocab_pieces;
     if (pieces == 0) {
       // keep the whole vocabulary's numerators while they take no more than 8 GiB (a
       // second computation of the logits costs a third more products)
-      const size_t all = Tp * align_up(Vh, 256) * qs, limit = (size_t)8 << 30;
+      const size_t all = Tp * align_up(Vh, 256) * es, limit = (size_t)8 << 30;
       pieces = (int)std::min<size_t>((all + limit - 1) / limit, (size_t)most);
     }
     pieces = std::min(pieces, most);
     p->piece_cols = (most + pieces - 1) / pieces * 256;
     p->pieces = (p->Vh + p->piece_cols - 1) / p->piece_cols;
     p->ldq = (size_t)p->piece_cols;
-    p->q = take(qs * Tp * p->ldq);
+    p->q = take(es * Tp * p->ldq);
+    if (tc) p->qres = (float*)take(4 * Tp);
     if (p->d_hidden || p->d_w1) {
-      p->splits = loss_simt_splits(p->T, p->Kx, p->piece_cols);
+      p->splits = tc ? loss_tc_splits(p->T, p->d_hidden ? p->H : 0, p->d_w1 ? p->r : 0,
+                                      p->piece_cols)
+                     : loss_simt_splits(p->T, p->Kx, p->piece_cols);
       p->dxp = (float*)take(sizeof(float) * p->splits * Tp * p->Kx);
     }
   }
@@ -133,19 +142,23 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
 }
 
 static cudaError_t run_loss(const LossPlan& p) {
+  const bool tc = p.dtype == DSPARK_BF16;
+  const auto logits = tc ? launch_loss_logits_tc : launch_loss_logits_simt;
+  const auto product_dx = tc ? launch_loss_dx_tc : launch_loss_dx_simt;
+  const auto product_dw = tc ? launch_loss_dw_tc : launch_loss_dw_simt;
   cudaError_t e = launch_loss_plan(p);
   if (e != cudaSuccess) return e;
   const bool keep = p.grads && p.pieces == 1;
-  e = launch_loss_logits_simt(p, 0, p.Vh, true, keep);
+  e = logits(p, 0, p.Vh, true, keep);
   if (e == cudaSuccess) e = launch_loss_rows(p);
   if (e != cudaSuccess || !p.grads) return e;
   const bool dx = p.d_hidden || p.d_w1, dw = p.d_lm_head || p.d_w2;
   for (int c = 0; c < p.pieces; ++c) {
     const int v0 = c * p.piece_cols, v1 = std::min(p.Vh, v0 + p.piece_cols);
-    if (!keep) e = launch_loss_logits_simt(p, v0, v1, false, true);
-    if (e == cudaSuccess) e = launch_loss_dz(p, v0, v1);
-    if (e == cudaSuccess && dx) e = launch_loss_dx_simt(p, v0, v1, c == 0);
-    if (e == cudaSuccess && dw) e = launch_loss_dw_simt(p, v0, v1);
+    if (!keep) e = logits(p, v0, v1, false, true);
+    if (e == cudaSuccess && (keep || !tc)) e = launch_loss_dz(p, v0, v1);
+    if (e == cudaSuccess && dx) e = product_dx(p, v0, v1, c == 0);
+    if (e == cudaSuccess && dw) e = product_dw(p, v0, v1);
     if (e != cudaSuccess) return e;
   }
   return dx ? launch_loss_dx(p) : cudaSuccess;

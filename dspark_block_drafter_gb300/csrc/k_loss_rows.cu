@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(128) loss_rows(const LossPlan p) {
   }
 }
 
-// q = w (softmax - onehot) from stored logits, in place (columns [v0, v1)).
-__global__ void __launch_bounds__(256) loss_dz(const LossPlan p, int v0, int v1) {
+// q = w (softmax - onehot) in place, columns [v0, v1): fp32 from stored logits.
+__global__ void __launch_bounds__(256) loss_dz_f32(const LossPlan p, int v0, int v1) {
   const int n_tok = (int)p.ctrl[kLossTok], i = blockIdx.x;
   if (i >= n_tok) return;
   const int end = min(v1, (int)p.ctrl[kLossVoc]);
@@ -225,8 +225,58 @@ __global__ void __launch_bounds__(256) loss_dz(const LossPlan p, int v0, int v1)
     q[v - v0] = w * (__expf(q[v - v0] - lse) - (v == lab ? 1.f : 0.f));
 }
 
-// CTA i: row i of the gradient of X, summed over the splits of the vocabulary, times the
-// scale: d_hidden's row, and the gradient of markov_w1's row prev (left in split 0).
+// The same in bf16 from the stored distances (one piece: v0 = 0), over whole 256-column
+// tiles: columns past the vocabulary become 0.  Eight columns a thread.
+__global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
+  const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc], i = blockIdx.x;
+  if (i >= n_tok) return;
+  uint4* q = (uint4*)((uint16_t*)p.q + (size_t)i * p.ldq);
+  const float lse = p.lse[i], w = p.wrow[i];
+  const int lab = p.lab[i], end = (n_voc + 255) / 256 * 32, tiles = (n_voc + 127) / 128;
+  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < end; c += gridDim.y * blockDim.x) {
+    const uint4 x = q[c];
+    const int tile = min(c / 16, tiles - 1);          // (a tile past the last is all far)
+    const float s = (p.stat[(size_t)i * p.n_stat + tile].x - lse) * 1.44269504f;
+    const uint32_t g[4] = {x.x, x.y, x.z, x.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int v = 8 * c + 2 * j;
+      float e0 = w * loss_gap_exp(g[j] & 0xFFFFu, s), e1 = w * loss_gap_exp(g[j] >> 16, s);
+      if (v == lab) e0 = loss_label_grad(p, i, e0 - w);
+      if (v + 1 == lab) e1 = loss_label_grad(p, i, e1 - w);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
+      o[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    q[c] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// The compact head of a bias-form bf16 head with masked rows: its rows and its columns of
+// markov_w2, then zeros up to a multiple of 256.
+__global__ void __launch_bounds__(256) loss_gather_head(const LossPlan p) {
+  const int n = (int)p.ctrl[kLossVoc];
+  if (n >= p.Vh) return;
+  const int end = min(p.Vh, (n + 255) / 256 * 256), per = p.H / 8;
+  const uint4* w = (const uint4*)p.lm_head;
+  uint4* wc = (uint4*)p.wc;
+  for (int j = blockIdx.x; j < end; j += gridDim.x) {
+    const size_t from = j < n ? (size_t)p.vlist[j] * per : 0;
+    for (int k = threadIdx.x; k < per; k += blockDim.x)
+      wc[(size_t)j * per + k] = j < n ? w[from + k] : make_uint4(0, 0, 0, 0);
+  }
+  const __nv_bfloat16* w2 = (const __nv_bfloat16*)p.w2;
+  __nv_bfloat16* w2c = (__nv_bfloat16*)p.w2c;
+  for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < end; j += gridDim.x * blockDim.x) {
+    const int v = j < n ? p.vlist[j] : -1;
+    for (int k = 0; k < p.r; ++k)
+      w2c[(size_t)k * p.Vh + j] = v >= 0 ? w2[(size_t)k * p.Vh + v] : __float2bfloat16(0.f);
+  }
+}
+
+// CTA i: row i of the gradient of X, summed over the splits of the vocabulary (and, in
+// bf16, with what q lost at the label), times the scale: d_hidden's row, and the gradient of
+// markov_w1's row prev (left in split 0).
 template <typename E>
 __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
   const int i = blockIdx.x;
@@ -234,16 +284,21 @@ __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
   const float k = __uint_as_float(p.ctrl[kLossScale]);
   const size_t step = (size_t)p.Tp * p.Kx;
   float* x = p.dxp + (size_t)i * p.Kx;
+  const float lost = p.qres ? p.qres[i] : 0.f;
+  const size_t row = (size_t)loss_head_row(p, p.lab[i]);
   for (int c = threadIdx.x; c < p.Kx; c += blockDim.x) {
-    if (c < p.Hp ? !p.d_hidden : !p.d_w1) continue;
+    const bool head = c < p.Hp;
+    if (head ? !p.d_hidden || c >= p.H : !p.d_w1 || c - p.Hp >= p.r) continue;
     float a = x[c];
     for (int s = 1; s < p.splits; ++s) a += x[s * step + c];
+    if (p.qres)
+      a += lost * to_f32(head ? ((const E*)p.lm_head)[row * p.H + c]
+                              : ((const E*)p.w2)[(size_t)(c - p.Hp) * p.Vh + row]);
     a *= k;
-    if (c < p.Hp) {
-      if (c < p.H) ((E*)p.d_hidden)[(size_t)p.tok[i] * p.H + c] = from_f32<E>(a);
-    } else {
+    if (head)
+      ((E*)p.d_hidden)[(size_t)p.tok[i] * p.H + c] = from_f32<E>(a);
+    else
       x[c] = a;
-    }
   }
 }
 
@@ -296,6 +351,7 @@ cudaError_t launch_loss_plan(const LossPlan& p) {
     e = cudaMemsetAsync(p.vinv, 0xFF, sizeof(int32_t) * (size_t)p.Vh, p.stream);
     if (e != cudaSuccess) return e;
     loss_vocab<<<std::min(256, (p.Vh + 255) / 256), 256, 0, p.stream>>>(p, chunks);
+    if (p.wc) loss_gather_head<<<1216, 256, 0, p.stream>>>(p);
   }
   loss_tokens<<<1, kPlanThreads, 0, p.stream>>>(p);
   const size_t es = p.dtype == 0 ? 4 : 2;
@@ -324,8 +380,13 @@ cudaError_t launch_loss_rows(const LossPlan& p) {
 }
 
 cudaError_t launch_loss_dz(const LossPlan& p, int v0, int v1) {
-  const unsigned blocks = (unsigned)std::min(64, (v1 - v0 + 255) / 256);
-  loss_dz<<<dim3((unsigned)p.T, blocks), 256, 0, p.stream>>>(p, v0, v1);
+  if (p.dtype == 0) {
+    const unsigned blocks = (unsigned)std::min(64, (v1 - v0 + 255) / 256);
+    loss_dz_f32<<<dim3((unsigned)p.T, blocks), 256, 0, p.stream>>>(p, v0, v1);
+  } else {
+    const unsigned blocks = (unsigned)std::min(16, (p.Vh + 2047) / 2048);
+    loss_dz_bf16<<<dim3((unsigned)p.T, blocks), 256, 0, p.stream>>>(p);
+  }
   return cudaGetLastError();
 }
 

@@ -7,8 +7,6 @@
 // i: compact rows, j: compact head rows, c: columns of X.  One 64 x 64 tile per CTA, 16
 // deep, four by four results per thread; operands pass through shared memory with the
 // index that is contiguous in memory spread over a warp's lanes.
-#include <cuda_bf16.h>
-
 #include <algorithm>
 
 #include "common.cuh"
@@ -60,15 +58,14 @@ __device__ __forceinline__ void tile_product(float (&acc)[4][4], int depth, bool
 
 // Columns [v0, v1) of the logits: their statistics per 64-column tile and the labels'
 // logits (`stats`), and the logits themselves (`store`).
-template <typename E>
 __global__ void __launch_bounds__(256)
 loss_logits(const LossPlan p, int v0, int v1, bool stats, bool store) {
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
   const int m0 = blockIdx.y * kTile, j0 = v0 + blockIdx.x * kTile;
   if (m0 >= n_tok || j0 >= n_voc) return;
-  const E* x = (const E*)p.x;
-  const E* w = (const E*)p.lm_head;
-  const E* w2 = (const E*)p.w2;
+  const float* x = (const float*)p.x;
+  const float* w = (const float*)p.lm_head;
+  const float* w2 = (const float*)p.w2;
   __shared__ int s_row[kTile];
   if (threadIdx.x < kTile)
     s_row[threadIdx.x] = j0 + (int)threadIdx.x < n_voc ? loss_head_row(p, j0 + threadIdx.x) : -1;
@@ -76,17 +73,17 @@ loss_logits(const LossPlan p, int v0, int v1, bool stats, bool store) {
   float acc[4][4] = {};
   tile_product(
       acc, p.Kx, true,
-      [&](int m, int k) { return to_f32(x[(size_t)(m0 + m) * p.Kx + k]); },
+      [&](int m, int k) { return x[(size_t)(m0 + m) * p.Kx + k]; },
       [&](float (*sb)[kTile + 4], int k0) {
         if (k0 < p.Hp)
           load_tile(sb, true, [&](int n, int k) {
             const int row = s_row[n], h = k0 + k;
-            return row >= 0 && h < p.H ? to_f32(w[(size_t)row * p.H + h]) : 0.f;
+            return row >= 0 && h < p.H ? (w[(size_t)row * p.H + h]) : 0.f;
           });
         else
           load_tile(sb, false, [&](int n, int k) {
             const int row = s_row[n], c = k0 - p.Hp + k;
-            return row >= 0 && c < p.r ? to_f32(w2[(size_t)c * p.Vh + row]) : 0.f;
+            return row >= 0 && c < p.r ? (w2[(size_t)c * p.Vh + row]) : 0.f;
           });
       });
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
@@ -126,7 +123,6 @@ loss_logits(const LossPlan p, int v0, int v1, bool stats, bool store) {
 }
 
 // dX of vocabulary columns [v0, v1): split blockIdx.z of their range.
-template <typename E>
 __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1, bool first) {
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
   const int m0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
@@ -134,8 +130,8 @@ __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1,
   const int share = ((v1 - v0 + (int)gridDim.z - 1) / (int)gridDim.z + kDepth - 1) / kDepth * kDepth;
   const int ja = v0 + (int)blockIdx.z * share, jb = min(n_voc, ja + share);
   const float* q = (const float*)p.q;
-  const E* w = (const E*)p.lm_head;
-  const E* w2 = (const E*)p.w2;
+  const float* w = (const float*)p.lm_head;
+  const float* w2 = (const float*)p.w2;
   float acc[4][4] = {};
   if (jb > ja)
     tile_product(
@@ -150,8 +146,8 @@ __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1,
             const int j = ja + k0 + k, c = c0 + n;
             if (j >= jb) return 0.f;
             const int row = loss_head_row(p, j);
-            if (head) return c < p.H ? to_f32(w[(size_t)row * p.H + c]) : 0.f;
-            return c - p.Hp < p.r ? to_f32(w2[(size_t)(c - p.Hp) * p.Vh + row]) : 0.f;
+            if (head) return c < p.H ? (w[(size_t)row * p.H + c]) : 0.f;
+            return c - p.Hp < p.r ? (w2[(size_t)(c - p.Hp) * p.Vh + row]) : 0.f;
           });
         });
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
@@ -168,14 +164,13 @@ __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1,
 }
 
 // dW of vocabulary columns [v0, v1).
-template <typename E>
 __global__ void __launch_bounds__(256) loss_dw(const LossPlan p, int v0, int v1) {
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
   const int j0 = v0 + blockIdx.y * kTile, c0 = blockIdx.x * kTile;
   const bool head = c0 < p.Hp;
   if (j0 >= n_voc || (head ? !p.d_lm_head : !p.d_w2)) return;
   const float* q = (const float*)p.q;
-  const E* x = (const E*)p.x;
+  const float* x = (const float*)p.x;
   float acc[4][4] = {};
   tile_product(
       acc, n_tok, false,
@@ -185,7 +180,7 @@ __global__ void __launch_bounds__(256) loss_dw(const LossPlan p, int v0, int v1)
       },
       [&](float (*sb)[kTile + 4], int k0) {
         load_tile(sb, false, [&](int n, int k) {
-          return k0 + k < n_tok ? to_f32(x[(size_t)(k0 + k) * p.Kx + c0 + n]) : 0.f;
+          return k0 + k < n_tok ? (x[(size_t)(k0 + k) * p.Kx + c0 + n]) : 0.f;
         });
       });
   const float scale = __uint_as_float(p.ctrl[kLossScale]);
@@ -199,9 +194,9 @@ __global__ void __launch_bounds__(256) loss_dw(const LossPlan p, int v0, int v1)
       const int row = loss_head_row(p, j);
       const float g = acc[a][b] * scale;
       if (head) {
-        if (c < p.H) ((E*)p.d_lm_head)[(size_t)row * p.H + c] = (E)g;
+        if (c < p.H) ((float*)p.d_lm_head)[(size_t)row * p.H + c] = g;
       } else if (c - p.Hp < p.r) {
-        ((E*)p.d_w2)[(size_t)(c - p.Hp) * p.Vh + row] = (E)g;
+        ((float*)p.d_w2)[(size_t)(c - p.Hp) * p.Vh + row] = g;
       }
     }
 }
@@ -216,28 +211,19 @@ int loss_simt_splits(int T, int Kx, int cols) {
 
 cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stats, bool store) {
   const dim3 grid((v1 - v0 + kTile - 1) / kTile, (p.T + kTile - 1) / kTile);
-  if (p.dtype == 0)
-    loss_logits<float><<<grid, 256, 0, p.stream>>>(p, v0, v1, stats, store);
-  else
-    loss_logits<__nv_bfloat16><<<grid, 256, 0, p.stream>>>(p, v0, v1, stats, store);
+  loss_logits<<<grid, 256, 0, p.stream>>>(p, v0, v1, stats, store);
   return cudaGetLastError();
 }
 
 cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first) {
   const dim3 grid(p.Kx / kTile, (p.T + kTile - 1) / kTile, p.splits);
-  if (p.dtype == 0)
-    loss_dx<float><<<grid, 256, 0, p.stream>>>(p, v0, v1, first);
-  else
-    loss_dx<__nv_bfloat16><<<grid, 256, 0, p.stream>>>(p, v0, v1, first);
+  loss_dx<<<grid, 256, 0, p.stream>>>(p, v0, v1, first);
   return cudaGetLastError();
 }
 
 cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1) {
   const dim3 grid(p.Kx / kTile, (v1 - v0 + kTile - 1) / kTile);
-  if (p.dtype == 0)
-    loss_dw<float><<<grid, 256, 0, p.stream>>>(p, v0, v1);
-  else
-    loss_dw<__nv_bfloat16><<<grid, 256, 0, p.stream>>>(p, v0, v1);
+  loss_dw<<<grid, 256, 0, p.stream>>>(p, v0, v1);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,659 @@
+// The training loss of a bf16 head: its three products on the 5th-generation tensor cores.
+//
+//   logits  z[i][j]  = X[i] . [lm_head[j] | markov_w2[:, j]] + bias[j]      K = columns of X
+//   dX      dx[i][c] = sum_j q[i][j] [lm_head | markov_w2^T][j][c]          K = head rows
+//   dW      [d_lm_head | d_markov_w2^T][j][c] = scale sum_i q[i][j] X[i][c] K = rows
+//
+// i: compact rows, j: compact head rows, c: columns of X.  One kernel form does all three:
+// a 128 (or, for a CTA pair, 256) x 256 tile of the result accumulates in TMEM over K-blocks
+// of 64.  Every operand comes in boxes of 64 x 64 elements straight from the array it lies
+// in, whichever of its two indices is contiguous: the box is a swizzled K-major tile when
+// that index is K and an MN-major one when it is not, and the matrix descriptors say which.
+// So no operand is ever transposed in memory, and the Markov term is nothing but some more
+// K-blocks (logits) or columns (gradients), read from markov_w1's gathered rows and from
+// markov_w2 as they are.
+//
+// Persistent and warp-specialised, one CTA per SM: warp 8 issues the TMA copies, one thread
+// of warp 9 the MMAs; warps 0-3 take the first 128 columns of a finished accumulator, warps
+// 4-7 the others (there are two accumulators, so that this overlaps the next products).
+//
+// The tensor core cuts each partial sum of an accumulator toward zero, so a long sum drifts:
+// over K = 4352 the losses were off by 5e-6.  The logits' accumulator is therefore read
+// every 512 of K and the parts are added in fp32 registers (which hold the tile's 128
+// columns of a row until it is complete).  The gradients, rounded to bf16, need no such care.
+//
+// The logits are never stored.  Their epilogue has one row per thread: it takes the maximum
+// and the sum of exponentials of each 128-column tile, and, when gradients follow, stores
+// how far each logit lies below its tile's maximum as a 16-bit fixed-point number (see
+// loss.h), from which the gradient is made once the row's log-sum-exp is known.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "loss.h"
+#include "ptx.cuh"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;
+constexpr uint32_t kBox = 64 * 64 * 2;               // bytes of one operand box
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kSumBlocks = 8;                        // K-blocks of one part of a logit's sum
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kBarBytes = 512;
+constexpr long long kWaitBudget = 2000000000ll;      // ~1 s of SM clocks
+
+enum : int { kLogits = 0, kDx = 1, kDw = 2 };
+// what the logits' epilogue makes: the statistics, the stored distances from the tile's
+// maximum, or (with the log-sum-exp known) the gradient of the logits
+enum : int { kWantStats = 1, kWantGap = 2, kWantGrad = 4 };
+
+struct Maps {
+  CUtensorMap x, q, w[2], w2[2];       // [1]: the compacted vocabulary of a bias-form head
+};
+
+struct TcArgs {
+  LossPlan p;
+  int v0, v1;          // compact head rows of this piece
+  int want;            // kWant...
+  int first;           // dX: the first piece (later ones add)
+  int n_head, n_markov;  // 256-column tiles of X's two parts that are computed
+};
+
+// One unit of work: a tile of the result and a range of K-blocks.
+struct Unit {
+  int m, n;            // first row of the tile (of M), tile index of N
+  int kb0, kb1;
+  int split;
+};
+
+template <int MODE, int CG>
+__device__ __forceinline__ int unit_count(const TcArgs& g, int n_tok, int n_voc) {
+  const int mt = (n_tok + kTileM * CG - 1) / (kTileM * CG);
+  const int cols = max(0, min(g.v1, n_voc) - g.v0);
+  const int nt = g.n_head + g.n_markov;
+  if (MODE == kLogits) return mt * ((cols + kTileN - 1) / kTileN);
+  if (MODE == kDx) return mt * nt * g.p.splits;
+  return (cols + kTileM * CG - 1) / (kTileM * CG) * nt;
+}
+
+constexpr int kRowGroup = 24;     // M tiles whose rows of X are kept in L2 together
+
+template <int MODE, int CG>
+__device__ __forceinline__ Unit unit_at(const TcArgs& g, int u, int n_tok, int n_voc) {
+  Unit t;
+  const int mt = (n_tok + kTileM * CG - 1) / (kTileM * CG);
+  const int cols = max(0, min(g.v1, n_voc) - g.v0);
+  const int nt = g.n_head + g.n_markov;
+  t.kb0 = 0;
+  t.split = 0;
+  if (MODE == kLogits) {
+    // head-row tiles in order, all M tiles of a group for each: the head streams once for
+    // every group
+    const int vt = (cols + kTileN - 1) / kTileN;
+    const int grp = u / (kRowGroup * vt), in = u - grp * kRowGroup * vt;
+    const int rows = min(kRowGroup, mt - grp * kRowGroup);
+    t.m = (grp * kRowGroup + in % rows) * kTileM * CG;
+    t.n = in / rows;
+    t.kb1 = g.p.Kx / kBlockK;
+  } else if (MODE == kDx) {
+    // splits of K in order, so that the CTAs at work share their operands' K range in L2
+    const int nkb = (cols + kBlockK - 1) / kBlockK;
+    t.split = u / (mt * nt);
+    const int in = u % (mt * nt);
+    t.m = in / nt * kTileM * CG;
+    t.n = in % nt;
+    t.kb0 = (int)((long long)nkb * t.split / g.p.splits);
+    t.kb1 = (int)((long long)nkb * (t.split + 1) / g.p.splits);
+  } else {
+    t.m = u / nt * kTileM * CG;
+    t.n = u % nt;
+    t.kb1 = (n_tok + kBlockK - 1) / kBlockK;
+  }
+  return t;
+}
+
+// Column of X at which N tile n starts, and whether it is of the Markov part.
+__device__ __forceinline__ bool column_tile(const TcArgs& g, int n, int* c0) {
+  const bool markov = n >= g.n_head;
+  *c0 = markov ? g.p.Hp + (n - g.n_head) * kTileN : n * kTileN;
+  return markov;
+}
+
+template <int CG>
+__device__ __forceinline__ void load_box(uint8_t* dst, const CUtensorMap* m, uint64_t* bar,
+                                         uint32_t bar_leader, int x, int y) {
+  if (CG == 2)
+    ptx::tma_load_2d_pair(dst, m, bar_leader, x, y);
+  else
+    ptx::tma_load_2d(dst, m, bar, x, y);
+}
+
+template <int MODE, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g, int stages) {
+  constexpr int kBoxB = kTileN / CG / 64;              // boxes of N this CTA stages
+  constexpr uint32_t kStageA = 2 * kBox, kStageB = kBoxB * kBox;
+  constexpr uint32_t kStage = kStageA + kStageB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = (uint64_t*)(smem + (size_t)stages * kStage);
+  uint64_t* empty = full + stages;
+  uint64_t* acc_full = empty + stages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = (uint32_t*)(drain + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0;
+  const bool leader = rank == 0;
+  const LossPlan& p = g.p;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&acc_full[a], 1);
+      ptx::mbar_init(&acc_empty[a], kEpiWarps * CG);
+    }
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0) {
+    if (CG == 2) {
+      ptx::tmem_alloc_pair(tmem_slot, 512);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(tmem_slot, 512);
+      ptx::tmem_relinquish();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (CG == 2) ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t full0 = CG == 2 ? ptx::mapa_shared(ptx::smem_u32(full), 0) : 0;
+  const uint32_t acc_empty0 = CG == 2 ? ptx::mapa_shared(ptx::smem_u32(acc_empty), 0) : 0;
+  const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc];
+  const int compact = n_voc < p.Vh ? 1 : 0;            // (Vh rows: the head itself)
+  const int units = unit_count<MODE, CG>(g, n_tok, n_voc);
+  const int u0 = blockIdx.x / CG, step = gridDim.x / CG;
+
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    flag_error(p.ctrl, kErrTimeout);
+  };
+
+  if (warp == kEpiWarps) {
+    // ---------------------------------------------------------------- producer
+    if (lane == 0) {
+      uint32_t it = 0, s = 0, ph = 0;
+      bool ok = true;
+      const int hb = p.Hp / kBlockK;
+      const CUtensorMap* mw = &maps.w[compact];
+      const CUtensorMap* mw2 = &maps.w2[compact];
+      for (int u = u0; u < units && ok; u += step) {
+        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc);
+        const int ma = t.m + (int)rank * kTileM;             // this CTA's rows of M
+        const int half = (int)rank * (kTileN / CG);          // and its share of N
+        int c0 = 0;
+        bool markov = false;
+        if (MODE != kLogits) markov = column_tile(g, t.n, &c0);
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          if (!ptx::mbar_wait(&empty[s], ph ^ 1, kWaitBudget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* a = smem + (size_t)s * kStage;
+          uint8_t* b = a + kStageA;
+          const uint32_t bar = full0 + s * 8;
+          if (leader) ptx::mbar_arrive_expect_tx(&full[s], CG * kStage);
+          const int k = kb * kBlockK;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (MODE == kLogits)
+              load_box<CG>(a + j * kBox, &maps.x, &full[s], bar, k, ma + 64 * j);
+            else if (MODE == kDx)
+              load_box<CG>(a + j * kBox, &maps.q, &full[s], bar, k, ma + 64 * j);
+            else
+              load_box<CG>(a + j * kBox, &maps.q, &full[s], bar, ma + 64 * j, k);
+          }
+#pragma unroll
+          for (int j = 0; j < kBoxB; ++j) {
+            const int n = half + 64 * j;
+            if (MODE == kLogits) {
+              const int v = g.v0 + t.n * kTileN + n;
+              if (kb < hb)
+                load_box<CG>(b + j * kBox, mw, &full[s], bar, k, v);
+              else
+                load_box<CG>(b + j * kBox, mw2, &full[s], bar, v, k - p.Hp);
+            } else if (MODE == kDx) {
+              if (!markov)
+                load_box<CG>(b + j * kBox, mw, &full[s], bar, c0 + n, g.v0 + k);
+              else
+                load_box<CG>(b + j * kBox, mw2, &full[s], bar, g.v0 + k, c0 - p.Hp + n);
+            } else {
+              load_box<CG>(b + j * kBox, &maps.x, &full[s], bar, c0 + n, k);
+            }
+          }
+          if (++s == (uint32_t)stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        give_up();
+        // let the copies already issued land before the CTA can exit
+        if (CG == 1) {
+          const uint32_t from = it > (uint32_t)stages ? it - stages : 0;
+          for (uint32_t j = from; j < it; ++j)
+            ptx::mbar_wait(&full[j % stages], (j / stages) & 1, kWaitBudget, nullptr);
+        } else {
+          const long long t0 = clock64();
+          while (clock64() - t0 < 1000000) {
+          }
+        }
+      }
+    }
+  } else if (warp == kEpiWarps + 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0 && leader) {
+      uint32_t s = 0, ph = 0, local = 0;
+      bool ok = true;
+      const int hb = p.Hp / kBlockK;
+      const uint32_t base = ptx::smem_u32(smem);
+      for (int u = u0; u < units; u += step) {
+        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc);
+        int c0 = 0;
+        bool b_mn = true;                       // dW; dX of the head's columns
+        if (MODE == kDx) b_mn = !column_tile(g, t.n, &c0);
+        constexpr bool a_mn = MODE == kDw;
+        for (int kb = t.kb0, part = 0; part == 0 || kb < t.kb1; ++part, ++local) {
+          const int part_end = MODE == kLogits ? min(t.kb1, kb + kSumBlocks) : t.kb1;
+          const uint32_t acc = local & 1, aph = (local >> 1) & 1;
+          if (!ptx::mbar_wait(&acc_empty[acc], aph ^ 1, kWaitBudget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t d = tmem + acc * kTileN;
+          uint32_t accum = 0u;
+          for (; kb < part_end; ++kb) {
+            if (!ptx::mbar_wait(&full[s], ph, kWaitBudget, abort_flag)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            if (MODE == kLogits) b_mn = kb >= hb;
+            const uint32_t idesc = ptx::idesc_bf16_f32(kTileM * CG, kTileN, a_mn, b_mn);
+            const uint32_t a0 = base + s * kStage, b0 = a0 + kStageA;
+            const uint64_t da = a_mn ? ptx::desc_mnmajor_sw128(a0, kBox, 1024)
+                                     : ptx::desc_kmajor_sw128(a0);
+            const uint64_t db = b_mn ? ptx::desc_mnmajor_sw128(b0, kBox, 1024)
+                                     : ptx::desc_kmajor_sw128(b0);
+            // 16 deep: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
+            const uint32_t sa = a_mn ? 128 : 2, sb = b_mn ? 128 : 2;
+#pragma unroll
+            for (int k = 0; k < kBlockK / 16; ++k) {
+              if (CG == 2)
+                ptx::mma_f16_pair(d, da + k * sa, db + k * sb, idesc, accum);
+              else
+                ptx::mma_f16(d, da + k * sa, db + k * sb, idesc, accum);
+              accum = 1u;
+            }
+            if (CG == 2)
+              ptx::mma_commit_pair_multicast(&empty[s], 0x3);
+            else
+              ptx::mma_commit(&empty[s]);
+            if (++s == (uint32_t)stages) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+          if (!ok) break;
+          if (CG == 2)
+            ptx::mma_commit_pair_multicast(&acc_full[acc], 0x3);
+          else
+            ptx::mma_commit(&acc_full[acc]);
+        }
+        if (!ok) break;
+      }
+      if (!ok) give_up();
+      if (CG == 2)
+        ptx::mma_commit_pair_multicast(drain, 0x1);
+      else
+        ptx::mma_commit(drain);
+      ptx::mbar_wait(drain, 0, kWaitBudget, nullptr);
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int quad = warp % 4, half = warp / 4;       // lanes and columns of this warp
+    const uint32_t at0 = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
+    const float scale = __uint_as_float(p.ctrl[kLossScale]);
+    uint32_t local = 0;
+    bool ok = true;
+    // the local-th accumulator is complete / has been read
+    auto acc_wait = [&]() {
+      ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&acc_full[local & 1], (local >> 1) & 1,
+                                                  kWaitBudget, abort_flag));
+      if (!ok) give_up();
+      ptx::tc_fence_after();
+      return ok;
+    };
+    auto acc_free = [&]() {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          ptx::mbar_arrive_cluster(acc_empty0 + (local & 1) * 8);
+        else
+          ptx::mbar_arrive(&acc_empty[local & 1]);
+      }
+      ++local;
+    };
+    for (int u = u0; u < units && ok; u += step) {
+      const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc);
+      const int m = t.m + (int)rank * kTileM + quad * 32 + lane;   // this thread's row of M
+      if (MODE == kLogits) {
+        const bool live = m < n_tok;
+        const int lab = live ? p.lab[m] : -1;
+        const int v0 = g.v0 + t.n * kTileN + half * 128;     // compact head row of column 0
+        const int n_in = n_voc - v0;                          // columns that exist
+        float z[128];
+        for (int kb = t.kb0; kb < t.kb1; kb += kSumBlocks) {
+          if (!acc_wait()) break;
+          const uint32_t at = at0 + (local & 1) * kTileN;
+          const bool first = kb == t.kb0;
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t r[32];
+            ptx::tmem_ld_32x32b_x32(at + c, r);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              z[c + j] = first ? __uint_as_float(r[j]) : z[c + j] + __uint_as_float(r[j]);
+          }
+          acc_free();
+        }
+        if (!ok) break;
+        if (p.vlist) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (j < n_in) z[j] += __ldg(p.biasc + v0 + j);
+        }
+        if (n_in < 128) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (j >= n_in) z[j] = -INFINITY;
+        }
+        float ref = 0.f, wt = 0.f;
+        if (g.want & kWantStats) {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 128; ++j) mx[j % 4] = fmaxf(mx[j % 4], z[j]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool here = lab >= v0 && lab < v0 + 128;
+          if (__any_sync(0xFFFFFFFFu, here)) {
+            float zl = 0.f;
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+              if (lab == v0 + j) zl = z[j];
+            if (here) p.zlab[m] = zl;
+          }
+          ref = top > -INFINITY ? top : 0.f;      // (a NaN passes the maximum, not the sum)
+          float sum[4] = {};
+#pragma unroll
+          for (int j = 0; j < 128; ++j) sum[j % 4] += __expf(z[j] - ref);
+          if (live && n_in > 0)
+            p.stat[(size_t)m * p.n_stat + v0 / 128] =
+                make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        } else if (live) {
+          ref = p.lse[m];
+          wt = p.wrow[m];
+        }
+        if (g.want & (kWantGap | kWantGrad)) {
+          uint16_t* qrow = (uint16_t*)p.q + (size_t)m * p.ldq + (v0 - g.v0);
+#pragma unroll
+          for (int c = 0; c < 128; c += 16) {
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float d0 = z[c + j] - ref, d1 = z[c + j + 1] - ref;
+              if (g.want & kWantGrad) {
+                float e0 = wt * __expf(d0), e1 = wt * __expf(d1);
+                if (lab == v0 + c + j) e0 = loss_label_grad(p, m, e0 - wt);
+                if (lab == v0 + c + j + 1) e1 = loss_label_grad(p, m, e1 - wt);
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+                o[j / 2] = *reinterpret_cast<const uint32_t*>(&b2);
+              } else {
+                o[j / 2] = __byte_perm(loss_gap(-d0), loss_gap(-d1), 0x5410);
+              }
+              if (!live) o[j / 2] = 0u;
+            }
+            ptx::st_global_v8(qrow + c, o);
+          }
+        }
+      } else {
+        if (!acc_wait()) break;
+        const uint32_t at = at0 + (local & 1) * kTileN;
+        const bool none = t.kb1 <= t.kb0;             // (nothing was accumulated)
+        int c0;
+        const bool markov = column_tile(g, t.n, &c0);
+        c0 += half * 128;
+        if (MODE == kDx) {
+          const int width = min(128, (markov ? p.Kx : p.Hp) - c0);
+          float* dx = p.dxp + ((size_t)t.split * p.Tp + m) * p.Kx + c0;
+#pragma unroll 1
+          for (int c = 0; c < width; c += 32) {
+            uint32_t r[32];
+            ptx::tmem_ld_32x32b_x32(at + c, r);
+            ptx::tmem_ld_wait();
+            if (m >= n_tok) continue;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              float x[8];
+#pragma unroll
+              for (int b = 0; b < 8; ++b) x[b] = none ? 0.f : __uint_as_float(r[j + b]);
+              if (!g.first) {
+                const float4 y0 = *reinterpret_cast<const float4*>(dx + c + j);
+                const float4 y1 = *reinterpret_cast<const float4*>(dx + c + j + 4);
+                x[0] += y0.x; x[1] += y0.y; x[2] += y0.z; x[3] += y0.w;
+                x[4] += y1.x; x[5] += y1.y; x[6] += y1.z; x[7] += y1.w;
+              }
+              ptx::st_global_v8(dx + c + j, x);
+            }
+          }
+        } else {
+          const int j0 = g.v0 + m;                            // compact head row
+          const bool live = j0 < min(g.v1, n_voc);
+          const size_t row = live ? (size_t)(compact ? p.vlist[j0] : j0) : 0;
+          const int width = min(128, markov ? p.r - (c0 - p.Hp) : p.H - c0);
+#pragma unroll 1
+          for (int c = 0; c < width; c += 32) {
+            uint32_t r[32];
+            ptx::tmem_ld_32x32b_x32(at + c, r);
+            ptx::tmem_ld_wait();
+            if (!live) continue;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              r[j] = none ? 0u : __float_as_uint(__uint_as_float(r[j]) * scale);
+            if (markov) {
+              __nv_bfloat16* d = (__nv_bfloat16*)p.d_w2 + (size_t)(c0 - p.Hp + c) * p.Vh + row;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (c + j < width) d[(size_t)j * p.Vh] = __float2bfloat16(__uint_as_float(r[j]));
+            } else {
+              __nv_bfloat16* d = (__nv_bfloat16*)p.d_lm_head + row * p.H + c0 + c;
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {               // (H is a multiple of 8)
+                if (c + j >= width) break;
+                uint4 o;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(
+                      __uint_as_float(r[j + 2 * b]), __uint_as_float(r[j + 2 * b + 1]));
+                  w[b] = *reinterpret_cast<const uint32_t*>(&b2);
+                }
+                *reinterpret_cast<uint4*>(d + j) = o;
+              }
+            }
+          }
+        }
+        acc_free();
+      }
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (CG == 2) ptx::cluster_sync();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    if (CG == 2)
+      ptx::tmem_dealloc_pair(tmem, 512);
+    else
+      ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                         cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
+  });
+  return fn;
+}
+
+// A [rows][ld] bf16 array, `cols` of each row in use, read in 64 x 64 boxes (zeros outside).
+bool encode_map(CUtensorMap* m, const void* base, size_t cols, size_t rows, size_t ld) {
+  auto encode = encode_fn();
+  if (!encode) return false;
+  cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
+  cuuint32_t box[2] = {64, 64}, es[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void*)base, dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_maps(const LossPlan& p, Maps* m) {
+  bool ok = encode_map(&m->x, p.x, p.Kx, p.Tp, p.Kx);
+  ok = ok && encode_map(&m->w[0], p.lm_head, p.H, p.Vh, p.H);
+  ok = ok && encode_map(&m->w[1], p.wc ? p.wc : p.lm_head, p.H, p.Vh, p.H);
+  m->w2[0] = m->w2[1] = m->w[0];
+  if (p.r > 0) {
+    ok = ok && encode_map(&m->w2[0], p.w2, p.Vh, p.r, p.Vh);
+    ok = ok && encode_map(&m->w2[1], p.w2c ? p.w2c : p.w2, p.Vh, p.r, p.Vh);
+  }
+  m->q = m->x;
+  if (p.q) ok = ok && encode_map(&m->q, p.q, p.ldq, p.Tp, p.ldq);
+  return ok;
+}
+
+template <int MODE, int CG>
+cudaError_t launch(const TcArgs& g, long long tiles) {
+  if (tiles <= 0) return cudaSuccess;
+  Maps maps;
+  if (!make_maps(g.p, &maps)) return cudaErrorInvalidValue;
+  constexpr uint32_t stage = 2 * kBox + kTileN / CG / 64 * kBox;
+  const int stages = (kSmemMax - 1024 - kBarBytes) / (int)stage;
+  const size_t smem = 1024 + kBarBytes + (size_t)stages * stage;
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e == cudaSuccess) e = raise_smem_limit((const void*)loss_product<MODE, CG>, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, std::max(1, sms / CG)) * CG);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = g.p.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, loss_product<MODE, CG>, maps, g, stages);
+}
+
+// Single CTAs (128-row tiles) when the rows fit one tile, pairs (256) otherwise.
+bool single(int T) { return T <= kTileM; }
+
+int row_tiles(int T) { return (T + 255) / 256; }   // (one tile of either height up to 128)
+
+}  // namespace
+
+// Splits of the vocabulary for dX.  A unit costs its K-blocks and about 12 K-blocks' time
+// for filling the pipeline and writing its partial result; the CTAs take the units in
+// waves.  The count with the least total is taken.
+int loss_tc_splits(int T, int H, int r, int cols) {
+  const long long tiles = (long long)row_tiles(T) * ((H + kTileN - 1) / kTileN +
+                                                     (r + kTileN - 1) / kTileN);
+  const int units = single(T) ? 152 : 76, nkb = (cols + kBlockK - 1) / kBlockK;
+  int best = 1;
+  double best_cost = 1e30;
+  for (int s = 1; s <= 64 && s * 8 <= std::max(8, nkb); ++s) {
+    const double cost = (double)((tiles * s + units - 1) / units) * ((double)nkb / s + 12.0);
+    if (cost < best_cost * 0.999) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats, bool store) {
+  TcArgs g{};
+  g.p = p;
+  g.v0 = v0;
+  g.v1 = v1;
+  g.want = stats ? kWantStats | (store ? kWantGap : 0) : kWantGrad;
+  const long long tiles = (long long)row_tiles(p.T) * ((v1 - v0 + kTileN - 1) / kTileN);
+  return single(p.T) ? launch<kLogits, 1>(g, tiles) : launch<kLogits, 2>(g, tiles);
+}
+
+cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first) {
+  TcArgs g{};
+  g.p = p;
+  g.v0 = v0;
+  g.v1 = v1;
+  g.first = first;
+  g.n_head = p.d_hidden ? (p.Hp + kTileN - 1) / kTileN : 0;
+  g.n_markov = p.d_w1 ? (p.rp + kTileN - 1) / kTileN : 0;
+  const long long tiles = (long long)row_tiles(p.T) * (g.n_head + g.n_markov) * p.splits;
+  return single(p.T) ? launch<kDx, 1>(g, tiles) : launch<kDx, 2>(g, tiles);
+}
+
+cudaError_t launch_loss_dw_tc(const LossPlan& p, int v0, int v1) {
+  TcArgs g{};
+  g.p = p;
+  g.v0 = v0;
+  g.v1 = v1;
+  g.n_head = p.d_lm_head ? (p.Hp + kTileN - 1) / kTileN : 0;
+  g.n_markov = p.d_w2 ? (p.rp + kTileN - 1) / kTileN : 0;
+  const long long tiles = (long long)((v1 - v0 + 255) / 256) * (g.n_head + g.n_markov);
+  return launch<kDw, 2>(g, tiles);
+}
+
+}  // namespace dspark

@@ -9,6 +9,7 @@
 // product z = X . [lm_head | markov_w2^T]^T and its gradients are columns of the others'.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -44,35 +45,74 @@ struct LossPlan {
                                       // the inverse or -1
   int* vchunk;                        // counts per chunk of the bias
   float* biasc;                       // [Vh] bias of the compact head rows
+  void *wc, *w2c;                     // bf16 bias form: the compact head [Vh][H], [r][Vh]
+                                      // (zeros up to a multiple of 256 rows past n_voc)
   void* x;                            // [Tp][Kx]
   float2* stat;                       // [Tp][n_stat] per vocabulary tile: the maximum of
                                       // z, and the sum of exp(z - maximum)
   int n_stat, stat_cols;
   float *zlab, *lse;                  // [Tp]
-  void* q;                            // [Tp][ldq]
+  void* q;                            // [Tp][ldq]; fp32: logits, then their gradient; bf16:
+                                      // the logits' distances from their tile's maximum
+                                      // (16 bits, loss_gap), then the gradient
   size_t ldq;
   int pieces, piece_cols;             // pieces of the vocabulary, columns of each
+  float* qres;                        // [Tp] bf16: what rounding the label's entry of q lost
   float* dxp;                         // [splits][Tp][Kx] partial gradients of X
   int splits;
   bool grads;                         // any gradient asked for
   cudaStream_t stream;
 };
 
+// The label's entry of row i of q, rounded to bf16; what the rounding lost is kept for the
+// gradient of X (this entry, about -w, makes up most of it).
+__device__ __forceinline__ float loss_label_grad(const LossPlan& p, int i, float x) {
+  const float b = __bfloat162float(__float2bfloat16(x));
+  p.qres[i] = x - b;
+  return b;
+}
+
 // compact -> head row, for kernels that read the head's own arrays
 __device__ __forceinline__ int loss_head_row(const LossPlan& p, int j) {
   return p.vlist ? p.vlist[j] : j;
 }
 
+// A logit's distance d >= 0 below its tile's maximum in 16 bits: steps of 1 / 896, so that a
+// probability is off by at most 0.06% (a bf16 rounding: 0.39%) down to e^-73 of the tile's
+// largest, below every fp32 gradient that sums to anything; kLossFar from there on (and for
+// anything that is not a number).
+constexpr float kLossSteps = 896.f;
+constexpr uint32_t kLossFar = 0xFFFFu;
+__device__ __forceinline__ uint32_t loss_gap(float d) {
+  // adding 2^23 rounds to an integer and leaves it in the low bits
+  const float t = fminf(fmaf(d, kLossSteps, 8388608.f), 8388608.f + 65535.f);
+  return __float_as_uint(t) & 0xFFFFu;
+}
+// scale * exp(-distance), given log2(scale)
+__device__ __forceinline__ float loss_gap_exp(uint32_t gap, float log2_scale) {
+  const float d = __uint_as_float(0x4B000000u | gap) - 8388608.f;
+  const float e = exp2f(fmaf(d, -1.44269504f / kLossSteps, log2_scale));
+  return gap == kLossFar ? 0.f : e;
+}
+
 // k_loss_rows.cu: everything but the products
 cudaError_t launch_loss_plan(const LossPlan& p);         // compaction, X, zeroed outputs
 cudaError_t launch_loss_rows(const LossPlan& p);         // lse, losses, total
-cudaError_t launch_loss_dz(const LossPlan& p, int v0, int v1);   // q from stored logits
+cudaError_t launch_loss_dz(const LossPlan& p, int v0, int v1);   // q from what is stored
 cudaError_t launch_loss_dx(const LossPlan& p);           // d_hidden and d_w1 from dxp
 
-// k_loss_simt.cu: the products on the CUDA cores
+// the products of columns [v0, v1) of the compact vocabulary.  Logits: with `stats` their
+// statistics, and with `store` what launch_loss_dz needs; without `stats` q's input again
+// (fp32) or q itself (bf16).  dX: `first` overwrites dxp, otherwise it is added to.
+// k_loss_simt.cu (fp32, on the CUDA cores)
 int loss_simt_splits(int T, int Kx, int cols);
 cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stats, bool store);
 cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first);
 cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1);
+// k_loss_tc.cu (bf16, on the tensor cores)
+int loss_tc_splits(int T, int H, int r, int cols);
+cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats, bool store);
+cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first);
+cudaError_t launch_loss_dw_tc(const LossPlan& p, int v0, int v1);
 
 }  // namespace dspark
