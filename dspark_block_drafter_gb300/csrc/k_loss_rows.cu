@@ -252,11 +252,10 @@ __global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
   }
 }
 
-// The compact head of a bias-form bf16 head with masked rows: its rows and its columns of
-// markov_w2, then zeros up to a multiple of 256.
+// The compact head of a bias-form bf16 head: its rows and its columns of markov_w2, then
+// zeros up to a multiple of 256.
 __global__ void __launch_bounds__(256) loss_gather_head(const LossPlan p) {
   const int n = (int)p.ctrl[kLossVoc];
-  if (n >= p.Vh) return;
   const int end = min(p.Vh, (n + 255) / 256 * 256), per = p.H / 8;
   const uint4* w = (const uint4*)p.lm_head;
   uint4* wc = (uint4*)p.wc;

@@ -6,9 +6,9 @@
 //
 // i: compact rows, j: compact head rows, c: columns of X.  One kernel form does all three:
 // a 128 (or, for a CTA pair, 256) x 256 tile of the result accumulates in TMEM over K-blocks
-// of 64.  Every operand comes in boxes of 64 x 64 elements straight from the array it lies
-// in, whichever of its two indices is contiguous: the box is a swizzled K-major tile when
-// that index is K and an MN-major one when it is not, and the matrix descriptors say which.
+// of 64.  Every operand comes by TMA straight from the array it lies in, 64 elements of its
+// contiguous index wide: a swizzled K-major tile when that index is K, a row of 64 x 64
+// MN-major tiles when it is not, and the matrix descriptors say which.
 // So no operand is ever transposed in memory, and the Markov term is nothing but some more
 // K-blocks (logits) or columns (gradients), read from markov_w1's gathered rows and from
 // markov_w2 as they are.
@@ -19,7 +19,7 @@
 //
 // The tensor core cuts each partial sum of an accumulator toward zero, so a long sum drifts:
 // over K = 4352 the losses were off by 5e-6.  The logits' accumulator is therefore read
-// every 512 of K and the parts are added in fp32 registers (which hold the tile's 128
+// every 768 of K and the parts are added in fp32 registers (which hold the tile's 128
 // columns of a row until it is complete).  The gradients, rounded to bf16, need no such care.
 //
 // The logits are never stored.  Their epilogue has one row per thread: it takes the maximum
@@ -32,6 +32,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -43,10 +44,10 @@ namespace dspark {
 namespace {
 
 constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;
-constexpr uint32_t kBox = 64 * 64 * 2;               // bytes of one operand box
+constexpr uint32_t kBox = 64 * 64 * 2;               // bytes of 64 rows of 64 elements
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
-constexpr int kSumBlocks = 8;                        // K-blocks of one part of a logit's sum
+constexpr int kSumBlocks = 12;                       // K-blocks of one part of a logit's sum
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kBarBytes = 512;
 constexpr long long kWaitBudget = 2000000000ll;      // ~1 s of SM clocks
@@ -56,8 +57,11 @@ enum : int { kLogits = 0, kDx = 1, kDw = 2 };
 // maximum, or (with the log-sum-exp known) the gradient of the logits
 enum : int { kWantStats = 1, kWantGap = 2, kWantGrad = 4 };
 
+// The operands as a product reads them: A, B, and the Markov part's B.  K-major ones in one
+// box a K-block, MN-major ones in one box of several 64-column chunks (or, where rows are
+// not whole chunks, in one box for each chunk).
 struct Maps {
-  CUtensorMap x, q, w[2], w2[2];       // [1]: the compacted vocabulary of a bias-form head
+  CUtensorMap a, b, b2;
 };
 
 struct TcArgs {
@@ -66,6 +70,7 @@ struct TcArgs {
   int want;            // kWant...
   int first;           // dX: the first piece (later ones add)
   int n_head, n_markov;  // 256-column tiles of X's two parts that are computed
+  int chunked;         // dX: lm_head rows are whole 64-column chunks
 };
 
 // One unit of work: a tile of the result and a range of K-blocks.
@@ -129,12 +134,21 @@ __device__ __forceinline__ bool column_tile(const TcArgs& g, int n, int* c0) {
 }
 
 template <int CG>
-__device__ __forceinline__ void load_box(uint8_t* dst, const CUtensorMap* m, uint64_t* bar,
-                                         uint32_t bar_leader, int x, int y) {
+__device__ __forceinline__ void load_2d(uint8_t* dst, const CUtensorMap* m, uint64_t* bar,
+                                        uint32_t bar_leader, int x, int y) {
   if (CG == 2)
     ptx::tma_load_2d_pair(dst, m, bar_leader, x, y);
   else
     ptx::tma_load_2d(dst, m, bar, x, y);
+}
+// columns [64 chunk, ...) of rows y ...
+template <int CG>
+__device__ __forceinline__ void load_chunks(uint8_t* dst, const CUtensorMap* m, uint64_t* bar,
+                                            uint32_t bar_leader, int y, int chunk) {
+  if (CG == 2)
+    ptx::tma_load_3d_pair(dst, m, bar_leader, 0, y, chunk);
+  else
+    ptx::tma_load_3d(dst, m, bar, 0, y, chunk);
 }
 
 template <int MODE, int CG>
@@ -187,7 +201,6 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
   const uint32_t full0 = CG == 2 ? ptx::mapa_shared(ptx::smem_u32(full), 0) : 0;
   const uint32_t acc_empty0 = CG == 2 ? ptx::mapa_shared(ptx::smem_u32(acc_empty), 0) : 0;
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc];
-  const int compact = n_voc < p.Vh ? 1 : 0;            // (Vh rows: the head itself)
   const int units = unit_count<MODE, CG>(g, n_tok, n_voc);
   const int u0 = blockIdx.x / CG, step = gridDim.x / CG;
 
@@ -198,60 +211,76 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
 
   if (warp == kEpiWarps) {
     // ---------------------------------------------------------------- producer
+    // One thread issues every copy: what it does for a K-block has to take less time than
+    // the block's MMAs (about 600 clocks).  With four 8 KB copies a block and the choice of
+    // operands inside the loop, it bounded the logits and dX at 60% of the tensor pipe.
     if (lane == 0) {
       uint32_t it = 0, s = 0, ph = 0;
       bool ok = true;
-      const int hb = p.Hp / kBlockK;
-      const CUtensorMap* mw = &maps.w[compact];
-      const CUtensorMap* mw2 = &maps.w2[compact];
-      for (int u = u0; u < units && ok; u += step) {
-        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc);
-        const int ma = t.m + (int)rank * kTileM;             // this CTA's rows of M
-        const int half = (int)rank * (kTileN / CG);          // and its share of N
-        int c0 = 0;
-        bool markov = false;
-        if (MODE != kLogits) markov = column_tile(g, t.n, &c0);
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+      auto run = [&](int kb0, int kb1, auto fill) {
+        for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
           if (!ptx::mbar_wait(&empty[s], ph ^ 1, kWaitBudget, abort_flag)) {
             ok = false;
-            break;
+            return;
           }
-          uint8_t* a = smem + (size_t)s * kStage;
-          uint8_t* b = a + kStageA;
-          const uint32_t bar = full0 + s * 8;
           if (leader) ptx::mbar_arrive_expect_tx(&full[s], CG * kStage);
-          const int k = kb * kBlockK;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (MODE == kLogits)
-              load_box<CG>(a + j * kBox, &maps.x, &full[s], bar, k, ma + 64 * j);
-            else if (MODE == kDx)
-              load_box<CG>(a + j * kBox, &maps.q, &full[s], bar, k, ma + 64 * j);
-            else
-              load_box<CG>(a + j * kBox, &maps.q, &full[s], bar, ma + 64 * j, k);
-          }
-#pragma unroll
-          for (int j = 0; j < kBoxB; ++j) {
-            const int n = half + 64 * j;
-            if (MODE == kLogits) {
-              const int v = g.v0 + t.n * kTileN + n;
-              if (kb < hb)
-                load_box<CG>(b + j * kBox, mw, &full[s], bar, k, v);
-              else
-                load_box<CG>(b + j * kBox, mw2, &full[s], bar, v, k - p.Hp);
-            } else if (MODE == kDx) {
-              if (!markov)
-                load_box<CG>(b + j * kBox, mw, &full[s], bar, c0 + n, g.v0 + k);
-              else
-                load_box<CG>(b + j * kBox, mw2, &full[s], bar, g.v0 + k, c0 - p.Hp + n);
-            } else {
-              load_box<CG>(b + j * kBox, &maps.x, &full[s], bar, c0 + n, k);
-            }
-          }
+          uint8_t* a = smem + (size_t)s * kStage;
+          fill(kb * kBlockK, a, a + kStageA, &full[s], full0 + s * 8);
           if (++s == (uint32_t)stages) {
             s = 0;
             ph ^= 1;
           }
+        }
+      };
+      for (int u = u0; u < units && ok; u += step) {
+        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc);
+        const int ma = t.m + (int)rank * kTileM;             // this CTA's rows of M
+        const int half = (int)rank * (kTileN / CG);          // and its share of N
+        if (MODE == kLogits) {
+          const int v = g.v0 + t.n * kTileN + half, hb = p.Hp / kBlockK;
+          run(t.kb0, hb, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
+            load_2d<CG>(a, &maps.a, bar, lead, k, ma);
+            load_2d<CG>(b, &maps.b, bar, lead, k, v);
+          });
+          run(hb, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
+            load_2d<CG>(a, &maps.a, bar, lead, k, ma);
+#pragma unroll
+            for (int j = 0; j < kBoxB; ++j)
+              load_2d<CG>(b + j * kBox, &maps.b2, bar, lead, v + 64 * j, k - p.Hp);
+          });
+        } else if (MODE == kDx) {
+          int c0;
+          const bool markov = column_tile(g, t.n, &c0);
+          const int v0 = g.v0;
+          if (markov) {
+            const int c = c0 - p.Hp + half;
+            run(t.kb0, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
+              load_2d<CG>(a, &maps.a, bar, lead, k, ma);
+              load_2d<CG>(b, &maps.b2, bar, lead, v0 + k, c);
+            });
+          } else if (g.chunked) {
+            const int c = (c0 + half) / 64;
+            run(t.kb0, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
+              load_2d<CG>(a, &maps.a, bar, lead, k, ma);
+              load_chunks<CG>(b, &maps.b, bar, lead, v0 + k, c);
+            });
+          } else {
+            const int c = c0 + half;
+            run(t.kb0, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
+              load_2d<CG>(a, &maps.a, bar, lead, k, ma);
+#pragma unroll
+              for (int j = 0; j < kBoxB; ++j)
+                load_2d<CG>(b + j * kBox, &maps.b, bar, lead, c + 64 * j, v0 + k);
+            });
+          }
+        } else {
+          int c0;
+          column_tile(g, t.n, &c0);
+          const int ca = ma / 64, cb = (c0 + half) / 64;
+          run(t.kb0, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
+            load_chunks<CG>(a, &maps.a, bar, lead, k, ca);
+            load_chunks<CG>(b, &maps.b, bar, lead, k, cb);
+          });
         }
       }
       if (!ok) {
@@ -273,56 +302,72 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
     if (lane == 0 && leader) {
       uint32_t s = 0, ph = 0, local = 0;
       bool ok = true;
-      const int hb = p.Hp / kBlockK;
       const uint32_t base = ptx::smem_u32(smem);
+      uint32_t d = 0, accum = 0;
+      auto run = [&](auto a_mn_c, auto b_mn_c, int blocks) {
+        constexpr bool a_mn = decltype(a_mn_c)::value, b_mn = decltype(b_mn_c)::value;
+        constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTileM * CG, kTileN, a_mn, b_mn);
+        const uint64_t da0 = a_mn ? ptx::desc_mnmajor_sw128(base, kBox, 1024)
+                                  : ptx::desc_kmajor_sw128(base);
+        const uint64_t db0 = b_mn ? ptx::desc_mnmajor_sw128(base + kStageA, kBox, 1024)
+                                  : ptx::desc_kmajor_sw128(base + kStageA);
+        // 16 deep: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
+        constexpr uint32_t sa = a_mn ? 128 : 2, sb = b_mn ? 128 : 2;
+        for (int q = 0; q < blocks; ++q) {
+          if (!ptx::mbar_wait(&full[s], ph, kWaitBudget, abort_flag)) {
+            ok = false;
+            return;
+          }
+          ptx::tc_fence_after();
+          const uint64_t da = da0 + s * (kStage / 16), db = db0 + s * (kStage / 16);
+#pragma unroll
+          for (int k = 0; k < kBlockK / 16; ++k) {
+            if (CG == 2)
+              ptx::mma_f16_pair(d, da + k * sa, db + k * sb, idesc, k == 0 ? accum : 1u);
+            else
+              ptx::mma_f16(d, da + k * sa, db + k * sb, idesc, k == 0 ? accum : 1u);
+          }
+          accum = 1u;
+          if (CG == 2)
+            ptx::mma_commit_pair_multicast(&empty[s], 0x3);
+          else
+            ptx::mma_commit(&empty[s]);
+          if (++s == (uint32_t)stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      };
+      using Mn = std::true_type;
+      using K = std::false_type;
       for (int u = u0; u < units; u += step) {
         const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc);
         int c0 = 0;
-        bool b_mn = true;                       // dW; dX of the head's columns
-        if (MODE == kDx) b_mn = !column_tile(g, t.n, &c0);
-        constexpr bool a_mn = MODE == kDw;
+        const bool markov = MODE != kLogits && column_tile(g, t.n, &c0);
         for (int kb = t.kb0, part = 0; part == 0 || kb < t.kb1; ++part, ++local) {
-          const int part_end = MODE == kLogits ? min(t.kb1, kb + kSumBlocks) : t.kb1;
+          const int end = MODE == kLogits ? min(t.kb1, kb + kSumBlocks) : t.kb1;
           const uint32_t acc = local & 1, aph = (local >> 1) & 1;
           if (!ptx::mbar_wait(&acc_empty[acc], aph ^ 1, kWaitBudget, abort_flag)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t d = tmem + acc * kTileN;
-          uint32_t accum = 0u;
-          for (; kb < part_end; ++kb) {
-            if (!ptx::mbar_wait(&full[s], ph, kWaitBudget, abort_flag)) {
-              ok = false;
-              break;
-            }
-            ptx::tc_fence_after();
-            if (MODE == kLogits) b_mn = kb >= hb;
-            const uint32_t idesc = ptx::idesc_bf16_f32(kTileM * CG, kTileN, a_mn, b_mn);
-            const uint32_t a0 = base + s * kStage, b0 = a0 + kStageA;
-            const uint64_t da = a_mn ? ptx::desc_mnmajor_sw128(a0, kBox, 1024)
-                                     : ptx::desc_kmajor_sw128(a0);
-            const uint64_t db = b_mn ? ptx::desc_mnmajor_sw128(b0, kBox, 1024)
-                                     : ptx::desc_kmajor_sw128(b0);
-            // 16 deep: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
-            const uint32_t sa = a_mn ? 128 : 2, sb = b_mn ? 128 : 2;
-#pragma unroll
-            for (int k = 0; k < kBlockK / 16; ++k) {
-              if (CG == 2)
-                ptx::mma_f16_pair(d, da + k * sa, db + k * sb, idesc, accum);
-              else
-                ptx::mma_f16(d, da + k * sa, db + k * sb, idesc, accum);
-              accum = 1u;
-            }
-            if (CG == 2)
-              ptx::mma_commit_pair_multicast(&empty[s], 0x3);
+          d = tmem + acc * kTileN;
+          accum = 0u;
+          if (MODE == kLogits) {
+            // lm_head, then markov_w2
+            const int head = max(0, min(end, p.Hp / kBlockK) - kb);
+            run(K{}, K{}, head);
+            if (ok) run(K{}, Mn{}, end - kb - head);
+          } else if (MODE == kDx) {
+            if (markov)
+              run(K{}, K{}, end - kb);
             else
-              ptx::mma_commit(&empty[s]);
-            if (++s == (uint32_t)stages) {
-              s = 0;
-              ph ^= 1;
-            }
+              run(K{}, Mn{}, end - kb);
+          } else {
+            run(Mn{}, Mn{}, end - kb);
           }
+          kb = end;
           if (!ok) break;
           if (CG == 2)
             ptx::mma_commit_pair_multicast(&acc_full[acc], 0x3);
@@ -479,7 +524,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
         } else {
           const int j0 = g.v0 + m;                            // compact head row
           const bool live = j0 < min(g.v1, n_voc);
-          const size_t row = live ? (size_t)(compact ? p.vlist[j0] : j0) : 0;
+          const size_t row = live ? (size_t)loss_head_row(p, j0) : 0;
           const int width = min(128, markov ? p.r - (c0 - p.Hp) : p.H - c0);
 #pragma unroll 1
           for (int c = 0; c < width; c += 32) {
@@ -544,29 +589,54 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A [rows][ld] bf16 array, `cols` of each row in use, read in 64 x 64 boxes (zeros outside).
-bool encode_map(CUtensorMap* m, const void* base, size_t cols, size_t rows, size_t ld) {
+// A [rows][ld] bf16 array, `cols` of each row in use, read 64 columns x `high` rows at a time
+// (zeros outside).
+bool map_2d(CUtensorMap* m, const void* base, size_t cols, size_t rows, size_t ld, int high) {
   auto encode = encode_fn();
   if (!encode) return false;
   cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
-  cuuint32_t box[2] = {64, 64}, es[2] = {1, 1};
+  cuuint32_t box[2] = {64, (cuuint32_t)high}, es[2] = {1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void*)base, dims, strides, box, es,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_maps(const LossPlan& p, Maps* m) {
-  bool ok = encode_map(&m->x, p.x, p.Kx, p.Tp, p.Kx);
-  ok = ok && encode_map(&m->w[0], p.lm_head, p.H, p.Vh, p.H);
-  ok = ok && encode_map(&m->w[1], p.wc ? p.wc : p.lm_head, p.H, p.Vh, p.H);
-  m->w2[0] = m->w2[1] = m->w[0];
-  if (p.r > 0) {
-    ok = ok && encode_map(&m->w2[0], p.w2, p.Vh, p.r, p.Vh);
-    ok = ok && encode_map(&m->w2[1], p.w2c ? p.w2c : p.w2, p.Vh, p.r, p.Vh);
+// The same as (64 columns, row, chunk of 64 columns), read 64 rows x `chunks` chunks at a
+// time; rows are whole chunks.
+bool map_chunks(CUtensorMap* m, const void* base, size_t cols, size_t rows, int chunks) {
+  auto encode = encode_fn();
+  if (!encode || cols % 64) return false;
+  cuuint64_t dims[3] = {64, rows, cols / 64}, strides[2] = {cols * 2, 128};
+  cuuint32_t box[3] = {64, 64, (cuuint32_t)chunks}, es[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)base, dims, strides, box, es,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int CG>
+bool make_maps(const TcArgs& g, Maps* m) {
+  const LossPlan& p = g.p;
+  constexpr int share = kTileN / CG;                   // rows of N a CTA stages
+  const void* w = p.wc ? p.wc : p.lm_head;
+  const void* w2 = p.wc ? p.w2c : p.w2;
+  bool ok;
+  if (MODE == kLogits) {
+    ok = map_2d(&m->a, p.x, p.Kx, p.Tp, p.Kx, kTileM) && map_2d(&m->b, w, p.H, p.Vh, p.H, share);
+    m->b2 = m->b;
+    if (p.r > 0) ok = ok && map_2d(&m->b2, w2, p.Vh, p.r, p.Vh, 64);
+  } else if (MODE == kDx) {
+    ok = map_2d(&m->a, p.q, p.ldq, p.Tp, p.ldq, kTileM) &&
+         (g.chunked ? map_chunks(&m->b, w, p.H, p.Vh, share / 64)
+                    : map_2d(&m->b, w, p.H, p.Vh, p.H, 64));
+    m->b2 = m->b;
+    if (p.r > 0) ok = ok && map_2d(&m->b2, w2, p.Vh, p.r, p.Vh, share);
+  } else {
+    ok = map_chunks(&m->a, p.q, p.ldq, p.Tp, kTileM / 64) &&
+         map_chunks(&m->b, p.x, p.Kx, p.Tp, share / 64);
+    m->b2 = m->b;
   }
-  m->q = m->x;
-  if (p.q) ok = ok && encode_map(&m->q, p.q, p.ldq, p.Tp, p.ldq);
   return ok;
 }
 
@@ -574,7 +644,7 @@ template <int MODE, int CG>
 cudaError_t launch(const TcArgs& g, long long tiles) {
   if (tiles <= 0) return cudaSuccess;
   Maps maps;
-  if (!make_maps(g.p, &maps)) return cudaErrorInvalidValue;
+  if (!make_maps<MODE, CG>(g, &maps)) return cudaErrorInvalidValue;
   constexpr uint32_t stage = 2 * kBox + kTileN / CG / 64 * kBox;
   const int stages = (kSmemMax - 1024 - kBarBytes) / (int)stage;
   const size_t smem = 1024 + kBarBytes + (size_t)stages * stage;
@@ -639,6 +709,7 @@ cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first) {
   g.v0 = v0;
   g.v1 = v1;
   g.first = first;
+  g.chunked = p.H % 64 == 0;
   g.n_head = p.d_hidden ? (p.Hp + kTileN - 1) / kTileN : 0;
   g.n_markov = p.d_w1 ? (p.rp + kTileN - 1) / kTileN : 0;
   const long long tiles = (long long)row_tiles(p.T) * (g.n_head + g.n_markov) * p.splits;

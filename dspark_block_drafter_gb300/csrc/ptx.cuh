@@ -403,7 +403,7 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t smem_addr, uint3
 // Instruction descriptor of kind::f16 with bf16 A and B, fp32 D.
 // a_mn / b_mn select MN-major operands; M in {64, 128, 256}, N a multiple of 8 (16 for
 // M = 128) up to 256.
-__host__ __device__ __forceinline__ uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {
+__host__ __device__ constexpr __forceinline__ uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {
   return (1u << 4)                      // D format: f32
          | (1u << 7)                    // A format: bf16
          | (1u << 10)                   // B format: bf16
