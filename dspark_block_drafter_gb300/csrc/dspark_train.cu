@@ -62,8 +62,8 @@ static dspark_status validate_loss(const dspark_loss_config* c, const dspark_hea
       return fail(DSPARK_ERR_UNSUPPORTED, "bf16 path needs V_head % 8 == 0 (16-byte rows)");
     if (!aligned(h->lm_head, 16) || (c->r > 0 && !aligned(h->markov_w2, 16)))
       return fail(DSPARK_ERR_INVALID_ARG, "bf16 weights must be 16-byte aligned");
-    if (!aligned(o->d_lm_head, 16))
-      return fail(DSPARK_ERR_INVALID_ARG, "bf16 d_lm_head must be 16-byte aligned");
+    if (!aligned(o->d_lm_head, 16) || !aligned(o->d_markov_w1, 16) || !aligned(o->d_markov_w2, 16))
+      return fail(DSPARK_ERR_INVALID_ARG, "bf16 weight gradients must be 16-byte aligned");
   }
   return DSPARK_OK;
 }
@@ -137,6 +137,15 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
                      : loss_simt_splits(p->T, p->Kx, p->piece_cols);
       p->dxp = (float*)take(sizeof(float) * p->splits * Tp * p->Kx);
     }
+  }
+  auto zero = [&](void* g, size_t bytes, const int32_t* keep, size_t row_bytes) {
+    if (g) p->zero[p->n_zero++] = {(char*)g, bytes, keep, (int)row_bytes};
+  };
+  zero(p->d_w1, es * c->V * c->r, nullptr, 0);
+  if (h->lm_bias) {
+    // (fp32: all of it, by a memset)
+    zero(p->d_lm_head, es * Vh * c->H, tc ? p->vinv : nullptr, es * c->H);
+    zero(p->d_w2, es * Vh * c->r, nullptr, 0);
   }
   return off;
 }

@@ -3,7 +3,9 @@
 // total, and the gradients that are sums over rows of X's gradient.
 //
 // Every kernel here is bound by its traffic or its latency; sums over rows are taken in a
-// fixed order, in fp64 where they join many values.
+// fixed order.  Sums of many values carry their rounding errors along in a second fp32 value:
+// fp64 additions run at a few per clock and SM here (with them the compaction alone took
+// 16 us for a handful of rows).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -27,18 +29,72 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16(x);
 }
 
-// Sum over a CTA of up to 1024 threads, in a fixed order; every thread gets it.
-template <typename S>
-__device__ __forceinline__ S block_sum(S v, S* s_warp) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = (blockDim.x + 31) / 32;
+// An fp32 sum that carries its rounding errors along (Knuth's two-sum).
+struct Sum2 {
+  float s = 0.f, c = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, b = t - s;
+    c += (s - (t - b)) + (x - b);
+    s = t;
+  }
+  __device__ __forceinline__ void add(const Sum2& o) {
+    add(o.s);
+    c += o.c;
+  }
+  __device__ __forceinline__ float value() const { return s + c; }
+};
+
+__device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    Sum2 u;
+    u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
+    u.c = __shfl_xor_sync(0xFFFFFFFFu, v.c, o);
+    v.add(u);
+  }
+  return v;
+}
+
+// Sum over a CTA, in a fixed order; lane 0 of warp 0 gets it.
+__device__ __forceinline__ Sum2 block_sum(Sum2 v, float2* s_warp) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  v = warp_sum(v);
+  if (lane == 0) s_warp[warp] = make_float2(v.s, v.c);
   __syncthreads();
-  if (lane == 0) s_warp[warp] = v;
-  __syncthreads();
-  S t = 0;
-  for (int w = 0; w < warps; ++w) t += s_warp[w];
-  return t;
+  Sum2 u;
+  if (warp == 0) {
+    if (lane < warps) {
+      u.s = s_warp[lane].x;
+      u.c = s_warp[lane].y;
+    }
+    u = warp_sum(u);
+  }
+  return u;
+}
+
+// Copies n elements, sixteen bytes at a time where both sides allow it.
+template <typename E>
+__device__ __forceinline__ void copy_row(E* dst, const E* src, int n) {
+  constexpr int kVec = 16 / sizeof(E);
+  int at = 0;
+  if ((((uintptr_t)dst | (uintptr_t)src) & 15) == 0) {
+    at = n / kVec * kVec;
+    for (int k = threadIdx.x; k < n / kVec; k += blockDim.x)
+      reinterpret_cast<uint4*>(dst)[k] = reinterpret_cast<const uint4*>(src)[k];
+  }
+  for (int k = at + threadIdx.x; k < n; k += blockDim.x) dst[k] = src[k];
+}
+
+template <typename E>
+__device__ __forceinline__ void zero_row(E* dst, int n) {
+  constexpr int kVec = 16 / sizeof(E);
+  int at = 0;
+  if (((uintptr_t)dst & 15) == 0) {
+    at = n / kVec * kVec;
+    for (int k = threadIdx.x; k < n / kVec; k += blockDim.x)
+      reinterpret_cast<uint4*>(dst)[k] = make_uint4(0, 0, 0, 0);
+  }
+  for (int k = at + threadIdx.x; k < n; k += blockDim.x) dst[k] = from_f32<E>(0.f);
 }
 
 // Bias form: the compact vocabulary's size, inverse map and biases.  vinv is -1 before.
@@ -63,10 +119,18 @@ __global__ void __launch_bounds__(256) loss_vocab(const LossPlan p, int chunks) 
 __device__ __forceinline__ int loss_label_row(const LossPlan& p, int t) {
   int row = t;
   if (p.d2t) {
-    int lo = 0, hi = p.Vh;                    // first entry >= t
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (p.d2t[mid] < t) lo = mid + 1; else hi = mid;
+    // first entry >= t: seven probes at a time, since each is a trip to memory
+    int lo = 0, hi = p.Vh;
+    while (hi > lo) {
+      const int n = hi - lo;
+      int above = 0;                              // probes whose entry is below t
+#pragma unroll
+      for (int q = 1; q < 8; ++q) above += p.d2t[lo + (int)((long long)n * q / 8)] < t;
+      // entries lo + n q / 8 (q <= above) are below t, the next one is not
+      const int l = lo, h = hi;
+      if (above > 0) lo = l + (int)((long long)n * above / 8) + 1;
+      if (above < 7) hi = l + (int)((long long)n * (above + 1) / 8);
+      else hi = h;
     }
     if (lo >= p.Vh || p.d2t[lo] != t) return -1;
     row = lo;
@@ -74,61 +138,75 @@ __device__ __forceinline__ int loss_label_row(const LossPlan& p, int t) {
   return p.vinv ? p.vinv[row] : row;
 }
 
-// One CTA: compacts the rows that carry a loss, in order, and sums their weights.
+// One CTA: compacts the rows that carry a loss, in order, and sums their weights.  Each
+// thread takes kPlanRows rows of a sweep, so that their loads overlap.
+constexpr int kPlanRows = 4;
 __global__ void __launch_bounds__(kPlanThreads) loss_tokens(const LossPlan p) {
   __shared__ int s_cnt[32];
-  __shared__ double s_w[32];
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  if (tid < 64 && tid != kLossVoc) p.ctrl[tid] = 0;
-  if (tid == 64 && !p.vlist) p.ctrl[kLossVoc] = (uint32_t)p.Vh;
+  __shared__ float2 s_w[32];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, warps = blockDim.x / 32;
+  for (int c = tid; c < 64; c += blockDim.x)
+    if (c != kLossVoc) p.ctrl[c] = 0;
+  if (tid == 0 && !p.vlist) p.ctrl[kLossVoc] = (uint32_t)p.Vh;
   __syncthreads();
   int base = 0;
-  double wsum = 0.0;
-  for (int t0 = 0; t0 < p.T; t0 += kPlanThreads) {
-    const int t = t0 + tid;
-    int j = -1, pv = 0;
-    if (t < p.T) {
-      const int label = p.labels[t];
-      if (label >= p.V)
+  Sum2 wsum;
+  for (int t0 = 0; t0 < p.T; t0 += kPlanRows * blockDim.x) {
+    int j[kPlanRows], pv[kPlanRows];
+    float w[kPlanRows];
+#pragma unroll
+    for (int q = 0; q < kPlanRows; ++q) {
+      const int t = t0 + q * blockDim.x + tid;
+      j[q] = t < p.T ? p.labels[t] : -1;
+      pv[q] = t < p.T && p.r > 0 ? p.prev[t] : 0;
+      w[q] = t < p.T && p.weights ? p.weights[t] : 1.f;
+    }
+#pragma unroll
+    for (int q = 0; q < kPlanRows; ++q) {
+      if (j[q] >= p.V) {
         flag_error(p.ctrl, kErrBadToken);
-      else if (label >= 0)
-        j = loss_label_row(p, label);
-      if (j >= 0 && p.r > 0) {
-        pv = p.prev[t];
-        if (pv < 0 || pv >= p.V) {
-          flag_error(p.ctrl, kErrBadToken);
-          j = -1;
+        j[q] = -1;
+      }
+      if (j[q] >= 0) j[q] = loss_label_row(p, j[q]);
+      if (j[q] >= 0 && p.r > 0 && (pv[q] < 0 || pv[q] >= p.V)) {
+        flag_error(p.ctrl, kErrBadToken);
+        j[q] = -1;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kPlanRows; ++q) {
+      const int t = t0 + q * blockDim.x + tid;
+      const unsigned m = __ballot_sync(0xFFFFFFFFu, j[q] >= 0);
+      __syncthreads();
+      if (lane == 0) s_cnt[warp] = __popc(m);
+      __syncthreads();
+      int n = lane < warps ? s_cnt[lane] : 0;     // inclusive scan over the warps
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, n, o);
+        if (lane >= o) n += y;
+      }
+      const int all = __shfl_sync(0xFFFFFFFFu, n, 31);
+      const int before = warp > 0 ? __shfl_sync(0xFFFFFFFFu, n, warp - 1) : 0;
+      if (t < p.T) {
+        const int i = base + before + __popc(m & ((1u << lane) - 1));
+        p.pos[t] = j[q] >= 0 ? i : -1;
+        if (j[q] >= 0) {
+          p.tok[i] = t;
+          p.lab[i] = j[q];
+          p.prevc[i] = pv[q];
+          p.wrow[i] = w[q];
+          wsum.add(w[q]);
         }
       }
+      base += all;
     }
-    const unsigned m = __ballot_sync(0xFFFFFFFFu, j >= 0);
-    __syncthreads();
-    if (lane == 0) s_cnt[warp] = __popc(m);
-    __syncthreads();
-    int before = base, all = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += s_cnt[w];
-      all += s_cnt[w];
-    }
-    if (t < p.T) {
-      const int i = before + __popc(m & ((1u << lane) - 1));
-      p.pos[t] = j >= 0 ? i : -1;
-      if (j >= 0) {
-        const float w = p.weights ? p.weights[t] : 1.f;
-        p.tok[i] = t;
-        p.lab[i] = j;
-        p.prevc[i] = pv;
-        p.wrow[i] = w;
-        wsum += (double)w;
-      }
-    }
-    base += all;
   }
-  const double w = block_sum(wsum, s_w);
+  const float w = block_sum(wsum, s_w).value();
   if (tid == 0) {
     p.ctrl[kLossTok] = (uint32_t)base;
     float k = p.loss_scale;
-    if (p.reduction == 1) k = w > 0.0 ? (float)((double)p.loss_scale / w) : 0.f;
+    if (p.reduction == 1) k = w > 0.f ? p.loss_scale / w : 0.f;
     p.ctrl[kLossScale] = __float_as_uint(k);
     if (p.n_rows) *p.n_rows = base;
   }
@@ -138,62 +216,72 @@ __global__ void __launch_bounds__(kPlanThreads) loss_tokens(const LossPlan p) {
 // row t.
 template <typename E>
 __global__ void __launch_bounds__(256) loss_gather(const LossPlan p) {
-  const int t = blockIdx.x, tid = threadIdx.x;
+  const int t = blockIdx.x;
   E* x = (E*)p.x;
-  const E zero = from_f32<E>(0.f);
-  if (t >= (int)p.ctrl[kLossTok])
-    for (int k = tid; k < p.Kx; k += blockDim.x) x[(size_t)t * p.Kx + k] = zero;
+  if (t >= (int)p.ctrl[kLossTok]) zero_row(x + (size_t)t * p.Kx, p.Kx);
   if (t >= p.T) return;
   const int i = p.pos[t];
   if (i < 0) {
-    if (tid == 0) p.loss[t] = 0.f;
-    if (p.d_hidden)
-      for (int k = tid; k < p.H; k += blockDim.x) ((E*)p.d_hidden)[(size_t)t * p.H + k] = zero;
+    if (threadIdx.x == 0) p.loss[t] = 0.f;
+    if (p.d_hidden) zero_row((E*)p.d_hidden + (size_t)t * p.H, p.H);
     return;
   }
-  const E* h = (const E*)p.hidden + (size_t)t * p.H;
-  for (int k = tid; k < p.Hp; k += blockDim.x)
-    x[(size_t)i * p.Kx + k] = k < p.H ? h[k] : zero;
+  E* xi = x + (size_t)i * p.Kx;
+  copy_row(xi, (const E*)p.hidden + (size_t)t * p.H, p.H);
+  if (p.H < p.Hp) zero_row(xi + p.H, p.Hp - p.H);
   if (p.rp) {
-    const E* w = (const E*)p.w1 + (size_t)p.prevc[i] * p.r;
-    for (int k = tid; k < p.rp; k += blockDim.x)
-      x[(size_t)i * p.Kx + p.Hp + k] = k < p.r ? w[k] : zero;
+    copy_row(xi + p.Hp, (const E*)p.w1 + (size_t)p.prevc[i] * p.r, p.r);
+    if (p.r < p.rp) zero_row(xi + p.Hp + p.r, p.rp - p.r);
   }
 }
 
 // CTA i: joins row i's statistics over the vocabulary tiles into its log-sum-exp and its
 // loss; the last CTA to finish sums the losses.
-__global__ void __launch_bounds__(128) loss_rows(const LossPlan p) {
-  __shared__ float s_f[32];
-  __shared__ double s_d[32];
+constexpr int kRowsThreads = 256;
+__global__ void __launch_bounds__(kRowsThreads) loss_rows(const LossPlan p) {
+  __shared__ float2 s_w[32];
   __shared__ bool s_last;
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc];
   const int i = blockIdx.x, tid = threadIdx.x;
   if (i < n_tok) {
     const int n = (n_voc + p.stat_cols - 1) / p.stat_cols;
     const float2* st = p.stat + (size_t)i * p.n_stat;
-    // running maximum and sum; a tile whose logits are all -inf has sum 0
+    // running maximum and sum over sweeps of eight tiles a thread (a maximum of -inf: all
+    // its logits are, and its sum is 0)
     float m = -INFINITY, s = 0.f;
-    for (int j = tid; j < n; j += blockDim.x) {
-      const float2 a = st[j];
-      const float mm = fmaxf(m, a.x);
-      if (mm > -INFINITY) s = s * __expf(m - mm) + a.y * __expf(a.x - mm);
-      else s += a.y;
+    for (int j0 = tid; j0 < n; j0 += 8 * kRowsThreads) {
+      float2 a[8];
+      float mm = m;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int j = j0 + q * kRowsThreads;
+        a[q] = j < n ? st[j] : make_float2(-INFINITY, 0.f);
+        mm = fmaxf(mm, a[q].x);
+      }
+      const float ref = mm > -INFINITY ? mm : 0.f;
+      s *= __expf(m - ref);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += a[q].y * __expf(a[q].x - ref);
       m = mm;
     }
+    // joined over the CTA: the maxima, then the sums at the common maximum
     float mx = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    if (tid % 32 == 0) s_f[tid / 32] = mx;
+    if (tid % 32 == 0) s_w[tid / 32].x = mx;
     __syncthreads();
-    mx = s_f[0];
-    for (int w = 1; w < (int)blockDim.x / 32; ++w) mx = fmaxf(mx, s_f[w]);
-    if (mx > -INFINITY) s *= expf(m - mx);
-    const double sum = block_sum((double)s, s_d);
+    mx = s_w[0].x;
+#pragma unroll
+    for (int w = 1; w < kRowsThreads / 32; ++w) mx = fmaxf(mx, s_w[w].x);
+    const float ref = mx > -INFINITY ? mx : 0.f;
+    Sum2 v;
+    v.s = s * __expf(m - ref);
+    __syncthreads();
+    const Sum2 sum = block_sum(v, s_w);
     if (tid == 0) {
-      const float lse = (float)((double)mx + log(sum));
-      p.lse[i] = lse;
-      p.loss[p.tok[i]] = (float)((double)mx + log(sum) - (double)p.zlab[i]);
+      const float l = logf(sum.value());
+      p.lse[i] = mx + l;
+      p.loss[p.tok[i]] = (mx - p.zlab[i]) + l;
     }
   }
   if (tid == 0) {
@@ -203,14 +291,15 @@ __global__ void __launch_bounds__(128) loss_rows(const LossPlan p) {
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  double a = 0.0;
-  for (int j = tid; j < n_tok; j += blockDim.x)
-    a += (double)p.wrow[j] * (double)__ldcg(p.loss + p.tok[j]);
-  const double t = block_sum(a, s_d);
-  if (tid == 0) {
-    const double k = (double)__uint_as_float(p.ctrl[kLossScale]);
-    *p.total = n_tok > 0 ? (float)(k * t) : 0.f;
+  Sum2 a;
+  for (int j = tid; j < n_tok; j += blockDim.x) {
+    // the product's rounding error goes into the sum too
+    const float w = p.wrow[j], x = __ldcg(p.loss + p.tok[j]), y = w * x;
+    a.add(y);
+    a.c += fmaf(w, x, -y);
   }
+  const Sum2 t = block_sum(a, s_w);
+  if (tid == 0) *p.total = n_tok > 0 ? __uint_as_float(p.ctrl[kLossScale]) * t.value() : 0.f;
 }
 
 // q = w (softmax - onehot) in place, columns [v0, v1): fp32 from stored logits.
@@ -226,50 +315,92 @@ __global__ void __launch_bounds__(256) loss_dz_f32(const LossPlan p, int v0, int
 }
 
 // The same in bf16 from the stored distances (one piece: v0 = 0), over whole 256-column
-// tiles: columns past the vocabulary become 0.  Eight columns a thread.
+// tiles: columns past the vocabulary become 0.  Two vectors of eight columns a thread and
+// sweep; the thread that has the label's column writes it again.
 __global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc], i = blockIdx.x;
   if (i >= n_tok) return;
   uint4* q = (uint4*)((uint16_t*)p.q + (size_t)i * p.ldq);
+  const float2* st = p.stat + (size_t)i * p.n_stat;
   const float lse = p.lse[i], w = p.wrow[i];
   const int lab = p.lab[i], end = (n_voc + 255) / 256 * 32, tiles = (n_voc + 127) / 128;
-  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < end; c += gridDim.y * blockDim.x) {
-    const uint4 x = q[c];
-    const int tile = min(c / 16, tiles - 1);          // (a tile past the last is all far)
-    const float s = (p.stat[(size_t)i * p.n_stat + tile].x - lse) * 1.44269504f;
-    const uint32_t g[4] = {x.x, x.y, x.z, x.w};
-    uint32_t o[4];
+  const int step = gridDim.y * blockDim.x;
+  for (int c0 = blockIdx.y * blockDim.x + threadIdx.x; c0 < end; c0 += 2 * step) {
+    uint4 x[2];
+    float s[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int v = 8 * c + 2 * j;
-      float e0 = w * loss_gap_exp(g[j] & 0xFFFFu, s), e1 = w * loss_gap_exp(g[j] >> 16, s);
-      if (v == lab) e0 = loss_label_grad(p, i, e0 - w);
-      if (v + 1 == lab) e1 = loss_label_grad(p, i, e1 - w);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
-      o[j] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 + h * step;
+      if (c >= end) break;
+      x[h] = q[c];
+      // (a tile past the last is all far)
+      s[h] = (st[min(c / 16, tiles - 1)].x - lse) * 1.44269504f;
     }
-    q[c] = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 + h * step;
+      if (c >= end) break;
+      const uint32_t g[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b =
+            __floats2bfloat162_rn(w * loss_gap_exp(g[j] & 0xFFFFu, s[h]),
+                                  w * loss_gap_exp(g[j] >> 16, s[h]));
+        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      q[c] = make_uint4(o[0], o[1], o[2], o[3]);
+      if (lab / 8 == c) {
+        const uint32_t gap = (g[lab % 8 / 2] >> (16 * (lab & 1))) & 0xFFFFu;
+        reinterpret_cast<__nv_bfloat16*>(q)[lab] =
+            loss_label_grad(p, i, w * loss_gap_exp(gap, s[h]) - w);
+      }
+    }
   }
 }
 
-// The compact head of a bias-form bf16 head: its rows and its columns of markov_w2, then
-// zeros up to a multiple of 256.
+// The compact head of a bias-form bf16 head: its rows (a warp each), then zeros up to a
+// multiple of 256, and below its columns of markov_w2.
 __global__ void __launch_bounds__(256) loss_gather_head(const LossPlan p) {
   const int n = (int)p.ctrl[kLossVoc];
-  const int end = min(p.Vh, (n + 255) / 256 * 256), per = p.H / 8;
+  const int end = min(p.Vh, (n + 255) / 256 * 256), per = p.H / 8, lane = threadIdx.x % 32;
   const uint4* w = (const uint4*)p.lm_head;
   uint4* wc = (uint4*)p.wc;
-  for (int j = blockIdx.x; j < end; j += gridDim.x) {
-    const size_t from = j < n ? (size_t)p.vlist[j] * per : 0;
-    for (int k = threadIdx.x; k < per; k += blockDim.x)
-      wc[(size_t)j * per + k] = j < n ? w[from + k] : make_uint4(0, 0, 0, 0);
+  for (int j = blockIdx.x * 8 + threadIdx.x / 32; j < end; j += gridDim.x * 8) {
+    const bool in = j < n;
+    const size_t from = in ? (size_t)p.vlist[j] * per : 0;
+    for (int k0 = lane; k0 < per; k0 += 8 * 32) {
+      uint4 x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int k = k0 + 32 * q;
+        x[q] = in && k < per ? __ldcs(w + from + k) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (k0 + 32 * q < per) wc[(size_t)j * per + k0 + 32 * q] = x[q];
+    }
   }
+}
+
+// CTA (x, y): 256 compact columns, rows 8 y ... of markov_w2.
+__global__ void __launch_bounds__(256) loss_gather_w2(const LossPlan p) {
+  const int n = (int)p.ctrl[kLossVoc], end = min(p.Vh, (n + 255) / 256 * 256);
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  if (j >= end) return;
   const __nv_bfloat16* w2 = (const __nv_bfloat16*)p.w2;
   __nv_bfloat16* w2c = (__nv_bfloat16*)p.w2c;
-  for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < end; j += gridDim.x * blockDim.x) {
-    const int v = j < n ? p.vlist[j] : -1;
-    for (int k = 0; k < p.r; ++k)
-      w2c[(size_t)k * p.Vh + j] = v >= 0 ? w2[(size_t)k * p.Vh + v] : __float2bfloat16(0.f);
+  const int v = j < n ? p.vlist[j] : -1;
+  __nv_bfloat16 x[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int k = blockIdx.y * 8 + q;
+    x[q] = v >= 0 && k < p.r ? w2[(size_t)k * p.Vh + v] : __float2bfloat16(0.f);
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int k = blockIdx.y * 8 + q;
+    if (k < p.r) w2c[(size_t)k * p.Vh + j] = x[q];
   }
 }
 
@@ -281,23 +412,51 @@ __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
   const int i = blockIdx.x;
   if (i >= (int)p.ctrl[kLossTok]) return;
   const float k = __uint_as_float(p.ctrl[kLossScale]);
-  const size_t step = (size_t)p.Tp * p.Kx;
-  float* x = p.dxp + (size_t)i * p.Kx;
+  const size_t step = (size_t)p.Tp * p.Kx / 4;
+  float4* x = (float4*)(p.dxp + (size_t)i * p.Kx);
   const float lost = p.qres ? p.qres[i] : 0.f;
   const size_t row = (size_t)loss_head_row(p, p.lab[i]);
-  for (int c = threadIdx.x; c < p.Kx; c += blockDim.x) {
+  E* dh = p.d_hidden ? (E*)p.d_hidden + (size_t)p.tok[i] * p.H : nullptr;
+  // four columns a thread (Hp and Kx are multiples of 64)
+  const int from = p.d_hidden ? 0 : p.Hp / 4, to = p.d_w1 ? p.Kx / 4 : p.Hp / 4;
+  for (int c4 = from + threadIdx.x; c4 < to; c4 += blockDim.x) {
+    float a[4] = {};
+    for (int s0 = 0; s0 < p.splits; s0 += 8) {
+      float4 y[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        y[s] = s0 + s < p.splits ? __ldcs(x + (s0 + s) * step + c4) : make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        a[0] += y[s].x; a[1] += y[s].y; a[2] += y[s].z; a[3] += y[s].w;
+      }
+    }
+    const int c = 4 * c4;
     const bool head = c < p.Hp;
-    if (head ? !p.d_hidden || c >= p.H : !p.d_w1 || c - p.Hp >= p.r) continue;
-    float a = x[c];
-    for (int s = 1; s < p.splits; ++s) a += x[s * step + c];
-    if (p.qres)
-      a += lost * to_f32(head ? ((const E*)p.lm_head)[row * p.H + c]
-                              : ((const E*)p.w2)[(size_t)(c - p.Hp) * p.Vh + row]);
-    a *= k;
-    if (head)
-      ((E*)p.d_hidden)[(size_t)p.tok[i] * p.H + c] = from_f32<E>(a);
-    else
-      x[c] = a;
+    if (p.qres) {                             // (bf16: H is a multiple of 8)
+      if (head) {
+        if (c < p.H) {
+          struct alignas(4 * sizeof(E)) Four { E e[4]; };
+          const Four w = *reinterpret_cast<const Four*>((const E*)p.lm_head + row * p.H + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[j] += lost * to_f32(w.e[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j - p.Hp < p.r)
+            a[j] += lost * to_f32(((const E*)p.w2)[(size_t)(c + j - p.Hp) * p.Vh + row]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] *= k;
+    if (head) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < p.H) dh[c + j] = from_f32<E>(a[j]);
+    } else {
+      x[c4] = make_float4(a[0], a[1], a[2], a[3]);
+    }
   }
 }
 
@@ -350,22 +509,18 @@ cudaError_t launch_loss_plan(const LossPlan& p) {
     e = cudaMemsetAsync(p.vinv, 0xFF, sizeof(int32_t) * (size_t)p.Vh, p.stream);
     if (e != cudaSuccess) return e;
     loss_vocab<<<std::min(256, (p.Vh + 255) / 256), 256, 0, p.stream>>>(p, chunks);
-    if (p.wc) loss_gather_head<<<1216, 256, 0, p.stream>>>(p);
+    if (p.wc) {
+      loss_gather_head<<<std::min(1216, (p.Vh + 7) / 8), 256, 0, p.stream>>>(p);
+      if (p.r > 0)
+        loss_gather_w2<<<dim3((p.Vh + 255) / 256, (p.r + 7) / 8), 256, 0, p.stream>>>(p);
+    }
   }
-  loss_tokens<<<1, kPlanThreads, 0, p.stream>>>(p);
-  const size_t es = p.dtype == 0 ? 4 : 2;
-  if (p.d_w1) {
-    e = cudaMemsetAsync(p.d_w1, 0, es * (size_t)p.V * p.r, p.stream);
-    if (e != cudaSuccess) return e;
-  }
-  if (p.vlist && p.d_lm_head) {
-    e = cudaMemsetAsync(p.d_lm_head, 0, es * (size_t)p.Vh * p.H, p.stream);
-    if (e != cudaSuccess) return e;
-  }
-  if (p.vlist && p.d_w2) {
-    e = cudaMemsetAsync(p.d_w2, 0, es * (size_t)p.Vh * p.r, p.stream);
-    if (e != cudaSuccess) return e;
-  }
+  loss_tokens<<<1, std::min(kPlanThreads, (p.T + 31) / 32 * 32), 0, p.stream>>>(p);
+  if (p.dtype == 0)
+    for (int z = 0; z < p.n_zero; ++z) {
+      e = cudaMemsetAsync(p.zero[z].p, 0, p.zero[z].bytes, p.stream);
+      if (e != cudaSuccess) return e;
+    }
   if (p.dtype == 0)
     loss_gather<float><<<p.Tp, 256, 0, p.stream>>>(p);
   else
@@ -374,7 +529,7 @@ cudaError_t launch_loss_plan(const LossPlan& p) {
 }
 
 cudaError_t launch_loss_rows(const LossPlan& p) {
-  loss_rows<<<p.T, 128, 0, p.stream>>>(p);
+  loss_rows<<<p.T, kRowsThreads, 0, p.stream>>>(p);
   return cudaGetLastError();
 }
 

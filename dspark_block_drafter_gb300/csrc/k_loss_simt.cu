@@ -4,9 +4,11 @@
 //   dX      dx[i][c] = sum_j q[i][j] [lm_head | markov_w2^T][j][c]
 //   dW      [d_lm_head | d_markov_w2^T][j][c] = scale * sum_i q[i][j] X[i][c]
 //
-// i: compact rows, j: compact head rows, c: columns of X.  One 64 x 64 tile per CTA, 16
+// i: compact rows, j: compact head rows, c: columns of X.  One 64 x 64 tile per CTA, 32
 // deep, four by four results per thread; operands pass through shared memory with the
-// index that is contiguous in memory spread over a warp's lanes.
+// index that is contiguous in memory spread over a warp's lanes, the next 32 deep waiting in
+// registers while these are multiplied (a small head is bound by the trips to memory: tiny
+// config, logits 60 -> XX us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -17,42 +19,57 @@ namespace dspark {
 
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
+constexpr int kTile = 64, kDepth = 32;
+constexpr int kLoads = kTile * kDepth / 256;
 
-// s[k][m] = at(m, k) for a 64 x 16 tile; `along_k`: k is the contiguous index in memory.
-template <typename F>
-__device__ __forceinline__ void load_tile(float (*s)[kTile + 4], bool along_k, F at) {
-#pragma unroll
-  for (int e = threadIdx.x; e < kTile * kDepth; e += 256) {
-    const int k = along_k ? e % kDepth : e / kTile;
-    const int m = along_k ? e / kDepth : e % kTile;
-    s[k][m] = at(m, k);
-  }
-}
-
-// acc[a][b] += sum_k A(4 ty + a, k) B(4 tx + b, k) over `depth`
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(float (&acc)[4][4], int depth, bool a_along_k,
-                                             FA a_at, FB b_tile) {
+// acc[a][b] += sum_k a_at(4 ty + a, k) b_at(4 tx + b, k) over `depth`.  a_along, b_along(k0):
+// whether k is the index contiguous in memory (from depth k0 on).
+template <typename FA, typename FB, typename AB>
+__device__ __forceinline__ void tile_product(float (&acc)[4][4], int depth, bool a_along,
+                                             FA a_at, AB b_along, FB b_at) {
   __shared__ __align__(16) float sa[kDepth][kTile + 4], sb[kDepth][kTile + 4];
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  float ra[kLoads], rb[kLoads];
+  auto place = [](bool along, int q, int& m, int& k) {
+    const int e = threadIdx.x + 256 * q;
+    k = along ? e % kDepth : e / kTile;
+    m = along ? e / kDepth : e % kTile;
+  };
+  auto load = [&](int k0) {
+    const bool bl = b_along(k0);
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      int m, k;
+      place(a_along, q, m, k);
+      ra[q] = a_at(m, k0 + k);
+      place(bl, q, m, k);
+      rb[q] = b_at(m, k0 + k);
+    }
+  };
+  load(0);
   for (int k0 = 0; k0 < depth; k0 += kDepth) {
-    __syncthreads();
-    load_tile(sa, a_along_k, [&](int m, int k) { return a_at(m, k0 + k); });
-    b_tile(sb, k0);
-    __syncthreads();
+    const bool bl = b_along(k0);
 #pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      int m, k;
+      place(a_along, q, m, k);
+      sa[k][m] = ra[q];
+      place(bl, q, m, k);
+      sb[k][m] = rb[q];
+    }
+    __syncthreads();
+    if (k0 + kDepth < depth) load(k0 + kDepth);
+#pragma unroll 8
     for (int k = 0; k < kDepth; ++k) {
-      float a[4], b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = sa[k][4 * ty + j];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = sb[k][4 * tx + j];
+      const float4 a4 = *reinterpret_cast<const float4*>(&sa[k][4 * ty]);
+      const float4 b4 = *reinterpret_cast<const float4*>(&sb[k][4 * tx]);
+      const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
     }
+    __syncthreads();
   }
 }
 
@@ -72,19 +89,13 @@ loss_logits(const LossPlan p, int v0, int v1, bool stats, bool store) {
   __syncthreads();
   float acc[4][4] = {};
   tile_product(
-      acc, p.Kx, true,
-      [&](int m, int k) { return x[(size_t)(m0 + m) * p.Kx + k]; },
-      [&](float (*sb)[kTile + 4], int k0) {
-        if (k0 < p.Hp)
-          load_tile(sb, true, [&](int n, int k) {
-            const int row = s_row[n], h = k0 + k;
-            return row >= 0 && h < p.H ? (w[(size_t)row * p.H + h]) : 0.f;
-          });
-        else
-          load_tile(sb, false, [&](int n, int k) {
-            const int row = s_row[n], c = k0 - p.Hp + k;
-            return row >= 0 && c < p.r ? (w2[(size_t)c * p.Vh + row]) : 0.f;
-          });
+      acc, p.Kx, true, [&](int m, int k) { return x[(size_t)(m0 + m) * p.Kx + k]; },
+      [&](int k0) { return k0 < p.Hp; },
+      [&](int n, int k) {
+        const int row = s_row[n], c = k - p.Hp;
+        if (row < 0) return 0.f;
+        if (c < 0) return k < p.H ? w[(size_t)row * p.H + k] : 0.f;
+        return c < p.r ? w2[(size_t)c * p.Vh + row] : 0.f;
       });
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll
@@ -133,6 +144,7 @@ __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1,
   const float* w = (const float*)p.lm_head;
   const float* w2 = (const float*)p.w2;
   float acc[4][4] = {};
+  const bool head = c0 < p.Hp;
   if (jb > ja)
     tile_product(
         acc, jb - ja, true,
@@ -140,15 +152,13 @@ __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1,
           const int j = ja + k;
           return m0 + m < n_tok && j < jb ? q[(size_t)(m0 + m) * p.ldq + (j - v0)] : 0.f;
         },
-        [&](float (*sb)[kTile + 4], int k0) {
-          const bool head = c0 < p.Hp;
-          load_tile(sb, !head, [&](int n, int k) {
-            const int j = ja + k0 + k, c = c0 + n;
-            if (j >= jb) return 0.f;
-            const int row = loss_head_row(p, j);
-            if (head) return c < p.H ? (w[(size_t)row * p.H + c]) : 0.f;
-            return c - p.Hp < p.r ? (w2[(size_t)(c - p.Hp) * p.Vh + row]) : 0.f;
-          });
+        [&](int) { return !head; },
+        [&](int n, int k) {
+          const int j = ja + k, c = c0 + n;
+          if (j >= jb) return 0.f;
+          const int row = loss_head_row(p, j);
+          if (head) return c < p.H ? w[(size_t)row * p.H + c] : 0.f;
+          return c - p.Hp < p.r ? w2[(size_t)(c - p.Hp) * p.Vh + row] : 0.f;
         });
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   float* dx = p.dxp + (size_t)blockIdx.z * p.Tp * p.Kx;
@@ -178,11 +188,8 @@ __global__ void __launch_bounds__(256) loss_dw(const LossPlan p, int v0, int v1)
         const int j = j0 + m;
         return j < n_voc && k < n_tok ? q[(size_t)k * p.ldq + (j - v0)] : 0.f;
       },
-      [&](float (*sb)[kTile + 4], int k0) {
-        load_tile(sb, false, [&](int n, int k) {
-          return k0 + k < n_tok ? (x[(size_t)(k0 + k) * p.Kx + c0 + n]) : 0.f;
-        });
-      });
+      [](int) { return false; },
+      [&](int n, int k) { return k < n_tok ? x[(size_t)k * p.Kx + c0 + n] : 0.f; });
   const float scale = __uint_as_float(p.ctrl[kLossScale]);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
 #pragma unroll

@@ -16,6 +16,8 @@
 // Persistent and warp-specialised, one CTA per SM: warp 8 issues the TMA copies, one thread
 // of warp 9 the MMAs; warps 0-3 take the first 128 columns of a finished accumulator, warps
 // 4-7 the others (there are two accumulators, so that this overlaps the next products).
+// Warp 10 writes the zeros of gradients that no product reaches (rows of masked tokens, of
+// tokens that precede no slot): the products leave most of the memory bandwidth unused.
 //
 // The tensor core cuts each partial sum of an accumulator toward zero, so a long sum drifts:
 // over K = 4352 the losses were off by 5e-6.  The logits' accumulator is therefore read
@@ -46,7 +48,9 @@ namespace {
 constexpr int kTileM = 128, kTileN = 256, kBlockK = 64;
 constexpr uint32_t kBox = 64 * 64 * 2;               // bytes of 64 rows of 64 elements
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kThreads = 32 * (kEpiWarps + 3);
+constexpr uint32_t kRowBytes = 128;                  // dW: a row's part of a staged store
+constexpr uint32_t kStaging = kEpiWarps * 32 * kRowBytes;
 constexpr int kSumBlocks = 12;                       // K-blocks of one part of a logit's sum
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kBarBytes = 512;
@@ -71,6 +75,7 @@ struct TcArgs {
   int first;           // dX: the first piece (later ones add)
   int n_head, n_markov;  // 256-column tiles of X's two parts that are computed
   int chunked;         // dX: lm_head rows are whole 64-column chunks
+  int zero0, zero1;    // the share of the plan's zeros this launch writes, in 1/64
 };
 
 // One unit of work: a tile of the result and a range of K-blocks.
@@ -151,6 +156,35 @@ __device__ __forceinline__ void load_chunks(uint8_t* dst, const CUtensorMap* m, 
     ptx::tma_load_3d(dst, m, bar, 0, y, chunk);
 }
 
+// This CTA's part of the zeros of a launch, by one warp.
+__device__ __forceinline__ void write_zeros(const TcArgs& g, int lane) {
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  const int parts = (int)gridDim.x, part = (int)blockIdx.x;
+  for (int z = 0; z < g.p.n_zero; ++z) {
+    const LossZero& q = g.p.zero[z];
+    // items: rows, or 16-byte vectors (and the odd bytes, all fewer than 16, at the end)
+    const long long items = q.keep ? (long long)(q.bytes / q.row_bytes) : (long long)(q.bytes / 16);
+    const long long lo = items * g.zero0 / 64, n = items * g.zero1 / 64 - lo;
+    const long long a = lo + n * part / parts, b = lo + n * (part + 1) / parts;
+    if (q.keep) {
+      const int per = q.row_bytes / 16;
+      for (long long r0 = a; r0 < b; r0 += 32) {
+        unsigned m = __ballot_sync(0xFFFFFFFFu, r0 + lane < b && q.keep[r0 + lane] < 0);
+        while (m) {
+          uint4* row = reinterpret_cast<uint4*>(q.p) + (r0 + __ffs(m) - 1) * per;
+          m &= m - 1;
+          for (int k = lane; k < per; k += 32) row[k] = none;
+        }
+      }
+    } else {
+      uint4* v = reinterpret_cast<uint4*>(q.p);
+#pragma unroll 4
+      for (long long k = a + lane; k < b; k += 32) v[k] = none;
+      if (g.zero1 == 64 && part == 0 && lane < (int)(q.bytes % 16)) q.p[items * 16 + lane] = 0;
+    }
+  }
+}
+
 template <int MODE, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g, int stages) {
@@ -166,6 +200,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = (uint32_t*)(drain + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  uint8_t* staging = smem + (size_t)stages * kStage + kBarBytes;   // dW only
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0;
@@ -383,6 +418,8 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
         ptx::mma_commit(drain);
       ptx::mbar_wait(drain, 0, kWaitBudget, nullptr);
     }
+  } else if (warp == kEpiWarps + 2) {
+    if (MODE != kDw && g.zero1 > g.zero0) write_zeros(g, lane);
   } else {
     // ---------------------------------------------------------------- epilogue
     const int quad = warp % 4, half = warp / 4;       // lanes and columns of this warp
@@ -444,20 +481,20 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
           for (int j = 0; j < 128; ++j)
             if (j >= n_in) z[j] = -INFINITY;
         }
+        const bool here = lab >= v0 && lab < v0 + 128;
+        float zl = 0.f;                           // the label's logit
+        if (__any_sync(0xFFFFFFFFu, here)) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (lab == v0 + j) zl = z[j];
+        }
         float ref = 0.f, wt = 0.f;
         if (g.want & kWantStats) {
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int j = 0; j < 128; ++j) mx[j % 4] = fmaxf(mx[j % 4], z[j]);
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool here = lab >= v0 && lab < v0 + 128;
-          if (__any_sync(0xFFFFFFFFu, here)) {
-            float zl = 0.f;
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (lab == v0 + j) zl = z[j];
-            if (here) p.zlab[m] = zl;
-          }
+          if (here) p.zlab[m] = zl;
           ref = top > -INFINITY ? top : 0.f;      // (a NaN passes the maximum, not the sum)
           float sum[4] = {};
 #pragma unroll
@@ -478,10 +515,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             for (int j = 0; j < 16; j += 2) {
               const float d0 = z[c + j] - ref, d1 = z[c + j + 1] - ref;
               if (g.want & kWantGrad) {
-                float e0 = wt * __expf(d0), e1 = wt * __expf(d1);
-                if (lab == v0 + c + j) e0 = loss_label_grad(p, m, e0 - wt);
-                if (lab == v0 + c + j + 1) e1 = loss_label_grad(p, m, e1 - wt);
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(wt * __expf(d0), wt * __expf(d1));
                 o[j / 2] = *reinterpret_cast<const uint32_t*>(&b2);
               } else {
                 o[j / 2] = __byte_perm(loss_gap(-d0), loss_gap(-d1), 0x5410);
@@ -490,6 +524,9 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             }
             ptx::st_global_v8(qrow + c, o);
           }
+          if ((g.want & kWantGrad) && here)       // (after this thread's vector store)
+            reinterpret_cast<__nv_bfloat16*>(qrow)[lab - v0] =
+                loss_label_grad(p, m, wt * __expf(zl - ref) - wt);
         }
       } else {
         if (!acc_wait()) break;
@@ -526,37 +563,54 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
           const bool live = j0 < min(g.v1, n_voc);
           const size_t row = live ? (size_t)loss_head_row(p, j0) : 0;
           const int width = min(128, markov ? p.r - (c0 - p.Hp) : p.H - c0);
-#pragma unroll 1
-          for (int c = 0; c < width; c += 32) {
+          uint32_t o[64];                                     // 128 columns, in pairs
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
             uint32_t r[32];
             ptx::tmem_ld_32x32b_x32(at + c, r);
             ptx::tmem_ld_wait();
-            if (!live) continue;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              r[j] = none ? 0u : __float_as_uint(__uint_as_float(r[j]) * scale);
-            if (markov) {
-              __nv_bfloat16* d = (__nv_bfloat16*)p.d_w2 + (size_t)(c0 - p.Hp + c) * p.Vh + row;
+            for (int j = 0; j < 32; j += 2) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(
+                  none ? 0.f : __uint_as_float(r[j]) * scale,
+                  none ? 0.f : __uint_as_float(r[j + 1]) * scale);
+              o[(c + j) / 2] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+          }
+          acc_free();
+          if (markov) {
+            // column by column: a warp's rows are neighbours there
+            uint16_t* d = (uint16_t*)p.d_w2 + (size_t)(c0 - p.Hp) * p.Vh + row;
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c + j < width) d[(size_t)j * p.Vh] = __float2bfloat16(__uint_as_float(r[j]));
-            } else {
-              __nv_bfloat16* d = (__nv_bfloat16*)p.d_lm_head + row * p.H + c0 + c;
+            for (int j = 0; j < 128; ++j)
+              if (live && j < width)
+                d[(size_t)j * p.Vh] = (uint16_t)(j & 1 ? o[j / 2] >> 16 : o[j / 2] & 0xFFFFu);
+          } else {
+            // through shared memory, so that eight lanes store 128 bytes of one row (one
+            // row a lane, 16 bytes at a time, reached a fifth of the write bandwidth)
+            uint8_t* st = staging + warp * 32 * kRowBytes;
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {               // (H is a multiple of 8)
-                if (c + j >= width) break;
-                uint4 o;
-                uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+            for (int c = 0; c < 128; c += 64) {
+              __syncwarp();
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(
-                      __uint_as_float(r[j + 2 * b]), __uint_as_float(r[j + 2 * b + 1]));
-                  w[b] = *reinterpret_cast<const uint32_t*>(&b2);
-                }
-                *reinterpret_cast<uint4*>(d + j) = o;
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint4*>(st + lane * kRowBytes + ((q ^ (lane & 7)) << 4)) =
+                    make_uint4(o[c / 2 + 4 * q], o[c / 2 + 4 * q + 1], o[c / 2 + 4 * q + 2],
+                               o[c / 2 + 4 * q + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const int rr = 4 * q + lane / 8, ch = lane & 7, col = c + 8 * ch;
+                const uint4 v =
+                    *reinterpret_cast<const uint4*>(st + rr * kRowBytes + ((ch ^ (rr & 7)) << 4));
+                const int to = __shfl_sync(0xFFFFFFFFu, live ? (int)row : -1, rr);
+                if (to >= 0 && col < width)                   // (H is a multiple of 8)
+                  *reinterpret_cast<uint4*>((__nv_bfloat16*)p.d_lm_head + (size_t)to * p.H + c0 +
+                                            col) = v;
               }
             }
           }
+          continue;
         }
         acc_free();
       }
@@ -646,8 +700,9 @@ cudaError_t launch(const TcArgs& g, long long tiles) {
   Maps maps;
   if (!make_maps<MODE, CG>(g, &maps)) return cudaErrorInvalidValue;
   constexpr uint32_t stage = 2 * kBox + kTileN / CG / 64 * kBox;
-  const int stages = (kSmemMax - 1024 - kBarBytes) / (int)stage;
-  const size_t smem = 1024 + kBarBytes + (size_t)stages * stage;
+  constexpr uint32_t fixed = 1024 + kBarBytes + (MODE == kDw ? kStaging : 0);
+  constexpr int stages = (kSmemMax - fixed) / stage;
+  constexpr size_t smem = fixed + (size_t)stages * stage;
   int sms = 0;
   cudaError_t e = device_sms(&sms);
   if (e == cudaSuccess) e = raise_smem_limit((const void*)loss_product<MODE, CG>, smem);
@@ -699,6 +754,7 @@ cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats,
   g.v0 = v0;
   g.v1 = v1;
   g.want = stats ? kWantStats | (store ? kWantGap : 0) : kWantGrad;
+  if (stats && p.n_zero > 0) g.zero1 = p.d_hidden || p.d_w1 ? 32 : 64;
   const long long tiles = (long long)row_tiles(p.T) * ((v1 - v0 + kTileN - 1) / kTileN);
   return single(p.T) ? launch<kLogits, 1>(g, tiles) : launch<kLogits, 2>(g, tiles);
 }
@@ -710,6 +766,10 @@ cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first) {
   g.v1 = v1;
   g.first = first;
   g.chunked = p.H % 64 == 0;
+  if (first && p.n_zero > 0) {
+    g.zero0 = 32;
+    g.zero1 = 64;
+  }
   g.n_head = p.d_hidden ? (p.Hp + kTileN - 1) / kTileN : 0;
   g.n_markov = p.d_w1 ? (p.rp + kTileN - 1) / kTileN : 0;
   const long long tiles = (long long)row_tiles(p.T) * (g.n_head + g.n_markov) * p.splits;

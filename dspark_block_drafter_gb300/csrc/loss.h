@@ -24,6 +24,15 @@ enum : int {
   kLossDone = 4,     // row CTAs whose loss is written
 };
 
+// Gradient memory that no product writes: `bytes` from `p` on, or, with `keep`, the rows of
+// `row_bytes` whose keep entry is negative.
+struct LossZero {
+  char* p;
+  size_t bytes;
+  const int32_t* keep;
+  int row_bytes;
+};
+
 struct LossPlan {
   int T, H, V, Vh, r, dtype, reduction;
   float loss_scale;
@@ -61,6 +70,8 @@ struct LossPlan {
   float* dxp;                         // [splits][Tp][Kx] partial gradients of X
   int splits;
   bool grads;                         // any gradient asked for
+  LossZero zero[3];
+  int n_zero;
   cudaStream_t stream;
 };
 
@@ -109,7 +120,8 @@ int loss_simt_splits(int T, int Kx, int cols);
 cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stats, bool store);
 cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first);
 cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1);
-// k_loss_tc.cu (bf16, on the tensor cores)
+// k_loss_tc.cu (bf16, on the tensor cores).  The logits with statistics and the first dX also
+// write the plan's zeros, half each (all in the logits when there is no dX).
 int loss_tc_splits(int T, int H, int r, int cols);
 cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats, bool store);
 cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first);

@@ -63,7 +63,8 @@ def test_struct_layouts_match_c():
     (dict(r=513), {}, {}, U), (dict(T=(1 << 20) + 1), {}, {}, U),
     (dict(dtype=1, H=60), {}, {}, U),
     (dict(dtype=1), dict(V_head=999, d2t=0x10), {}, U),
-    (dict(dtype=1), {}, dict(d_lm_head=0x9008), I),
+    (dict(dtype=1), {}, dict(d_lm_head=0x9008), I), (dict(dtype=1), {}, dict(d_markov_w1=0x9008), I),
+    (dict(dtype=1), {}, dict(d_markov_w2=0x9004), I),
     (dict(dtype=1), dict(lm_head=0x1002), {}, I), (dict(dtype=1), dict(markov_w2=0x3008), {}, I),
 ])
 def test_loss_refusals(cfg, head, out, status):
