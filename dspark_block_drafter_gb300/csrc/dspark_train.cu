@@ -132,8 +132,7 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
     p->q = take(es * Tp * p->ldq);
     if (tc) p->qres = (float*)take(4 * Tp);
     if (p->d_hidden || p->d_w1) {
-      p->splits = tc ? loss_tc_splits(p->T, p->d_hidden ? p->H : 0, p->d_w1 ? p->r : 0,
-                                      p->piece_cols)
+      p->splits = tc ? loss_tc_splits(p->T, p->d_hidden ? p->Hp : 0, p->d_w1 ? p->rp : 0)
                      : loss_simt_splits(p->T, p->Kx, p->piece_cols);
       p->dxp = (float*)take(sizeof(float) * p->splits * Tp * p->Kx);
     }
@@ -203,14 +202,12 @@ static size_t plan_norm(const dspark_norm_config* c, char* ws, NormArgs* a) {
     off = align_up(off + 4 * floats, kAlign);
     return (float*)at;
   };
-  const size_t units = (size_t)c->T;
+  // (as many CTAs as there are units: rows, or parts of the rows that share a gate row)
+  const size_t parts = (size_t)norm_span_parts(c->T, c->gate_span);
+  const size_t rows = ((size_t)c->T + c->gate_span - 1) / c->gate_span;
+  const size_t units = std::max((size_t)c->T, rows * parts);
   a->w_part = take(2 * std::min(units, (size_t)norm_max_ctas(c->H)) * c->H);
-  const int parts = norm_span_parts(c->T, c->gate_span);
-  a->gate_part = nullptr;
-  if (parts > 1) {
-    const size_t rows = ((size_t)c->T + c->gate_span - 1) / c->gate_span;
-    a->gate_part = take(rows * parts * c->H);
-  }
+  a->gate_part = parts > 1 ? take(rows * parts * c->H) : nullptr;
   return off;
 }
 
@@ -336,7 +333,7 @@ dspark_status dspark_block_norm_backward(const dspark_norm_config* cfg, const vo
 
 size_t dspark_clip_grads_workspace_size(int32_t count, const dspark_grad* grads) {
   if (validate_clip(count, grads) != DSPARK_OK) return 0;
-  return align_up(sizeof(double) * clip_partials(count), kAlign);
+  return align_up(sizeof(float) * clip_partials(count), kAlign);
 }
 
 dspark_status dspark_clip_grads(int32_t count, const dspark_grad* grads, float max_norm,
@@ -347,9 +344,9 @@ dspark_status dspark_clip_grads(int32_t count, const dspark_grad* grads, float m
   if (!(max_norm >= 0.f)) return fail(DSPARK_ERR_INVALID_ARG, "max_norm must be >= 0");
   if (!norm) return fail(DSPARK_ERR_INVALID_ARG, "norm is required");
   st = check_workspace(workspace, workspace_bytes,
-                       align_up(sizeof(double) * clip_partials(count), kAlign));
+                       align_up(sizeof(float) * clip_partials(count), kAlign));
   if (st != DSPARK_OK) return st;
-  const cudaError_t e = launch_clip_grads(count, grads, max_norm, norm, (double*)workspace,
+  const cudaError_t e = launch_clip_grads(count, grads, max_norm, norm, (float*)workspace,
                                           (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "gradient clipping kernels");
   return DSPARK_OK;

@@ -2,6 +2,9 @@
 //
 //   norm = sqrt(sum in^2),   out = in * min(1, max_norm / (norm + 1e-6))
 //
+// Squares are summed in fp32: within a thread with the rounding errors carried along, then over
+// the CTA and over the CTAs pairwise (fp64 runs at a few additions per clock and SM here).
+//
 // Bound by memory.  Two passes: the first sums squares, CTA by CTA in a fixed assignment of
 // chunks; the second first joins the CTAs' sums (every CTA for itself, the same way), then
 // scales, from the last chunk to the first, because the last ones read are still in L2.
@@ -12,6 +15,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "train.h"
 
 namespace dspark {
@@ -83,28 +87,37 @@ __device__ __forceinline__ float chunk_squares(const E* p, long long n, long lon
   return s;
 }
 
-__device__ __forceinline__ double clip_block_sum(double v) {
-  __shared__ double s[kThreads / 32];
+// Sum over the CTA in a fixed order; every thread gets it.
+__device__ __forceinline__ float clip_block_sum(float v) {
+  __shared__ float s[kThreads / 32];
+  const int lane = threadIdx.x % 32;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
+  if (lane == 0) s[threadIdx.x / 32] = v;
   __syncthreads();
-  double t = 0.0;
-  for (int w = 0; w < kThreads / 32; ++w) t += s[w];
-  return t;
+  v = lane < kThreads / 32 ? s[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
 }
 
 __global__ void __launch_bounds__(kThreads) clip_squares(const __grid_constant__ ClipList l,
-                                                         double* partial) {
-  double acc = 0.0;
+                                                         float* partial) {
+  pdl_wait();
+  pdl_signal();
+  float acc = 0.f, low = 0.f;
   for (int c = blockIdx.x; c < l.first[l.count]; c += gridDim.x) {
     const int g = clip_find(l, c);
     const long long lc = c - l.first[g];
-    acc += (double)(l.bf16[g]
+    const float x = l.bf16[g]
                         ? chunk_squares((const __nv_bfloat16*)l.in[g], l.n[g], lc, l.vec[g])
-                        : chunk_squares((const float*)l.in[g], l.n[g], lc, l.vec[g]));
+                        : chunk_squares((const float*)l.in[g], l.n[g], lc, l.vec[g]);
+    const float t = acc + x;                     // (both are >= 0: the larger one's error)
+    low += acc >= x ? (acc - t) + x : (x - t) + acc;
+    acc = t;
   }
-  const double s = clip_block_sum(acc);
+  // (an infinite sum has no rounding error to carry)
+  const float s = clip_block_sum(acc < INFINITY ? acc + low : acc);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
@@ -141,11 +154,13 @@ __device__ __forceinline__ void chunk_scale(const E* p, E* out, long long n, lon
 }
 
 __global__ void __launch_bounds__(kThreads) clip_scale(const __grid_constant__ ClipList l,
-                                                       const double* partial, int partials,
+                                                       const float* partial, int partials,
                                                        float max_norm, float* norm_out) {
-  double a = 0.0;
+  pdl_wait();
+  pdl_signal();
+  float a = 0.f;
   for (int j = threadIdx.x; j < partials; j += kThreads) a += partial[j];
-  const float norm = (float)sqrt(clip_block_sum(a));
+  const float norm = sqrtf(clip_block_sum(a));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   // (a norm that is not finite: everything is left as it is)
   const float k = norm < INFINITY ? fminf(1.f, max_norm / (norm + 1e-6f)) : 1.f;
@@ -184,7 +199,7 @@ size_t clip_partials(int count) {
 }
 
 cudaError_t launch_clip_grads(int count, const dspark_grad* grads, float max_norm, float* norm,
-                              double* partial, cudaStream_t stream) {
+                              float* partial, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
@@ -193,14 +208,16 @@ cudaError_t launch_clip_grads(int count, const dspark_grad* grads, float max_nor
   for (int a = 0; a < count; a += kClipList) {
     const ClipList l = make_list(grads + a, std::min(kClipList, count - a));
     const int grid = std::min(most, std::max(1, l.first[l.count]));
-    clip_squares<<<grid, kThreads, 0, stream>>>(l, partial + partials);
+    e = launch_after(clip_squares, grid, kThreads, 0, stream, l, partial + partials);
+    if (e != cudaSuccess) return e;
     partials += grid;
   }
   for (int a = (count - 1) / kClipList * kClipList; a >= 0; a -= kClipList) {
     const ClipList l = make_list(grads + a, std::min(kClipList, count - a));
     const int grid = std::min(most, std::max(1, l.first[l.count]));
-    clip_scale<<<grid, kThreads, 0, stream>>>(l, partial, partials, max_norm,
-                                              a == 0 ? norm : nullptr);
+    e = launch_after(clip_scale, grid, kThreads, 0, stream, l, partial, partials, max_norm,
+                     a == 0 ? norm : nullptr);
+    if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }

@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "loss.h"
 
 namespace dspark {
@@ -99,6 +100,8 @@ __device__ __forceinline__ void zero_row(E* dst, int n) {
 
 // Bias form: the compact vocabulary's size, inverse map and biases.  vinv is -1 before.
 __global__ void __launch_bounds__(256) loss_vocab(const LossPlan p, int chunks) {
+  pdl_wait();
+  pdl_signal();
   __shared__ int s_n;
   if (threadIdx.x == 0) {
     int n = 0;
@@ -138,10 +141,47 @@ __device__ __forceinline__ int loss_label_row(const LossPlan& p, int t) {
   return p.vinv ? p.vinv[row] : row;
 }
 
+// Splits of the vocabulary in dX's sum over it, chosen by one warp once the rows are counted.
+// bf16: a unit (a tile of dX over one split) costs its K-blocks of 64, about 12 K-blocks'
+// time for filling the pipeline and writing its partial result, and that result's traffic
+// (256 KB written and read: 0.23 K-blocks' time of the whole GPU); CTAs (pairs above 128
+// rows) take the units in waves.  The count with the least total is taken.  Measured with
+// 512 rows of the 151936 x 4096 head, dX and its sum: 2 splits 409 us (chosen), 1 698 us,
+// 3 530 us, 5 501 us, 13 442 us; with 3686 rows: 5 splits 2993 us, 2 2977 us, 3 3110 us.
+__device__ __forceinline__ int loss_pick_splits(const LossPlan& p, int n_tok, int n_voc, int lane) {
+  if (p.dtype == 0) return p.splits;
+  const bool pairs = p.T > 128;
+  const int nt = (p.d_hidden ? (p.Hp + 255) / 256 : 0) + (p.d_w1 ? (p.rp + 255) / 256 : 0);
+  const int tiles = max(1, (n_tok + 255) / 256) * nt, ctas = pairs ? 76 : 152;
+  const int nkb = (min(p.piece_cols, n_voc) + 63) / 64;
+  float cost = INFINITY;
+  int best = 1;
+  for (int s = 1 + lane; s <= p.splits && (s == 1 || s * 8 <= nkb); s += 32) {
+    const float c = (float)((tiles * s + ctas - 1) / ctas) * ((float)nkb / (float)s + 12.f) +
+                    0.23f * (float)(tiles * s);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float c = __shfl_xor_sync(0xFFFFFFFFu, cost, o);
+    const int b = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+    if (c < cost || (c == cost && b < best)) {
+      cost = c;
+      best = b;
+    }
+  }
+  return best;
+}
+
 // One CTA: compacts the rows that carry a loss, in order, and sums their weights.  Each
 // thread takes kPlanRows rows of a sweep, so that their loads overlap.
 constexpr int kPlanRows = 4;
 __global__ void __launch_bounds__(kPlanThreads) loss_tokens(const LossPlan p) {
+  pdl_wait();
+  pdl_signal();
   __shared__ int s_cnt[32];
   __shared__ float2 s_w[32];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, warps = blockDim.x / 32;
@@ -202,6 +242,10 @@ __global__ void __launch_bounds__(kPlanThreads) loss_tokens(const LossPlan p) {
       base += all;
     }
   }
+  if (warp == 0 && p.dxp) {
+    const int best = loss_pick_splits(p, base, (int)p.ctrl[kLossVoc], lane);
+    if (lane == 0) p.ctrl[kLossSplits] = (uint32_t)best;
+  }
   const float w = block_sum(wsum, s_w).value();
   if (tid == 0) {
     p.ctrl[kLossTok] = (uint32_t)base;
@@ -216,6 +260,8 @@ __global__ void __launch_bounds__(kPlanThreads) loss_tokens(const LossPlan p) {
 // row t.
 template <typename E>
 __global__ void __launch_bounds__(256) loss_gather(const LossPlan p) {
+  pdl_wait();
+  pdl_signal();
   const int t = blockIdx.x;
   E* x = (E*)p.x;
   if (t >= (int)p.ctrl[kLossTok]) zero_row(x + (size_t)t * p.Kx, p.Kx);
@@ -239,6 +285,8 @@ __global__ void __launch_bounds__(256) loss_gather(const LossPlan p) {
 // loss; the last CTA to finish sums the losses.
 constexpr int kRowsThreads = 256;
 __global__ void __launch_bounds__(kRowsThreads) loss_rows(const LossPlan p) {
+  pdl_wait();
+  pdl_signal();
   __shared__ float2 s_w[32];
   __shared__ bool s_last;
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc];
@@ -304,6 +352,8 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows(const LossPlan p) {
 
 // q = w (softmax - onehot) in place, columns [v0, v1): fp32 from stored logits.
 __global__ void __launch_bounds__(256) loss_dz_f32(const LossPlan p, int v0, int v1) {
+  pdl_wait();
+  pdl_signal();
   const int n_tok = (int)p.ctrl[kLossTok], i = blockIdx.x;
   if (i >= n_tok) return;
   const int end = min(v1, (int)p.ctrl[kLossVoc]);
@@ -318,6 +368,8 @@ __global__ void __launch_bounds__(256) loss_dz_f32(const LossPlan p, int v0, int
 // tiles: columns past the vocabulary become 0.  Two vectors of eight columns a thread and
 // sweep; the thread that has the label's column writes it again.
 __global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
+  pdl_wait();
+  pdl_signal();
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc], i = blockIdx.x;
   if (i >= n_tok) return;
   uint4* q = (uint4*)((uint16_t*)p.q + (size_t)i * p.ldq);
@@ -362,6 +414,8 @@ __global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
 // The compact head of a bias-form bf16 head: its rows (a warp each), then zeros up to a
 // multiple of 256, and below its columns of markov_w2.
 __global__ void __launch_bounds__(256) loss_gather_head(const LossPlan p) {
+  pdl_wait();
+  pdl_signal();
   const int n = (int)p.ctrl[kLossVoc];
   const int end = min(p.Vh, (n + 255) / 256 * 256), per = p.H / 8, lane = threadIdx.x % 32;
   const uint4* w = (const uint4*)p.lm_head;
@@ -385,6 +439,8 @@ __global__ void __launch_bounds__(256) loss_gather_head(const LossPlan p) {
 
 // CTA (x, y): 256 compact columns, rows 8 y ... of markov_w2.
 __global__ void __launch_bounds__(256) loss_gather_w2(const LossPlan p) {
+  pdl_wait();
+  pdl_signal();
   const int n = (int)p.ctrl[kLossVoc], end = min(p.Vh, (n + 255) / 256 * 256);
   const int j = blockIdx.x * 256 + threadIdx.x;
   if (j >= end) return;
@@ -409,10 +465,13 @@ __global__ void __launch_bounds__(256) loss_gather_w2(const LossPlan p) {
 // markov_w1's row prev (left in split 0).
 template <typename E>
 __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
+  pdl_wait();
+  pdl_signal();
   const int i = blockIdx.x;
   if (i >= (int)p.ctrl[kLossTok]) return;
   const float k = __uint_as_float(p.ctrl[kLossScale]);
   const size_t step = (size_t)p.Tp * p.Kx / 4;
+  const int splits = (int)p.ctrl[kLossSplits];
   float4* x = (float4*)(p.dxp + (size_t)i * p.Kx);
   const float lost = p.qres ? p.qres[i] : 0.f;
   const size_t row = (size_t)loss_head_row(p, p.lab[i]);
@@ -421,11 +480,11 @@ __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
   const int from = p.d_hidden ? 0 : p.Hp / 4, to = p.d_w1 ? p.Kx / 4 : p.Hp / 4;
   for (int c4 = from + threadIdx.x; c4 < to; c4 += blockDim.x) {
     float a[4] = {};
-    for (int s0 = 0; s0 < p.splits; s0 += 8) {
+    for (int s0 = 0; s0 < splits; s0 += 8) {
       float4 y[8];
 #pragma unroll
       for (int s = 0; s < 8; ++s)
-        y[s] = s0 + s < p.splits ? __ldcs(x + (s0 + s) * step + c4) : make_float4(0, 0, 0, 0);
+        y[s] = s0 + s < splits ? __ldcs(x + (s0 + s) * step + c4) : make_float4(0, 0, 0, 0);
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         a[0] += y[s].x; a[1] += y[s].y; a[2] += y[s].z; a[3] += y[s].w;
@@ -464,6 +523,8 @@ __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
 // prev in row order, each warp over its share of the rows, the warps in order.
 template <typename E>
 __global__ void __launch_bounds__(256) loss_w1_rows(const LossPlan p) {
+  pdl_wait();
+  pdl_signal();
   __shared__ bool s_seen;
   extern __shared__ float s_acc[];             // [warps][rp]
   const int n_tok = (int)p.ctrl[kLossTok], i = blockIdx.x, tid = threadIdx.x;
@@ -501,63 +562,53 @@ __global__ void __launch_bounds__(256) loss_w1_rows(const LossPlan p) {
 }  // namespace
 
 cudaError_t launch_loss_plan(const LossPlan& p) {
+  const bool f32 = p.dtype == 0;
   cudaError_t e = cudaSuccess;
+  if (f32)
+    for (int z = 0; z < p.n_zero && e == cudaSuccess; ++z)
+      e = cudaMemsetAsync(p.zero[z].p, 0, p.zero[z].bytes, p.stream);
   if (p.vlist) {
     int chunks = 0;
-    e = launch_emit_rows(p.bias, p.Vh, p.vchunk, p.vlist, &chunks, p.stream);
-    if (e != cudaSuccess) return e;
-    e = cudaMemsetAsync(p.vinv, 0xFF, sizeof(int32_t) * (size_t)p.Vh, p.stream);
-    if (e != cudaSuccess) return e;
-    loss_vocab<<<std::min(256, (p.Vh + 255) / 256), 256, 0, p.stream>>>(p, chunks);
-    if (p.wc) {
-      loss_gather_head<<<std::min(1216, (p.Vh + 7) / 8), 256, 0, p.stream>>>(p);
-      if (p.r > 0)
-        loss_gather_w2<<<dim3((p.Vh + 255) / 256, (p.r + 7) / 8), 256, 0, p.stream>>>(p);
-    }
+    if (e == cudaSuccess)
+      e = cudaMemsetAsync(p.vinv, 0xFF, sizeof(int32_t) * (size_t)p.Vh, p.stream);
+    if (e == cudaSuccess) e = launch_emit_rows(p.bias, p.Vh, p.vchunk, p.vlist, &chunks, p.stream);
+    if (e == cudaSuccess)
+      e = launch_after(loss_vocab, std::min(256, (p.Vh + 255) / 256), 256, 0, p.stream, p, chunks);
+    if (e == cudaSuccess && p.wc)
+      e = launch_after(loss_gather_head, std::min(1216, (p.Vh + 7) / 8), 256, 0, p.stream, p);
+    if (e == cudaSuccess && p.wc && p.r > 0)
+      e = launch_after(loss_gather_w2, dim3((p.Vh + 255) / 256, (p.r + 7) / 8), 256, 0, p.stream,
+                       p);
   }
-  loss_tokens<<<1, std::min(kPlanThreads, (p.T + 31) / 32 * 32), 0, p.stream>>>(p);
-  if (p.dtype == 0)
-    for (int z = 0; z < p.n_zero; ++z) {
-      e = cudaMemsetAsync(p.zero[z].p, 0, p.zero[z].bytes, p.stream);
-      if (e != cudaSuccess) return e;
-    }
-  if (p.dtype == 0)
-    loss_gather<float><<<p.Tp, 256, 0, p.stream>>>(p);
-  else
-    loss_gather<__nv_bfloat16><<<p.Tp, 256, 0, p.stream>>>(p);
-  return cudaGetLastError();
+  if (e == cudaSuccess)
+    e = launch_after(loss_tokens, 1, std::min(kPlanThreads, (p.T + 31) / 32 * 32), 0, p.stream, p);
+  if (e == cudaSuccess)
+    e = launch_after(f32 ? loss_gather<float> : loss_gather<__nv_bfloat16>, p.Tp, 256, 0, p.stream,
+                     p);
+  return e;
 }
 
 cudaError_t launch_loss_rows(const LossPlan& p) {
-  loss_rows<<<p.T, kRowsThreads, 0, p.stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(loss_rows, p.T, kRowsThreads, 0, p.stream, p);
 }
 
 cudaError_t launch_loss_dz(const LossPlan& p, int v0, int v1) {
   if (p.dtype == 0) {
     const unsigned blocks = (unsigned)std::min(64, (v1 - v0 + 255) / 256);
-    loss_dz_f32<<<dim3((unsigned)p.T, blocks), 256, 0, p.stream>>>(p, v0, v1);
-  } else {
-    const unsigned blocks = (unsigned)std::min(16, (p.Vh + 2047) / 2048);
-    loss_dz_bf16<<<dim3((unsigned)p.T, blocks), 256, 0, p.stream>>>(p);
+    return launch_after(loss_dz_f32, dim3((unsigned)p.T, blocks), 256, 0, p.stream, p, v0, v1);
   }
-  return cudaGetLastError();
+  const unsigned blocks = (unsigned)std::min(16, (p.Vh + 2047) / 2048);
+  return launch_after(loss_dz_bf16, dim3((unsigned)p.T, blocks), 256, 0, p.stream, p);
 }
 
 cudaError_t launch_loss_dx(const LossPlan& p) {
   const bool f32 = p.dtype == 0;
-  if (f32)
-    loss_dx_rows<float><<<p.T, 256, 0, p.stream>>>(p);
-  else
-    loss_dx_rows<__nv_bfloat16><<<p.T, 256, 0, p.stream>>>(p);
-  if (p.d_w1) {
-    const size_t smem = sizeof(float) * 8 * (size_t)p.rp;
-    if (f32)
-      loss_w1_rows<float><<<p.T, 256, smem, p.stream>>>(p);
-    else
-      loss_w1_rows<__nv_bfloat16><<<p.T, 256, smem, p.stream>>>(p);
-  }
-  return cudaGetLastError();
+  cudaError_t e = launch_after(f32 ? loss_dx_rows<float> : loss_dx_rows<__nv_bfloat16>, p.T, 256,
+                               0, p.stream, p);
+  if (e == cudaSuccess && p.d_w1)
+    e = launch_after(f32 ? loss_w1_rows<float> : loss_w1_rows<__nv_bfloat16>, p.T, 256,
+                     sizeof(float) * 8 * (size_t)p.rp, p.stream, p);
+  return e;
 }
 
 }  // namespace dspark

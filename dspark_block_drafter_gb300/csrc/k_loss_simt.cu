@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "loss.h"
 
 namespace dspark {
@@ -77,6 +78,8 @@ __device__ __forceinline__ void tile_product(float (&acc)[4][4], int depth, bool
 // logits (`stats`), and the logits themselves (`store`).
 __global__ void __launch_bounds__(256)
 loss_logits(const LossPlan p, int v0, int v1, bool stats, bool store) {
+  pdl_wait();
+  pdl_signal();
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
   const int m0 = blockIdx.y * kTile, j0 = v0 + blockIdx.x * kTile;
   if (m0 >= n_tok || j0 >= n_voc) return;
@@ -135,6 +138,8 @@ loss_logits(const LossPlan p, int v0, int v1, bool stats, bool store) {
 
 // dX of vocabulary columns [v0, v1): split blockIdx.z of their range.
 __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1, bool first) {
+  pdl_wait();
+  pdl_signal();
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
   const int m0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
   if (m0 >= n_tok) return;
@@ -175,6 +180,8 @@ __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1,
 
 // dW of vocabulary columns [v0, v1).
 __global__ void __launch_bounds__(256) loss_dw(const LossPlan p, int v0, int v1) {
+  pdl_wait();
+  pdl_signal();
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
   const int j0 = v0 + blockIdx.y * kTile, c0 = blockIdx.x * kTile;
   const bool head = c0 < p.Hp;
@@ -218,20 +225,17 @@ int loss_simt_splits(int T, int Kx, int cols) {
 
 cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stats, bool store) {
   const dim3 grid((v1 - v0 + kTile - 1) / kTile, (p.T + kTile - 1) / kTile);
-  loss_logits<<<grid, 256, 0, p.stream>>>(p, v0, v1, stats, store);
-  return cudaGetLastError();
+  return launch_after(loss_logits, grid, 256, 0, p.stream, p, v0, v1, stats, store);
 }
 
 cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first) {
   const dim3 grid(p.Kx / kTile, (p.T + kTile - 1) / kTile, p.splits);
-  loss_dx<<<grid, 256, 0, p.stream>>>(p, v0, v1, first);
-  return cudaGetLastError();
+  return launch_after(loss_dx, grid, 256, 0, p.stream, p, v0, v1, first);
 }
 
 cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1) {
   const dim3 grid(p.Kx / kTile, (v1 - v0 + kTile - 1) / kTile);
-  loss_dw<<<grid, 256, 0, p.stream>>>(p, v0, v1);
-  return cudaGetLastError();
+  return launch_after(loss_dw, grid, 256, 0, p.stream, p, v0, v1);
 }
 
 }  // namespace dspark

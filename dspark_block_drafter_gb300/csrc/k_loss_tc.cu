@@ -75,7 +75,9 @@ struct TcArgs {
   int first;           // dX: the first piece (later ones add)
   int n_head, n_markov;  // 256-column tiles of X's two parts that are computed
   int chunked;         // dX: lm_head rows are whole 64-column chunks
-  int zero0, zero1;    // the share of the plan's zeros this launch writes, in 1/64
+  // the share of the plan's zeros this launch writes, in 1/64: of the plain ones (which have
+  // to be there before dW), and of the masked rows
+  int zero0, zero1, keep0, keep1;
 };
 
 // One unit of work: a tile of the result and a range of K-blocks.
@@ -86,19 +88,21 @@ struct Unit {
 };
 
 template <int MODE, int CG>
-__device__ __forceinline__ int unit_count(const TcArgs& g, int n_tok, int n_voc) {
+__device__ __forceinline__ int unit_count(const TcArgs& g, int n_tok, int n_voc,
+                                          int splits) {
   const int mt = (n_tok + kTileM * CG - 1) / (kTileM * CG);
   const int cols = max(0, min(g.v1, n_voc) - g.v0);
   const int nt = g.n_head + g.n_markov;
   if (MODE == kLogits) return mt * ((cols + kTileN - 1) / kTileN);
-  if (MODE == kDx) return mt * nt * g.p.splits;
+  if (MODE == kDx) return mt * nt * splits;
   return (cols + kTileM * CG - 1) / (kTileM * CG) * nt;
 }
 
 constexpr int kRowGroup = 24;     // M tiles whose rows of X are kept in L2 together
 
 template <int MODE, int CG>
-__device__ __forceinline__ Unit unit_at(const TcArgs& g, int u, int n_tok, int n_voc) {
+__device__ __forceinline__ Unit unit_at(const TcArgs& g, int u, int n_tok, int n_voc,
+                                        int splits) {
   Unit t;
   const int mt = (n_tok + kTileM * CG - 1) / (kTileM * CG);
   const int cols = max(0, min(g.v1, n_voc) - g.v0);
@@ -121,8 +125,8 @@ __device__ __forceinline__ Unit unit_at(const TcArgs& g, int u, int n_tok, int n
     const int in = u % (mt * nt);
     t.m = in / nt * kTileM * CG;
     t.n = in % nt;
-    t.kb0 = (int)((long long)nkb * t.split / g.p.splits);
-    t.kb1 = (int)((long long)nkb * (t.split + 1) / g.p.splits);
+    t.kb0 = (int)((long long)nkb * t.split / splits);
+    t.kb1 = (int)((long long)nkb * (t.split + 1) / splits);
   } else {
     t.m = u / nt * kTileM * CG;
     t.n = u % nt;
@@ -164,7 +168,8 @@ __device__ __forceinline__ void write_zeros(const TcArgs& g, int lane) {
     const LossZero& q = g.p.zero[z];
     // items: rows, or 16-byte vectors (and the odd bytes, all fewer than 16, at the end)
     const long long items = q.keep ? (long long)(q.bytes / q.row_bytes) : (long long)(q.bytes / 16);
-    const long long lo = items * g.zero0 / 64, n = items * g.zero1 / 64 - lo;
+    const int z0 = q.keep ? g.keep0 : g.zero0, z1 = q.keep ? g.keep1 : g.zero1;
+    const long long lo = items * z0 / 64, n = items * z1 / 64 - lo;
     const long long a = lo + n * part / parts, b = lo + n * (part + 1) / parts;
     if (q.keep) {
       const int per = q.row_bytes / 16;
@@ -180,7 +185,7 @@ __device__ __forceinline__ void write_zeros(const TcArgs& g, int lane) {
       uint4* v = reinterpret_cast<uint4*>(q.p);
 #pragma unroll 4
       for (long long k = a + lane; k < b; k += 32) v[k] = none;
-      if (g.zero1 == 64 && part == 0 && lane < (int)(q.bytes % 16)) q.p[items * 16 + lane] = 0;
+      if (z1 == 64 && z0 < 64 && part == 0 && lane < (int)(q.bytes % 16)) q.p[items * 16 + lane] = 0;
     }
   }
 }
@@ -235,8 +240,11 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
   const uint32_t tmem = *tmem_slot;
   const uint32_t full0 = CG == 2 ? ptx::mapa_shared(ptx::smem_u32(full), 0) : 0;
   const uint32_t acc_empty0 = CG == 2 ? ptx::mapa_shared(ptx::smem_u32(acc_empty), 0) : 0;
+  pdl_wait();
+  pdl_signal();
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc];
-  const int units = unit_count<MODE, CG>(g, n_tok, n_voc);
+  const int splits = MODE == kDx ? (int)p.ctrl[kLossSplits] : 1;
+  const int units = unit_count<MODE, CG>(g, n_tok, n_voc, splits);
   const int u0 = blockIdx.x / CG, step = gridDim.x / CG;
 
   auto give_up = [&]() {
@@ -268,7 +276,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
         }
       };
       for (int u = u0; u < units && ok; u += step) {
-        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc);
+        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc, splits);
         const int ma = t.m + (int)rank * kTileM;             // this CTA's rows of M
         const int half = (int)rank * (kTileN / CG);          // and its share of N
         if (MODE == kLogits) {
@@ -376,7 +384,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       using Mn = std::true_type;
       using K = std::false_type;
       for (int u = u0; u < units; u += step) {
-        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc);
+        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc, splits);
         int c0 = 0;
         const bool markov = MODE != kLogits && column_tile(g, t.n, &c0);
         for (int kb = t.kb0, part = 0; part == 0 || kb < t.kb1; ++part, ++local) {
@@ -419,7 +427,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       ptx::mbar_wait(drain, 0, kWaitBudget, nullptr);
     }
   } else if (warp == kEpiWarps + 2) {
-    if (MODE != kDw && g.zero1 > g.zero0) write_zeros(g, lane);
+    if (g.zero1 > g.zero0 || g.keep1 > g.keep0) write_zeros(g, lane);
   } else {
     // ---------------------------------------------------------------- epilogue
     const int quad = warp % 4, half = warp / 4;       // lanes and columns of this warp
@@ -440,14 +448,16 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       __syncwarp();
       if (lane == 0) {
         if (CG == 2)
-          ptx::mbar_arrive_cluster(acc_empty0 + (local & 1) * 8);
+          // (not a cluster-wide release: that waits for the last tile's stores, and held the
+          // next products up by half their time when K is short)
+          ptx::mbar_arrive_cluster_tmem(acc_empty0 + (local & 1) * 8);
         else
           ptx::mbar_arrive(&acc_empty[local & 1]);
       }
       ++local;
     };
     for (int u = u0; u < units && ok; u += step) {
-      const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc);
+      const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc, splits);
       const int m = t.m + (int)rank * kTileM + quad * 32 + lane;   // this thread's row of M
       if (MODE == kLogits) {
         const bool live = m < n_tok;
@@ -712,13 +722,15 @@ cudaError_t launch(const TcArgs& g, long long tiles) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = g.p.stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, loss_product<MODE, CG>, maps, g, stages);
 }
 
@@ -729,23 +741,12 @@ int row_tiles(int T) { return (T + 255) / 256; }   // (one tile of either height
 
 }  // namespace
 
-// Splits of the vocabulary for dX.  A unit costs its K-blocks and about 12 K-blocks' time
-// for filling the pipeline and writing its partial result; the CTAs take the units in
-// waves.  The count with the least total is taken.
-int loss_tc_splits(int T, int H, int r, int cols) {
-  const long long tiles = (long long)row_tiles(T) * ((H + kTileN - 1) / kTileN +
-                                                     (r + kTileN - 1) / kTileN);
-  const int units = single(T) ? 152 : 76, nkb = (cols + kBlockK - 1) / kBlockK;
-  int best = 1;
-  double best_cost = 1e30;
-  for (int s = 1; s <= 64 && s * 8 <= std::max(8, nkb); ++s) {
-    const double cost = (double)((tiles * s + units - 1) / units) * ((double)nkb / s + 12.0);
-    if (cost < best_cost * 0.999) {
-      best = s;
-      best_cost = cost;
-    }
-  }
-  return best;
+// The most splits of the vocabulary that loss_pick_splits may take: eight units for each CTA
+// (or pair), at least 6.
+int loss_tc_splits(int T, int Hp, int rp) {
+  const int tiles = row_tiles(T) * ((Hp + kTileN - 1) / kTileN + (rp + kTileN - 1) / kTileN);
+  const int units = single(T) ? 152 : 76;
+  return std::max(6, std::min(64, (8 * units + tiles - 1) / std::max(1, tiles)));
 }
 
 cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats, bool store) {
@@ -754,7 +755,11 @@ cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats,
   g.v0 = v0;
   g.v1 = v1;
   g.want = stats ? kWantStats | (store ? kWantGap : 0) : kWantGrad;
-  if (stats && p.n_zero > 0) g.zero1 = p.d_hidden || p.d_w1 ? 32 : 64;
+  if (stats && p.n_zero > 0) {
+    const bool dx = p.d_hidden || p.d_w1;
+    g.zero1 = dx ? 32 : 64;
+    g.keep1 = dx ? 22 : 40;
+  }
   const long long tiles = (long long)row_tiles(p.T) * ((v1 - v0 + kTileN - 1) / kTileN);
   return single(p.T) ? launch<kLogits, 1>(g, tiles) : launch<kLogits, 2>(g, tiles);
 }
@@ -769,6 +774,8 @@ cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first) {
   if (first && p.n_zero > 0) {
     g.zero0 = 32;
     g.zero1 = 64;
+    g.keep0 = 22;
+    g.keep1 = 40;
   }
   g.n_head = p.d_hidden ? (p.Hp + kTileN - 1) / kTileN : 0;
   g.n_markov = p.d_w1 ? (p.rp + kTileN - 1) / kTileN : 0;
@@ -781,6 +788,11 @@ cudaError_t launch_loss_dw_tc(const LossPlan& p, int v0, int v1) {
   g.p = p;
   g.v0 = v0;
   g.v1 = v1;
+  if (v0 == 0 && p.n_zero > 0) {
+    g.zero0 = g.zero1 = 64;
+    g.keep0 = 40;
+    g.keep1 = 64;
+  }
   g.n_head = p.d_lm_head ? (p.Hp + kTileN - 1) / kTileN : 0;
   g.n_markov = p.d_w2 ? (p.rp + kTileN - 1) / kTileN : 0;
   const long long tiles = (long long)((v1 - v0 + 255) / 256) * (g.n_head + g.n_markov);

@@ -1,22 +1,29 @@
 // The norms around the end of a drafter block, and their gradient.
 //
-//   ry = 1 / sqrt(mean(y^2) + eps)   u = y ry (o + w_post)     (u = y without w_post)
-//   x' = x + s g u                   rx = 1 / sqrt(mean(x'^2) + eps)
-//   h  = x' rx (o + w_pre)
+//   ry = 1 / sqrt(mean(y^2) + eps)   yn = y ry   p = s g yn (o + w_post)   (p = s g y without)
+//   x' = x + p                       rx = 1 / sqrt(mean(x'^2) + eps)   xn = x' rx
+//   h  = xn (o + w_pre)
 //
-// With a = dh (o + w_pre) and xn = x' rx, yn = y ry:
+// With a = dh (o + w_pre):
 //   dx' = d_x_out + rx (a - xn mean(a xn))      dx = dx'     dw_pre = sum_t dh xn
-//   dg = s dx' u                                du = s g dx'  dw_post = sum_t du yn
+//   dg = s dx' yn (o + w_post)                  du = s g dx'  dw_post = sum_t du yn
 //   b = du (o + w_post)                         dy = ry (b - yn mean(b yn))
+// where b yn = p dx', so that its mean too follows from sums over the row that need no dx':
+//   sum p dx' = sum p d_x_out + rx sum p a - rx^2 mean(a xn) sum p x'
+// A row takes two sums over the CTA: y^2, then the other five at once.
 //
-// Bound by memory: each input is read once and each output written once, a row stays in
-// registers (eight elements a thread) between its reductions, and everything is fp32.
+// Bound by memory: each input is read once and each output written once.  A CTA takes rows in
+// turn, eight elements a thread.  Each thread copies its own elements of the next row to
+// shared memory (cp.async) while it works on this one's, which it reads there again after
+// each sum instead of holding them in registers: at 64 registers two rows of 4096 are at
+// work on an SM and two more on their way.  Everything is computed in fp32.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "train.h"
 
 namespace dspark {
@@ -24,235 +31,544 @@ namespace dspark {
 namespace {
 
 constexpr int kPer = 8;               // elements of a row per thread
-constexpr int kNormUnit = 16;         // rows of one gate row that a CTA takes at a time
+
+// Rows of one gate row that a CTA takes at a time: 16 in a large batch (their gate gradient
+// is summed in registers), fewer where that would leave SMs without rows.
+__host__ __device__ int norm_unit(int T) { return T >= 16 * 512 ? 16 : T >= 1024 ? T / 512 : 1; }
 
 int row_threads(int H) { return (H + kPer * 32 - 1) / (kPer * 32) * 32; }
 
-// Column of element e of thread `tid`: vectors of VEC consecutive elements, the threads'
-// vectors side by side.
-template <int VEC>
-__device__ __forceinline__ int column(int e) {
-  return ((e / VEC) * (int)blockDim.x + (int)threadIdx.x) * VEC + e % VEC;
+// Two fp32 values in one 64-bit register, for the packed arithmetic (half the instructions).
+struct F2 {
+  unsigned long long v;
+  __device__ __forceinline__ F2() {}
+  __device__ __forceinline__ F2(float lo, float hi) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  }
+  explicit __device__ __forceinline__ F2(float x) : F2(x, x) {}
+  __device__ __forceinline__ float lo() const {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return a;
+  }
+  __device__ __forceinline__ float hi() const {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return b;
+  }
+};
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
 }
 
+__device__ __forceinline__ F2 pair_of(const float* p) { return F2(p[0], p[1]); }
+__device__ __forceinline__ F2 pair_of(const __nv_bfloat16* p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  return F2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// A thread's elements of one row of one tensor, as they lie in memory: vectors of VEC
+// consecutive elements, the threads' vectors side by side.
 template <typename E, int VEC>
-__device__ __forceinline__ void load_row(float (&r)[kPer], const E* p, int H) {
+struct Part {
   struct alignas(sizeof(E) * VEC) Vec { E e[VEC]; };
+  Vec v[kPer / VEC];
+
+  static __device__ __forceinline__ int column(int e) {
+    return ((e / VEC) * (int)blockDim.x + (int)threadIdx.x) * VEC + e % VEC;
+  }
+  __device__ __forceinline__ void load(const void* base, size_t row, int H) {
+    const E* p = (const E*)base + row * H;
 #pragma unroll
-  for (int q = 0; q < kPer; q += VEC) {
-    const int c = column<VEC>(q);
-    if (c < H) {
-      const Vec v = *reinterpret_cast<const Vec*>(p + c);
+    for (int q = 0; q < kPer / VEC; ++q) {
+      const int c = column(q * VEC);
+      if (c < H) {
+        v[q] = *reinterpret_cast<const Vec*>(p + c);
+      } else {                                // (zeros past the row)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) r[q + j] = to_f32(v.e[j]);
+        for (int j = 0; j < VEC; ++j) v[q].e[j] = (E)0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int e) const { return to_f32(v[e / VEC].e[e % VEC]); }
+  // elements 2 q and 2 q + 1
+  __device__ __forceinline__ void set(int q, F2 x) {
+    if constexpr (sizeof(E) == 2 && VEC > 1) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x.lo(), x.hi());
+      *reinterpret_cast<__nv_bfloat162*>(&v[2 * q / VEC].e[2 * q % VEC]) = b;
     } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) r[q + j] = 0.f;
+      v[2 * q / VEC].e[2 * q % VEC] = (E)x.lo();
+      v[(2 * q + 1) / VEC].e[(2 * q + 1) % VEC] = (E)x.hi();
     }
   }
-}
-
-template <typename E, int VEC>
-__device__ __forceinline__ void store_row(E* p, const float (&r)[kPer], int H) {
-  struct alignas(sizeof(E) * VEC) Vec { E e[VEC]; };
-#pragma unroll
-  for (int q = 0; q < kPer; q += VEC) {
-    const int c = column<VEC>(q);
-    if (c >= H) continue;
-    Vec v;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) v.e[j] = (E)r[q + j];
-    *reinterpret_cast<Vec*>(p + c) = v;
+  // stores the vectors that the pair ending in element e completes
+  __device__ __forceinline__ void put(void* base, size_t row, int H, int e) const {
+    E* p = (E*)base + row * H;
+    if constexpr (VEC == 1) {
+      if (column(e - 1) < H) *reinterpret_cast<Vec*>(p + column(e - 1)) = v[e - 1];
+      if (column(e) < H) *reinterpret_cast<Vec*>(p + column(e)) = v[e];
+    } else {
+      const int q = e / VEC, c = column(q * VEC);
+      if (e % VEC == VEC - 1 && c < H) *reinterpret_cast<Vec*>(p + c) = v[q];
+    }
   }
-}
-
-// Sums of two values over the CTA, in a fixed order.  `s` holds two buffers, taken in
-// turn, so that one barrier a sum is enough.
-struct RowSum {
-  float2 (*s)[32];
-  int turn;
-  __device__ float2 operator()(float a, float b) {
+  static __device__ __forceinline__ void store(void* base, size_t row, int H,
+                                               const float (&x)[kPer]) {
+    E* p = (E*)base + row * H;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-    }
-    const int warps = blockDim.x / 32;
-    if (warps == 1) return make_float2(a, b);
-    if (threadIdx.x % 32 == 0) s[turn][threadIdx.x / 32] = make_float2(a, b);
-    __syncthreads();
-    const int lane = threadIdx.x % 32;
-    const float2 v = lane < warps ? s[turn][lane] : make_float2(0.f, 0.f);
-    turn ^= 1;
-    a = v.x;
-    b = v.y;
+    for (int q = 0; q < kPer / VEC; ++q) {
+      const int c = column(q * VEC);
+      if (c >= H) continue;
+      Vec o;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+      for (int j = 0; j < VEC; ++j) o.e[j] = (E)x[q * VEC + j];
+      *reinterpret_cast<Vec*>(p + c) = o;
     }
-    return make_float2(a, b);
   }
 };
 
-template <typename E, int VEC>
-__global__ void __launch_bounds__(1024) block_norm(const NormArgs a) {
-  __shared__ float2 s_sum[2][32];
-  RowSum sum{s_sum, 0};
-  const int t = blockIdx.x, H = a.H;
-  const float inv_h = 1.f / (float)H;
-  float x[kPer];
-  load_row<E, VEC>(x, (const E*)a.x + (size_t)t * H, H);
-  if (a.y) {
-    float u[kPer];
-    load_row<E, VEC>(u, (const E*)a.y + (size_t)t * H, H);
-    float g[kPer];
-    if (a.gate) load_row<E, VEC>(g, (const E*)a.gate + (size_t)(t / a.span) * H, H);
-    if (a.w_post) {
-      float w[kPer];
-      load_row<E, VEC>(w, (const E*)a.w_post, H);
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) ss += u[e] * u[e];
-      const float ry = rsqrtf(sum(ss, 0.f).x * inv_h + a.eps);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) u[e] = u[e] * ry * (a.offset + w[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) x[e] += a.scale * (a.gate ? g[e] * u[e] : u[e]);
-  }
-  if (a.x_out) store_row<E, VEC>((E*)a.x_out + (size_t)t * H, x, H);
-  float w[kPer];
-  load_row<E, VEC>(w, (const E*)a.w_pre, H);
-  float ss = 0.f;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) ss += x[e] * x[e];   // (0 past the row)
-  const float rx = rsqrtf(sum(ss, 0.f).x * inv_h + a.eps);
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) x[e] = x[e] * rx * (a.offset + w[e]);
-  store_row<E, VEC>((E*)a.h + (size_t)t * H, x, H);
-}
+// The current and the next row of N tensors, and the two weight vectors (w_post, w_pre).
+// Vectors of 16 bytes go through shared memory, each thread's own 16 bytes to its own place
+// (so no barrier is needed); without that alignment a row is loaded into registers when its
+// turn comes, and the weights stay there.
+template <typename E, int VEC, int N>
+struct Rows {
+  static constexpr bool kAsync = VEC > 1;
+  static constexpr int kVecs = kPer / VEC;
+  using P = Part<E, VEC>;
+  uint4* slots;                               // [2 N + 2][kVecs][threads]
+  int turn = 0;
+  P held[kAsync ? 1 : N + 2];
 
-// A unit is up to kNormUnit consecutive rows of one gate row (one row without a gate);
-// CTAs take units in turn and keep their column sums in registers.
+  static size_t smem(int threads) {
+    return kAsync ? (size_t)(2 * N + 2) * kVecs * threads * sizeof(uint4) : 0;
+  }
+  __device__ __forceinline__ uint4* slot(int stage, int n, int q) const {
+    return slots + ((stage * N + n) * kVecs + q) * blockDim.x + threadIdx.x;
+  }
+  __device__ __forceinline__ void init(uint4* smem_base, const NormArgs& a) {
+    slots = smem_base;
+    if constexpr (kAsync)
+      for (int i = 0; i < 2 * N * kVecs; ++i)   // (zeros past the row, for good)
+        slots[i * blockDim.x + threadIdx.x] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const void* base = w ? a.w_pre : a.w_post;
+      if (!base) continue;
+      P p;
+      p.load(base, 0, a.H);
+      if constexpr (kAsync) {
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q)
+          slots[((2 * N + w) * kVecs + q) * blockDim.x + threadIdx.x] =
+              *reinterpret_cast<const uint4*>(&p.v[q]);
+      } else {
+        held[N + w] = p;
+      }
+    }
+  }
+  __device__ __forceinline__ P weight(int w) const {
+    if constexpr (kAsync) {
+      P p;
+#pragma unroll
+      for (int q = 0; q < kVecs; ++q)
+        *reinterpret_cast<uint4*>(&p.v[q]) =
+            slots[((2 * N + w) * kVecs + q) * blockDim.x + threadIdx.x];
+      return p;
+    } else {
+      return held[N + w];
+    }
+  }
+  // start on a row of tensor n (the next one when async)
+  __device__ __forceinline__ void fetch(int n, const void* base, size_t row, int H) {
+    if constexpr (kAsync) {
+      const E* p = (const E*)base + row * H;
+#pragma unroll
+      for (int q = 0; q < kVecs; ++q) {
+        const int c = P::column(q * VEC);
+        if (c < H)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           (uint32_t)__cvta_generic_to_shared(slot(turn ^ 1, n, q))),
+                       "l"(p + c)
+                       : "memory");
+      }
+    } else {
+      held[n].load(base, row, H);
+    }
+  }
+  __device__ __forceinline__ void commit() {
+    if (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // the fetched row becomes the current one
+  __device__ __forceinline__ void next() {
+    if (kAsync) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    turn ^= 1;
+  }
+  // elements [4 c, 4 c + 4) of the current row of tensor n, or of a weight vector
+  struct alignas(4 * sizeof(E)) Four { E e[4]; };
+  __device__ __forceinline__ void four(F2 (&x)[2], int n, int c) const {
+    place(x, (turn * N + n) * kVecs, n, c);
+  }
+  __device__ __forceinline__ void weight_four(F2 (&x)[2], int w, int c) const {
+    place(x, (2 * N + w) * kVecs, N + w, c);
+  }
+  __device__ __forceinline__ void place(F2 (&x)[2], int vec0, int h, int c) const {
+    if constexpr (kAsync) {
+      const uint4* v = slots + (vec0 + 4 * c / VEC) * blockDim.x + threadIdx.x;
+      const Four f = *(reinterpret_cast<const Four*>(v) + 4 * c % VEC / 4);
+      x[0] = pair_of(f.e);
+      x[1] = pair_of(f.e + 2);
+    } else {
+      x[0] = F2(held[h][4 * c], held[h][4 * c + 1]);
+      x[1] = F2(held[h][4 * c + 2], held[h][4 * c + 3]);
+    }
+  }
+  __device__ __forceinline__ P get(int n) const {
+    if constexpr (kAsync) {
+      P p;
+#pragma unroll
+      for (int q = 0; q < kVecs; ++q)
+        *reinterpret_cast<uint4*>(&p.v[q]) = *slot(turn, n, q);
+      return p;
+    } else {
+      return held[n];
+    }
+  }
+};
+
+// Sums of up to five values over the CTA, in a fixed order.  Two buffers taken in turn make
+// one barrier a sum enough.
+struct RowSum {
+  float (*s)[32][5];
+  int turn;
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xFFFFFFFFu, v[j], o);
+    const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
+    if (warps == 1) return;
+    if (lane == 0)
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[turn][threadIdx.x / 32][j] = v[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = lane < warps ? s[turn][lane][j] : 0.f;
+    turn ^= 1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xFFFFFFFFu, v[j], o);
+  }
+};
+
+extern __shared__ uint4 norm_smem[];
+
 template <typename E, int VEC>
-__global__ void __launch_bounds__(1024) block_norm_backward(const NormArgs a, int units,
-                                                            int per_span) {
-  __shared__ float2 s_sum[2][32];
+__global__ void __launch_bounds__(1024, 1) block_norm(const NormArgs a) {
+  using P = Part<E, VEC>;
+  __shared__ float s_sum[2][32][5];
   RowSum sum{s_sum, 0};
+  pdl_wait();
+  pdl_signal();
   const int H = a.H;
   const float inv_h = 1.f / (float)H;
-  float dw_pre[kPer] = {}, dw_post[kPer] = {};
-  for (int un = blockIdx.x; un < units; un += gridDim.x) {
-    const int row_g = a.gate ? un / per_span : un;
-    const int t0 = a.gate ? row_g * a.span + un % per_span * kNormUnit : un;
-    const int t1 = a.gate ? min(min(a.T, (row_g + 1) * a.span), t0 + kNormUnit) : un + 1;
-    float g[kPer], dg[kPer] = {};
-    if (a.gate) load_row<E, VEC>(g, (const E*)a.gate + (size_t)row_g * H, H);
-    for (int t = t0; t < t1; ++t) {
-      const size_t at = (size_t)t * H;
-      float x[kPer], y[kPer], d[kPer], dh[kPer], w[kPer];
-      load_row<E, VEC>(x, (const E*)a.x + at, H);
-      load_row<E, VEC>(dh, (const E*)a.d_h + at, H);
-      if (a.d_x_out) load_row<E, VEC>(d, (const E*)a.d_x_out + at, H);
-      float ry = 1.f;
-      if (a.y) {
-        load_row<E, VEC>(y, (const E*)a.y + at, H);
-        if (a.w_post) {
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) ss += y[e] * y[e];
-          ry = rsqrtf(sum(ss, 0.f).x * inv_h + a.eps);
-          load_row<E, VEC>(w, (const E*)a.w_post, H);
-        }
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          y[e] *= ry;                                   // yn
-          const float u = a.w_post ? y[e] * (a.offset + w[e]) : y[e];
-          x[e] += a.scale * (a.gate ? g[e] * u : u);    // x'
-        }
-      }
-      float wp[kPer];
-      load_row<E, VEC>(wp, (const E*)a.w_pre, H);
-      float ss = 0.f, ax = 0.f;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        ss += x[e] * x[e];
-        ax += dh[e] * (a.offset + wp[e]) * x[e];
-      }
-      const float2 r = sum(ss, ax);
-      const float rx = rsqrtf(r.x * inv_h + a.eps);
-      const float mean = r.y * inv_h * rx;              // mean(a xn)
-      float by = 0.f;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const float xn = x[e] * rx;
-        dw_pre[e] += dh[e] * xn;
-        const float v = rx * (dh[e] * (a.offset + wp[e]) - xn * mean);
-        x[e] = a.d_x_out ? d[e] + v : v;                // dx'
-      }
-      store_row<E, VEC>((E*)a.d_x + at, x, H);
-      if (!a.y) continue;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const float ow = a.w_post ? a.offset + w[e] : 1.f;
-        if (a.gate) dg[e] += a.scale * x[e] * (y[e] * ow);
-        const float du = a.scale * (a.gate ? g[e] * x[e] : x[e]);
-        dw_post[e] += du * y[e];
-        x[e] = du * ow;                                 // b
-        by += x[e] * y[e];
-      }
-      if (a.w_post) {
-        const float mb = sum(by, 0.f).x * inv_h;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) x[e] = ry * (x[e] - y[e] * mb);
-      }
-      store_row<E, VEC>((E*)a.d_y + at, x, H);
+  Rows<E, VEC, 3> rows;                       // x, y, gate
+  rows.init(norm_smem, a);
+  auto fetch = [&](int t) {
+    if (t < a.T) {
+      rows.fetch(0, a.x, t, H);
+      if (a.y) rows.fetch(1, a.y, t, H);
+      if (a.gate) rows.fetch(2, a.gate, t / a.span, H);
     }
-    if (a.gate) {
-      if (per_span == 1)
-        store_row<E, VEC>((E*)a.d_gate + (size_t)row_g * H, dg, H);
-      else
+    rows.commit();
+  };
+  if (rows.kAsync) fetch(blockIdx.x);
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    if (!rows.kAsync) fetch(t);
+    rows.next();
+    if (rows.kAsync) fetch(t + gridDim.x);
+    float x[kPer];
+    {
+      const P px = rows.get(0);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          if (column<VEC>(e) < H) a.gate_part[(size_t)un * H + column<VEC>(e)] = dg[e];
+      for (int e = 0; e < kPer; ++e) x[e] = px[e];
+    }
+    if (a.y) {
+      float f = a.scale;
+      if (a.w_post) {
+        const P py = rows.get(1);
+        float ss[1] = {};
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) ss[0] += py[e] * py[e];
+        sum(ss);
+        f *= rsqrtf(ss[0] * inv_h + a.eps);
+      }
+      const P py = rows.get(1);
+      P pg, wo;
+      if (a.gate) pg = rows.get(2);
+      if (a.w_post) wo = rows.weight(0);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        float u = py[e];
+        if (a.w_post) u *= a.offset + wo[e];
+        if (a.gate) u *= pg[e];
+        x[e] += f * u;
+      }
+    }
+    if (a.x_out) P::store(a.x_out, t, H, x);
+    float ss[1] = {};
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) ss[0] += x[e] * x[e];     // (0 past the row)
+    sum(ss);
+    const float rx = rsqrtf(ss[0] * inv_h + a.eps);
+    const P wi = rows.weight(1);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = x[e] * rx * (a.offset + wi[e]);
+    P::store(a.h, t, H, x);
+  }
+}
+
+// A unit is up to norm_unit(T) consecutive rows of one gate row (one row without shared gate
+// rows); a CTA takes units in turn and keeps its column sums in registers.
+// GATE: 0 none, 1 a gate row for each row, 2 shared gate rows, whose gradients are sums too.
+// FULL: y, w_post and d_x_out are all there (else what is there is looked up).
+template <typename E, int VEC, int GATE, bool FULL>
+__global__ void __launch_bounds__(1024, 1) block_norm_backward(const NormArgs a, int units,
+                                                               int per_span) {
+  using P = Part<E, VEC>;
+  constexpr bool kShared = GATE == 2;
+  const bool has_y = FULL || a.y, has_post = FULL || a.w_post, has_up = FULL || a.d_x_out;
+  __shared__ float s_sum[2][32][5];
+  RowSum sum{s_sum, 0};
+  pdl_wait();
+  pdl_signal();
+  const int H = a.H;
+  const float inv_h = 1.f / (float)H;
+  const F2 off(a.offset), zero2(0.f);
+  F2 dw_pre[kPer / 2], dw_post[kPer / 2], dg[kShared ? kPer / 2 : 1];
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) {
+    dw_pre[e] = dw_post[e] = zero2;
+    if (kShared) dg[e] = zero2;
+  }
+  Rows<E, VEC, 5> rows;                       // x, dh, y, d_x_out, gate
+  rows.init(norm_smem, a);
+  // row t of rows [t, t1) of unit un
+  int un = blockIdx.x, t = 0, t1 = 0;
+  auto settle = [&]() {
+    if (!kShared) {
+      t = un;
+      t1 = un + 1;
+      return;
+    }
+    const int unit_rows = norm_unit(a.T);
+    while (un < units) {
+      const int row_g = un / per_span;
+      t = row_g * a.span + un % per_span * unit_rows;
+      t1 = min(min(a.T, (row_g + 1) * a.span), t + unit_rows);
+      if (t < t1) break;
+      // (the last gate row's last units may hold no row: their part of d_gate is zero)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        if (P::column(e) < H) a.gate_part[(size_t)un * H + P::column(e)] = 0.f;
+      un += gridDim.x;
+    }
+  };
+  auto fetch = [&]() {
+    if (un < units) {
+      rows.fetch(0, a.x, t, H);
+      rows.fetch(1, a.d_h, t, H);
+      if (has_y) rows.fetch(2, a.y, t, H);
+      if (has_up) rows.fetch(3, a.d_x_out, t, H);
+      if (GATE) rows.fetch(4, a.gate, kShared ? un / per_span : t, H);
+    }
+    rows.commit();
+  };
+  settle();
+  if (rows.kAsync) fetch();
+  while (un < units) {
+    const int row = t, unit = un;
+    if (!rows.kAsync) fetch();
+    rows.next();
+    if (++t == t1) {
+      un += gridDim.x;
+      settle();
+    }
+    if (rows.kAsync) fetch();
+    float f = a.scale, ry = 1.f;              // p = f g y (o + w_post)
+    if (has_post) {
+      F2 s2 = zero2;
+#pragma unroll
+      for (int c = 0; c < kPer / 4; ++c) {
+        F2 y[2];
+        rows.four(y, 2, c);
+        s2 = fma2(y[0], y[0], s2);
+        s2 = fma2(y[1], y[1], s2);
+      }
+      float ss[1] = {s2.lo() + s2.hi()};
+      sum(ss);
+      ry = rsqrtf(ss[0] * inv_h + a.eps);
+      f *= ry;
+    }
+    // Four elements at a time, read from shared memory when their turn comes (the fences keep
+    // the compiler from reading ahead, which took more registers than there are).
+    F2 v2[5] = {zero2, zero2, zero2, zero2, zero2};   // x'^2, a x', p x', p a, p d_x_out
+    const F2 f2(f);
+#pragma unroll
+    for (int c = 0; c < kPer / 4; ++c) {
+      F2 x[2], y[2], g[2], h[2], d[2], wo[2], wi[2];
+      asm volatile("" ::: "memory");
+      rows.four(x, 0, c);
+      rows.four(h, 1, c);
+      rows.weight_four(wi, 1, c);
+      if (has_y) rows.four(y, 2, c);
+      if (has_up) rows.four(d, 3, c);
+      if (GATE) rows.four(g, 4, c);
+      if (has_post) rows.weight_four(wo, 0, c);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        F2 p = zero2;
+        if (has_y) {
+          p = f2 * y[j];
+          if (has_post) p = p * (off + wo[j]);
+          if (GATE) p = p * g[j];
+        }
+        const F2 xx = x[j] + p, aa = h[j] * (off + wi[j]);
+        v2[0] = fma2(xx, xx, v2[0]);
+        v2[1] = fma2(aa, xx, v2[1]);
+        v2[2] = fma2(p, xx, v2[2]);
+        v2[3] = fma2(p, aa, v2[3]);
+        if (has_up) v2[4] = fma2(p, d[j], v2[4]);
+      }
+    }
+    float v[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) v[j] = v2[j].lo() + v2[j].hi();
+    sum(v);
+    const float rx = rsqrtf(v[0] * inv_h + a.eps);
+    const float mean = v[1] * inv_h * rx;                       // mean(a xn)
+    const float mb = (v[4] + rx * v[3] - rx * rx * mean * v[2]) * inv_h;   // mean(b yn)
+    const F2 rx2(rx), ry2(ry), m2(-mean), mb2(-mb), s2(a.scale);
+    P o_dx, o_dy, o_dg;
+#pragma unroll
+    for (int c = 0; c < kPer / 4; ++c) {
+      F2 x[2], y[2], g[2], h[2], d[2], wo[2], wi[2];
+      asm volatile("" ::: "memory");
+      rows.four(x, 0, c);
+      rows.four(h, 1, c);
+      rows.weight_four(wi, 1, c);
+      if (has_y) rows.four(y, 2, c);
+      if (has_up) rows.four(d, 3, c);
+      if (GATE) rows.four(g, 4, c);
+      if (has_post) rows.weight_four(wo, 0, c);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int q = 2 * c + j;
+        F2 u = zero2, ow;                                       // u = s yn (o + w_post)
+        if (has_y) u = f2 * y[j];
+        if (has_post) {
+          ow = off + wo[j];
+          u = u * ow;
+        }
+        const F2 xn = (GATE ? fma2(g[j], u, x[j]) : x[j] + u) * rx2;
+        dw_pre[q] = fma2(h[j], xn, dw_pre[q]);
+        const F2 in = fma2(xn, m2, h[j] * (off + wi[j]));
+        const F2 dx = has_up ? fma2(rx2, in, d[j]) : rx2 * in;
+        o_dx.set(q, dx);
+        o_dx.put(a.d_x, row, H, 2 * q + 1);
+        if (kShared) {
+          dg[q] = fma2(dx, u, dg[q]);
+        } else if (GATE) {
+          o_dg.set(q, dx * u);
+          o_dg.put(a.d_gate, row, H, 2 * q + 1);
+        }
+        if (has_y) {
+          const F2 du = GATE ? (s2 * g[j]) * dx : s2 * dx;
+          F2 dy = du;
+          if (has_post) {
+            const F2 yn = y[j] * ry2;
+            dw_post[q] = fma2(du, yn, dw_post[q]);
+            dy = ry2 * fma2(yn, mb2, du * ow);
+          }
+          o_dy.set(q, dy);
+          o_dy.put(a.d_y, row, H, 2 * q + 1);
+        }
+      }
+    }
+    if constexpr (kShared) {
+      if (un != unit) {                       // the unit is done
+#pragma unroll
+        for (int q = 0; q < kPer / 2; ++q) {
+          if (per_span == 1) {
+            o_dg.set(q, dg[q]);
+            o_dg.put(a.d_gate, unit, H, 2 * q + 1);
+          } else {
+            float* to = a.gate_part + (size_t)unit * H;
+            if (P::column(2 * q) < H) to[P::column(2 * q)] = dg[q].lo();
+            if (P::column(2 * q + 1) < H) to[P::column(2 * q + 1)] = dg[q].hi();
+          }
+          dg[q] = zero2;
+        }
+      }
     }
   }
   float* part = a.w_part + (size_t)blockIdx.x * H;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
-    const int c = column<VEC>(e);
+    const int c = P::column(e);
     if (c >= H) continue;
-    part[c] = dw_pre[e];
-    if (a.w_post) part[(size_t)gridDim.x * H + c] = dw_post[e];
+    part[c] = e & 1 ? dw_pre[e / 2].hi() : dw_pre[e / 2].lo();
+    if (has_post)
+      part[(size_t)gridDim.x * H + c] = e & 1 ? dw_post[e / 2].hi() : dw_post[e / 2].lo();
   }
 }
 
-// Column sums of part[rows][H] in row order: 32 columns and 8 interleaved row lanes a CTA.
+// Column sums of part[rows][H] in a fixed order: 32 columns and 32 interleaved row lanes a CTA.
 template <typename E>
-__global__ void __launch_bounds__(256) column_sums(const float* part, int rows, int H, E* out0,
+__global__ void __launch_bounds__(1024) column_sums(const float* part, int rows, int H, E* out0,
                                                    E* out1) {
-  __shared__ float s[8][33];
+  __shared__ float s[32][33];
+  pdl_wait();
+  pdl_signal();
   const int c = blockIdx.x * 32 + threadIdx.x % 32, lane = threadIdx.x / 32;
   const float* p = part + (size_t)blockIdx.y * rows * H;
   float a = 0.f;
   if (c < H)
-    for (int r = lane; r < rows; r += 8) a += p[(size_t)r * H + c];
+#pragma unroll 4
+    for (int r = lane; r < rows; r += 32) a += p[(size_t)r * H + c];
   s[lane][threadIdx.x % 32] = a;
   __syncthreads();
   if (lane != 0 || c >= H) return;
-  for (int j = 1; j < 8; ++j) a += s[j][threadIdx.x];
+  for (int j = 1; j < 32; ++j) a += s[j][threadIdx.x];
   (blockIdx.y == 0 ? out0 : out1)[c] = (E)a;
 }
 
-// d_gate rows of long spans, from their parts in order.
+// d_gate rows of shared gate rows, from their parts in order.
 template <typename E>
-__global__ void __launch_bounds__(256) gate_sums(const float* part, int per_span, int H, E* out) {
-  for (int c = threadIdx.x; c < H; c += blockDim.x) {
-    float a = 0.f;
-    for (int j = 0; j < per_span; ++j) a += part[((size_t)blockIdx.x * per_span + j) * H + c];
-    out[(size_t)blockIdx.x * H + c] = (E)a;
-  }
+__global__ void __launch_bounds__(128) gate_sums(const float* part, int per_span, int H, E* out) {
+  pdl_wait();
+  pdl_signal();
+  const int c = blockIdx.y * 128 + threadIdx.x;
+  if (c >= H) return;
+  const float* p = part + (size_t)blockIdx.x * per_span * H + c;
+  float a = 0.f;
+#pragma unroll 8
+  for (int j = 0; j < per_span; ++j) a += p[(size_t)j * H];
+  out[(size_t)blockIdx.x * H + c] = (E)a;
 }
 
 bool vector_rows(const NormArgs& a) {
@@ -265,49 +581,79 @@ bool vector_rows(const NormArgs& a) {
   return all % 16 == 0;
 }
 
-template <typename E, int VEC>
-cudaError_t backward(const NormArgs& a) {
-  const int threads = row_threads(a.H);
-  const int per_span = a.gate ? norm_span_parts(a.T, a.span) : 1;
-  const int units = a.gate ? (a.T + a.span - 1) / a.span * per_span : a.T;
+// CTAs that are resident at once, at most `items`.
+cudaError_t resident(const void* kernel, int threads, size_t smem, int items, int* grid) {
   int sms = 0, per_sm = 0;
   cudaError_t e = device_sms(&sms);
-  if (e == cudaSuccess)
-    e = blocks_per_sm((const void*)block_norm_backward<E, VEC>, threads, 0, &per_sm);
+  if (e == cudaSuccess && smem > 0) e = raise_smem_limit(kernel, smem);
+  if (e == cudaSuccess) e = blocks_per_sm(kernel, threads, smem, &per_sm);
+  *grid = std::min(items, std::max(1, per_sm) * sms);
+  return e;
+}
+
+constexpr size_t kSmemMost = 200 * 1024;   // (fp32 rows above 4096 do not fit it twice over)
+
+template <typename E, int VEC>
+cudaError_t forward(const NormArgs& a) {
+  const int threads = row_threads(a.H);
+  const size_t smem = Rows<E, VEC, 3>::smem(threads);
+  if constexpr (VEC > 1)
+    if (smem > kSmemMost) return forward<E, 1>(a);
+  int grid = 0;
+  const cudaError_t e = resident((const void*)block_norm<E, VEC>, threads, smem, a.T, &grid);
   if (e != cudaSuccess) return e;
-  const int grid = std::min({units, std::max(1, per_sm) * sms, norm_max_ctas(a.H)});
-  block_norm_backward<E, VEC><<<grid, threads, 0, a.stream>>>(a, units, per_span);
-  column_sums<E><<<dim3((a.H + 31) / 32, a.w_post ? 2 : 1), 256, 0, a.stream>>>(
-      a.w_part, grid, a.H, (E*)a.d_w_pre, (E*)a.d_w_post);
-  if (per_span > 1)
-    gate_sums<E><<<units / per_span, 256, 0, a.stream>>>(a.gate_part, per_span, a.H,
-                                                         (E*)a.d_gate);
-  return cudaGetLastError();
+  return launch_after(block_norm<E, VEC>, grid, threads, smem, a.stream, a);
+}
+
+template <typename E, int VEC, int GATE, bool FULL>
+cudaError_t backward(const NormArgs& a) {
+  const int threads = row_threads(a.H);
+  const size_t smem = Rows<E, VEC, 5>::smem(threads);
+  if constexpr (VEC > 1)
+    if (smem > kSmemMost) return backward<E, 1, GATE, false>(a);
+  const int per_span = GATE == 2 ? norm_span_parts(a.T, a.span) : 1;
+  const int units = GATE == 2 ? (a.T + a.span - 1) / a.span * per_span : a.T;
+  const auto kernel = block_norm_backward<E, VEC, GATE, FULL>;
+  int grid = 0;
+  const cudaError_t e = resident((const void*)kernel, threads, smem, units, &grid);
+  if (e != cudaSuccess) return e;
+  grid = std::min(grid, norm_max_ctas(a.H));
+  cudaError_t e2 = launch_after(kernel, grid, threads, smem, a.stream, a, units, per_span);
+  if (e2 == cudaSuccess)
+    e2 = launch_after(column_sums<E>, dim3((a.H + 31) / 32, a.w_post ? 2 : 1), 1024, 0, a.stream,
+                      a.w_part, grid, a.H, (E*)a.d_w_pre, (E*)a.d_w_post);
+  if (e2 == cudaSuccess && per_span > 1)
+    e2 = launch_after(gate_sums<E>, dim3(units / per_span, (a.H + 127) / 128), 128, 0, a.stream,
+                      a.gate_part, per_span, a.H, (E*)a.d_gate);
+  return e2;
+}
+
+template <typename E, int VEC>
+cudaError_t backward_of(const NormArgs& a) {
+  // (without 16-byte vectors, memory latency hides what the look-ups cost)
+  constexpr bool kFull = VEC > 1;
+  const bool full = kFull && a.y && a.w_post && a.d_x_out;
+  if (!a.gate) return full ? backward<E, VEC, 0, kFull>(a) : backward<E, VEC, 0, false>(a);
+  if (a.span == 1) return full ? backward<E, VEC, 1, kFull>(a) : backward<E, VEC, 1, false>(a);
+  return full ? backward<E, VEC, 2, kFull>(a) : backward<E, VEC, 2, false>(a);
 }
 
 }  // namespace
 
 int norm_max_ctas(int H) { return 160 * std::max(1, 2048 / row_threads(H)); }
 
-int norm_span_parts(int T, int span) { return (std::min(span, T) + kNormUnit - 1) / kNormUnit; }
+int norm_span_parts(int T, int span) { return (std::min(span, T) + norm_unit(T) - 1) / norm_unit(T); }
 
 cudaError_t launch_block_norm(const NormArgs& a) {
-  const int threads = row_threads(a.H);
   const bool v = vector_rows(a);
-  if (a.dtype == DSPARK_F32) {
-    if (v) block_norm<float, 4><<<a.T, threads, 0, a.stream>>>(a);
-    else block_norm<float, 1><<<a.T, threads, 0, a.stream>>>(a);
-  } else {
-    if (v) block_norm<__nv_bfloat16, 8><<<a.T, threads, 0, a.stream>>>(a);
-    else block_norm<__nv_bfloat16, 1><<<a.T, threads, 0, a.stream>>>(a);
-  }
-  return cudaGetLastError();
+  if (a.dtype == DSPARK_F32) return v ? forward<float, 4>(a) : forward<float, 1>(a);
+  return v ? forward<__nv_bfloat16, 8>(a) : forward<__nv_bfloat16, 1>(a);
 }
 
 cudaError_t launch_block_norm_backward(const NormArgs& a) {
   const bool v = vector_rows(a);
-  if (a.dtype == DSPARK_F32) return v ? backward<float, 4>(a) : backward<float, 1>(a);
-  return v ? backward<__nv_bfloat16, 8>(a) : backward<__nv_bfloat16, 1>(a);
+  if (a.dtype == DSPARK_F32) return v ? backward_of<float, 4>(a) : backward_of<float, 1>(a);
+  return v ? backward_of<__nv_bfloat16, 8>(a) : backward_of<__nv_bfloat16, 1>(a);
 }
 
 }  // namespace dspark

@@ -22,6 +22,7 @@ enum : int {
   kLossVoc = 2,      // compact head rows
   kLossScale = 3,    // float: loss_scale / D, the factor of every gradient
   kLossDone = 4,     // row CTAs whose loss is written
+  kLossSplits = 5,   // splits of the vocabulary in dX's sum, at most LossPlan::splits
 };
 
 // Gradient memory that no product writes: `bytes` from `p` on, or, with `keep`, the rows of
@@ -68,7 +69,7 @@ struct LossPlan {
   int pieces, piece_cols;             // pieces of the vocabulary, columns of each
   float* qres;                        // [Tp] bf16: what rounding the label's entry of q lost
   float* dxp;                         // [splits][Tp][Kx] partial gradients of X
-  int splits;
+  int splits;                         // the most; fp32: what is used
   bool grads;                         // any gradient asked for
   LossZero zero[3];
   int n_zero;
@@ -120,9 +121,10 @@ int loss_simt_splits(int T, int Kx, int cols);
 cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stats, bool store);
 cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first);
 cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1);
-// k_loss_tc.cu (bf16, on the tensor cores).  The logits with statistics and the first dX also
-// write the plan's zeros, half each (all in the logits when there is no dX).
-int loss_tc_splits(int T, int H, int r, int cols);
+// k_loss_tc.cu (bf16, on the tensor cores).  The logits with statistics, the first dX and the
+// first dW also write the plan's zeros, each a share (masked rows come with a d_lm_head, so
+// with a dW).
+int loss_tc_splits(int T, int Hp, int rp);   // the most that may be chosen
 cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats, bool store);
 cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first);
 cudaError_t launch_loss_dw_tc(const LossPlan& p, int v0, int v1);

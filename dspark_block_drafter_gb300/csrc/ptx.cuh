@@ -177,6 +177,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
+// The same arrival without ordering the thread's earlier global accesses for the cluster: for
+// barriers that only say an accumulator in TMEM has been read (its loads waited for, and
+// tcgen05.fence::before_thread_sync before).
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // TMA loads into this CTA's shared memory whose completion is counted on the mbarrier
 // of the pair's leader CTA (cluster address), for cta_group::2 MMAs.
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t bar,

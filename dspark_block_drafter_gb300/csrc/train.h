@@ -32,8 +32,8 @@ cudaError_t launch_block_norm_backward(const NormArgs& a);
 constexpr int kClipMaxCtas = 1216;   // CTAs of one pass over the gradients, at most
 constexpr int kClipList = 96;        // gradients of one launch
 
-size_t clip_partials(int count);     // fp64 values of workspace
+size_t clip_partials(int count);     // fp32 values of workspace
 cudaError_t launch_clip_grads(int count, const dspark_grad* grads, float max_norm, float* norm,
-                              double* partial, cudaStream_t stream);
+                              float* partial, cudaStream_t stream);
 
 }  // namespace dspark

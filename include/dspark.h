@@ -556,8 +556,8 @@ size_t dspark_clip_grads_workspace_size(int32_t count, const dspark_grad* grads)
  * max_norm >= 0
  * norm     device [1] fp32
  *
- * Squares are summed in fp32 within a thread and in fp64 above, in a fixed order.  When
- * the norm is not finite, out = in: the norm says so, and the caller skips the step.
+ * Squares are summed in fp32, in a fixed order.  When the norm is not finite (or its
+ * square leaves fp32's range), out = in: the norm says so, and the caller skips the step.
  * Where out is in and the factor is 1 nothing is written.
  */
 dspark_status dspark_clip_grads(int32_t count, const dspark_grad* grads, float max_norm,
