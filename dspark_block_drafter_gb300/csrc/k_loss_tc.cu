@@ -20,9 +20,12 @@
 // tokens that precede no slot): the products leave most of the memory bandwidth unused.
 //
 // The tensor core cuts each partial sum of an accumulator toward zero, so a long sum drifts:
-// over K = 4352 the losses were off by 5e-6.  The logits' accumulator is therefore read
-// every 768 of K and the parts are added in fp32 registers (which hold the tile's 128
-// columns of a row until it is complete).  The gradients, rounded to bf16, need no such care.
+// over K = 4352 the losses were off by 5e-6 of their size.  The logits' accumulator is
+// therefore read every few K-blocks and the parts are added in fp32 registers (which hold the
+// tile's 128 columns of a row until it is complete).  Pairs read it every 12 K-blocks (losses
+// off by 5e-7, the logits of 4096 rows 6% slower than in one sum; every 8: 2e-7, 11%), single
+// CTAs, which wait for memory anyway, every 4.  The gradients, rounded to bf16, need no such
+// care.
 //
 // The logits are never stored.  Their epilogue has one row per thread: it takes the maximum
 // and the sum of exponentials of each 128-column tile, and, when gradients follow, stores
@@ -51,7 +54,8 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarps + 3);
 constexpr uint32_t kRowBytes = 128;                  // dW: a row's part of a staged store
 constexpr uint32_t kStaging = kEpiWarps * 32 * kRowBytes;
-constexpr int kSumBlocks = 12;                       // K-blocks of one part of a logit's sum
+template <int CG>
+constexpr int kSumBlocks = CG == 2 ? 12 : 4;         // K-blocks of one part of a logit's sum
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kBarBytes = 512;
 constexpr long long kWaitBudget = 2000000000ll;      // ~1 s of SM clocks
@@ -388,7 +392,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
         int c0 = 0;
         const bool markov = MODE != kLogits && column_tile(g, t.n, &c0);
         for (int kb = t.kb0, part = 0; part == 0 || kb < t.kb1; ++part, ++local) {
-          const int end = MODE == kLogits ? min(t.kb1, kb + kSumBlocks) : t.kb1;
+          const int end = MODE == kLogits ? min(t.kb1, kb + kSumBlocks<CG>) : t.kb1;
           const uint32_t acc = local & 1, aph = (local >> 1) & 1;
           if (!ptx::mbar_wait(&acc_empty[acc], aph ^ 1, kWaitBudget, abort_flag)) {
             ok = false;
@@ -465,7 +469,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
         const int v0 = g.v0 + t.n * kTileN + half * 128;     // compact head row of column 0
         const int n_in = n_voc - v0;                          // columns that exist
         float z[128];
-        for (int kb = t.kb0; kb < t.kb1; kb += kSumBlocks) {
+        for (int kb = t.kb0; kb < t.kb1; kb += kSumBlocks<CG>) {
           if (!acc_wait()) break;
           const uint32_t at = at0 + (local & 1) * kTileN;
           const bool first = kb == t.kb0;
@@ -591,10 +595,25 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
           if (markov) {
             // column by column: a warp's rows are neighbours there
             uint16_t* d = (uint16_t*)p.d_w2 + (size_t)(c0 - p.Hp) * p.Vh + row;
+            if (p.vlist) {
 #pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (live && j < width)
-                d[(size_t)j * p.Vh] = (uint16_t)(j & 1 ? o[j / 2] >> 16 : o[j / 2] & 0xFFFFu);
+              for (int j = 0; j < 128; ++j)
+                if (live && j < width)
+                  d[(size_t)j * p.Vh] = (uint16_t)(j & 1 ? o[j / 2] >> 16 : o[j / 2] & 0xFFFFu);
+            } else {
+              // lanes in pairs: the even one stores both rows of the even column, the odd one
+              // those of the odd column (V_head is a multiple of 8, so both rows exist)
+              const int odd = lane & 1;
+              d -= odd;
+#pragma unroll
+              for (int q = 0; q < 64; ++q) {
+                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, o[q], 1);
+                const uint32_t both = odd ? __byte_perm(other, o[q], 0x7632)
+                                          : __byte_perm(o[q], other, 0x5410);
+                if (live && 2 * q + odd < width)
+                  *reinterpret_cast<uint32_t*>(d + (size_t)(2 * q + odd) * p.Vh) = both;
+              }
+            }
           } else {
             // through shared memory, so that eight lanes store 128 bytes of one row (one
             // row a lane, 16 bytes at a time, reached a fifth of the write bandwidth)

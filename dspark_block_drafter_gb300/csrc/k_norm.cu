@@ -30,13 +30,19 @@ namespace dspark {
 
 namespace {
 
-constexpr int kPer = 8;               // elements of a row per thread
-
 // Rows of one gate row that a CTA takes at a time: 16 in a large batch (their gate gradient
 // is summed in registers), fewer where that would leave SMs without rows.
 __host__ __device__ int norm_unit(int T) { return T >= 16 * 512 ? 16 : T >= 1024 ? T / 512 : 1; }
 
-int row_threads(int H) { return (H + kPer * 32 - 1) / (kPer * 32) * 32; }
+// Threads of a row with `per` elements each.  Wide rows take 16 each, 512 threads at most: half
+// the threads make half the shuffles of a sum, and their 128 registers hold what the gradient
+// keeps (8192 rows of 4096, gradient: 512 threads at 64 registers 133 us, at 128 120 us; 256
+// threads 108 us).
+int row_per(int H) { return H > 2048 ? 16 : 8; }
+int row_threads(int H) {
+  const int n = row_per(H) * 32;
+  return (H + n - 1) / n * 32;
+}
 
 // Two fp32 values in one 64-bit register, for the packed arithmetic (half the instructions).
 struct F2 {
@@ -81,7 +87,7 @@ __device__ __forceinline__ F2 pair_of(const __nv_bfloat16* p) {
 
 // A thread's elements of one row of one tensor, as they lie in memory: vectors of VEC
 // consecutive elements, the threads' vectors side by side.
-template <typename E, int VEC>
+template <typename E, int VEC, int kPer>
 struct Part {
   struct alignas(sizeof(E) * VEC) Vec { E e[VEC]; };
   Vec v[kPer / VEC];
@@ -143,11 +149,11 @@ struct Part {
 // Vectors of 16 bytes go through shared memory, each thread's own 16 bytes to its own place
 // (so no barrier is needed); without that alignment a row is loaded into registers when its
 // turn comes, and the weights stay there.
-template <typename E, int VEC, int N>
+template <typename E, int VEC, int N, int kPer>
 struct Rows {
   static constexpr bool kAsync = VEC > 1;
   static constexpr int kVecs = kPer / VEC;
-  using P = Part<E, VEC>;
+  using P = Part<E, VEC, kPer>;
   uint4* slots;                               // [2 N + 2][kVecs][threads]
   int turn = 0;
   P held[kAsync ? 1 : N + 2];
@@ -277,16 +283,16 @@ struct RowSum {
 
 extern __shared__ uint4 norm_smem[];
 
-template <typename E, int VEC>
-__global__ void __launch_bounds__(1024, 1) block_norm(const NormArgs a) {
-  using P = Part<E, VEC>;
+template <typename E, int VEC, int kPer>
+__global__ void __launch_bounds__(32 * kPer, 1) block_norm(const NormArgs a) {
+  using P = Part<E, VEC, kPer>;
   __shared__ float s_sum[2][32][5];
   RowSum sum{s_sum, 0};
   pdl_wait();
   pdl_signal();
   const int H = a.H;
   const float inv_h = 1.f / (float)H;
-  Rows<E, VEC, 3> rows;                       // x, y, gate
+  Rows<E, VEC, 3, kPer> rows;                       // x, y, gate
   rows.init(norm_smem, a);
   auto fetch = [&](int t) {
     if (t < a.T) {
@@ -346,10 +352,10 @@ __global__ void __launch_bounds__(1024, 1) block_norm(const NormArgs a) {
 // rows); a CTA takes units in turn and keeps its column sums in registers.
 // GATE: 0 none, 1 a gate row for each row, 2 shared gate rows, whose gradients are sums too.
 // FULL: y, w_post and d_x_out are all there (else what is there is looked up).
-template <typename E, int VEC, int GATE, bool FULL>
-__global__ void __launch_bounds__(1024, 1) block_norm_backward(const NormArgs a, int units,
+template <typename E, int VEC, int kPer, int GATE, bool FULL>
+__global__ void __launch_bounds__(32 * kPer, 1) block_norm_backward(const NormArgs a, int units,
                                                                int per_span) {
-  using P = Part<E, VEC>;
+  using P = Part<E, VEC, kPer>;
   constexpr bool kShared = GATE == 2;
   const bool has_y = FULL || a.y, has_post = FULL || a.w_post, has_up = FULL || a.d_x_out;
   __shared__ float s_sum[2][32][5];
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(1024, 1) block_norm_backward(const NormArgs a,
     dw_pre[e] = dw_post[e] = zero2;
     if (kShared) dg[e] = zero2;
   }
-  Rows<E, VEC, 5> rows;                       // x, dh, y, d_x_out, gate
+  Rows<E, VEC, 5, kPer> rows;                       // x, dh, y, d_x_out, gate
   rows.init(norm_smem, a);
   // row t of rows [t, t1) of unit un
   int un = blockIdx.x, t = 0, t1 = 0;
@@ -593,27 +599,27 @@ cudaError_t resident(const void* kernel, int threads, size_t smem, int items, in
 
 constexpr size_t kSmemMost = 200 * 1024;   // (fp32 rows above 4096 do not fit it twice over)
 
-template <typename E, int VEC>
+template <typename E, int VEC, int kPer>
 cudaError_t forward(const NormArgs& a) {
   const int threads = row_threads(a.H);
-  const size_t smem = Rows<E, VEC, 3>::smem(threads);
+  const size_t smem = Rows<E, VEC, 3, kPer>::smem(threads);
   if constexpr (VEC > 1)
-    if (smem > kSmemMost) return forward<E, 1>(a);
+    if (smem > kSmemMost) return forward<E, 1, kPer>(a);
   int grid = 0;
-  const cudaError_t e = resident((const void*)block_norm<E, VEC>, threads, smem, a.T, &grid);
+  const cudaError_t e = resident((const void*)block_norm<E, VEC, kPer>, threads, smem, a.T, &grid);
   if (e != cudaSuccess) return e;
-  return launch_after(block_norm<E, VEC>, grid, threads, smem, a.stream, a);
+  return launch_after(block_norm<E, VEC, kPer>, grid, threads, smem, a.stream, a);
 }
 
-template <typename E, int VEC, int GATE, bool FULL>
+template <typename E, int VEC, int kPer, int GATE, bool FULL>
 cudaError_t backward(const NormArgs& a) {
   const int threads = row_threads(a.H);
-  const size_t smem = Rows<E, VEC, 5>::smem(threads);
+  const size_t smem = Rows<E, VEC, 5, kPer>::smem(threads);
   if constexpr (VEC > 1)
-    if (smem > kSmemMost) return backward<E, 1, GATE, false>(a);
+    if (smem > kSmemMost) return backward<E, 1, kPer, GATE, false>(a);
   const int per_span = GATE == 2 ? norm_span_parts(a.T, a.span) : 1;
   const int units = GATE == 2 ? (a.T + a.span - 1) / a.span * per_span : a.T;
-  const auto kernel = block_norm_backward<E, VEC, GATE, FULL>;
+  const auto kernel = block_norm_backward<E, VEC, kPer, GATE, FULL>;
   int grid = 0;
   const cudaError_t e = resident((const void*)kernel, threads, smem, units, &grid);
   if (e != cudaSuccess) return e;
@@ -628,14 +634,27 @@ cudaError_t backward(const NormArgs& a) {
   return e2;
 }
 
-template <typename E, int VEC>
+template <typename E, int VEC, int kPer>
 cudaError_t backward_of(const NormArgs& a) {
   // (without 16-byte vectors, memory latency hides what the look-ups cost)
   constexpr bool kFull = VEC > 1;
   const bool full = kFull && a.y && a.w_post && a.d_x_out;
-  if (!a.gate) return full ? backward<E, VEC, 0, kFull>(a) : backward<E, VEC, 0, false>(a);
-  if (a.span == 1) return full ? backward<E, VEC, 1, kFull>(a) : backward<E, VEC, 1, false>(a);
-  return full ? backward<E, VEC, 2, kFull>(a) : backward<E, VEC, 2, false>(a);
+  if (!a.gate)
+    return full ? backward<E, VEC, kPer, 0, kFull>(a) : backward<E, VEC, kPer, 0, false>(a);
+  if (a.span == 1)
+    return full ? backward<E, VEC, kPer, 1, kFull>(a) : backward<E, VEC, kPer, 1, false>(a);
+  return full ? backward<E, VEC, kPer, 2, kFull>(a) : backward<E, VEC, kPer, 2, false>(a);
+}
+
+template <typename E, int VEC>
+cudaError_t launch_of(const NormArgs& a, bool grad) {
+  if (row_per(a.H) == 16) return grad ? backward_of<E, VEC, 16>(a) : forward<E, VEC, 16>(a);
+  return grad ? backward_of<E, VEC, 8>(a) : forward<E, VEC, 8>(a);
+}
+
+template <typename E, int VEC>
+cudaError_t launch_of_type(const NormArgs& a, bool grad) {
+  return vector_rows(a) ? launch_of<E, VEC>(a, grad) : launch_of<E, 1>(a, grad);
 }
 
 }  // namespace
@@ -645,15 +664,13 @@ int norm_max_ctas(int H) { return 160 * std::max(1, 2048 / row_threads(H)); }
 int norm_span_parts(int T, int span) { return (std::min(span, T) + norm_unit(T) - 1) / norm_unit(T); }
 
 cudaError_t launch_block_norm(const NormArgs& a) {
-  const bool v = vector_rows(a);
-  if (a.dtype == DSPARK_F32) return v ? forward<float, 4>(a) : forward<float, 1>(a);
-  return v ? forward<__nv_bfloat16, 8>(a) : forward<__nv_bfloat16, 1>(a);
+  return a.dtype == DSPARK_F32 ? launch_of_type<float, 4>(a, false)
+                               : launch_of_type<__nv_bfloat16, 8>(a, false);
 }
 
 cudaError_t launch_block_norm_backward(const NormArgs& a) {
-  const bool v = vector_rows(a);
-  if (a.dtype == DSPARK_F32) return v ? backward_of<float, 4>(a) : backward_of<float, 1>(a);
-  return v ? backward_of<__nv_bfloat16, 8>(a) : backward_of<__nv_bfloat16, 1>(a);
+  return a.dtype == DSPARK_F32 ? launch_of_type<float, 4>(a, true)
+                               : launch_of_type<__nv_bfloat16, 8>(a, true);
 }
 
 }  // namespace dspark

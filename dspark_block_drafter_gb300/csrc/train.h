@@ -22,7 +22,7 @@ struct NormArgs {
   cudaStream_t stream;
 };
 
-constexpr int kNormMaxH = 8192;      // eight elements for each of 1024 threads
+constexpr int kNormMaxH = 8192;      // 16 elements for each of 512 threads
 
 int norm_max_ctas(int H);              // CTAs of the gradient kernel, at most
 int norm_span_parts(int T, int span);  // parts of the rows that share a gate row

@@ -181,7 +181,7 @@ def _checked(name: str, t: Optional[torch.Tensor], shape, dtype) -> Optional[int
     """The address of a dense tensor of the given shape and type (None stays None)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
     return t.data_ptr()
