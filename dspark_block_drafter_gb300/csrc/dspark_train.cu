@@ -53,8 +53,8 @@ static dspark_status validate_loss(const dspark_loss_config* c, const dspark_hea
     return fail(DSPARK_ERR_INVALID_ARG, "without d2t, V_head must equal V");
   if (c->r > 512) return fail(DSPARK_ERR_UNSUPPORTED, "Markov rank above 512");
   if (c->T > kMaxLossRows) return fail(DSPARK_ERR_UNSUPPORTED, "more than 2^20 rows");
-  if (c->H > (1 << 20) || c->V > (1 << 28))
-    return fail(DSPARK_ERR_UNSUPPORTED, "sizes too large");
+  if (c->H > (1 << 16) || c->V > (1 << 24))
+    return fail(DSPARK_ERR_UNSUPPORTED, "H above 2^16 or V above 2^24");
   if (c->dtype == DSPARK_BF16) {
     if (c->H % 8 != 0)
       return fail(DSPARK_ERR_UNSUPPORTED, "bf16 path needs H % 8 == 0 (16-byte rows)");
@@ -184,6 +184,7 @@ static dspark_status validate_norm(const dspark_norm_config* c) {
     return fail(DSPARK_ERR_INVALID_ARG,
                 "eps must be positive, residual_scale and weight_offset finite");
   if (c->H > kNormMaxH) return fail(DSPARK_ERR_UNSUPPORTED, "H above 8192");
+  if (c->T > (1 << 30)) return fail(DSPARK_ERR_UNSUPPORTED, "more than 2^30 rows");
   return DSPARK_OK;
 }
 

@@ -17,7 +17,9 @@
 // of warp 9 the MMAs; warps 0-3 take the first 128 columns of a finished accumulator, warps
 // 4-7 the others (there are two accumulators, so that this overlaps the next products).
 // Warp 10 writes the zeros of gradients that no product reaches (rows of masked tokens, of
-// tokens that precede no slot): the products leave most of the memory bandwidth unused.
+// tokens that precede no slot): the logits and dX leave most of the memory bandwidth unused.
+// (1.3 GB of them in the 448 x 2816 x 262144 head with 32768 rows in use: logits 90 -> 174 us,
+// dX 70 -> 152 us, against 235 us by themselves.  dW, which writes, took twice as long.)
 //
 // The tensor core cuts each partial sum of an accumulator toward zero, so a long sum drifts:
 // over K = 4352 the losses were off by 5e-6 of their size.  The logits' accumulator is
@@ -79,9 +81,7 @@ struct TcArgs {
   int first;           // dX: the first piece (later ones add)
   int n_head, n_markov;  // 256-column tiles of X's two parts that are computed
   int chunked;         // dX: lm_head rows are whole 64-column chunks
-  // the share of the plan's zeros this launch writes, in 1/64: of the plain ones (which have
-  // to be there before dW), and of the masked rows
-  int zero0, zero1, keep0, keep1;
+  int zero0, zero1;    // the share of the plan's zeros this launch writes, in 1/64
 };
 
 // One unit of work: a tile of the result and a range of K-blocks.
@@ -102,6 +102,7 @@ __device__ __forceinline__ int unit_count(const TcArgs& g, int n_tok, int n_voc,
   return (cols + kTileM * CG - 1) / (kTileM * CG) * nt;
 }
 
+constexpr int kZeroShare = 34;    // of the zeros the logits write, in 1/64; dX the others
 constexpr int kRowGroup = 24;     // M tiles whose rows of X are kept in L2 together
 
 template <int MODE, int CG>
@@ -172,8 +173,7 @@ __device__ __forceinline__ void write_zeros(const TcArgs& g, int lane) {
     const LossZero& q = g.p.zero[z];
     // items: rows, or 16-byte vectors (and the odd bytes, all fewer than 16, at the end)
     const long long items = q.keep ? (long long)(q.bytes / q.row_bytes) : (long long)(q.bytes / 16);
-    const int z0 = q.keep ? g.keep0 : g.zero0, z1 = q.keep ? g.keep1 : g.zero1;
-    const long long lo = items * z0 / 64, n = items * z1 / 64 - lo;
+    const long long lo = items * g.zero0 / 64, n = items * g.zero1 / 64 - lo;
     const long long a = lo + n * part / parts, b = lo + n * (part + 1) / parts;
     if (q.keep) {
       const int per = q.row_bytes / 16;
@@ -189,7 +189,7 @@ __device__ __forceinline__ void write_zeros(const TcArgs& g, int lane) {
       uint4* v = reinterpret_cast<uint4*>(q.p);
 #pragma unroll 4
       for (long long k = a + lane; k < b; k += 32) v[k] = none;
-      if (z1 == 64 && z0 < 64 && part == 0 && lane < (int)(q.bytes % 16)) q.p[items * 16 + lane] = 0;
+      if (g.zero1 == 64 && part == 0 && lane < (int)(q.bytes % 16)) q.p[items * 16 + lane] = 0;
     }
   }
 }
@@ -431,7 +431,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       ptx::mbar_wait(drain, 0, kWaitBudget, nullptr);
     }
   } else if (warp == kEpiWarps + 2) {
-    if (g.zero1 > g.zero0 || g.keep1 > g.keep0) write_zeros(g, lane);
+    if (MODE != kDw && g.zero1 > g.zero0) write_zeros(g, lane);
   } else {
     // ---------------------------------------------------------------- epilogue
     const int quad = warp % 4, half = warp / 4;       // lanes and columns of this warp
@@ -774,11 +774,7 @@ cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats,
   g.v0 = v0;
   g.v1 = v1;
   g.want = stats ? kWantStats | (store ? kWantGap : 0) : kWantGrad;
-  if (stats && p.n_zero > 0) {
-    const bool dx = p.d_hidden || p.d_w1;
-    g.zero1 = dx ? 32 : 64;
-    g.keep1 = dx ? 22 : 40;
-  }
+  if (stats && p.n_zero > 0) g.zero1 = p.d_hidden || p.d_w1 ? kZeroShare : 64;
   const long long tiles = (long long)row_tiles(p.T) * ((v1 - v0 + kTileN - 1) / kTileN);
   return single(p.T) ? launch<kLogits, 1>(g, tiles) : launch<kLogits, 2>(g, tiles);
 }
@@ -791,10 +787,8 @@ cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first) {
   g.first = first;
   g.chunked = p.H % 64 == 0;
   if (first && p.n_zero > 0) {
-    g.zero0 = 32;
+    g.zero0 = kZeroShare;
     g.zero1 = 64;
-    g.keep0 = 22;
-    g.keep1 = 40;
   }
   g.n_head = p.d_hidden ? (p.Hp + kTileN - 1) / kTileN : 0;
   g.n_markov = p.d_w1 ? (p.rp + kTileN - 1) / kTileN : 0;
@@ -807,11 +801,6 @@ cudaError_t launch_loss_dw_tc(const LossPlan& p, int v0, int v1) {
   g.p = p;
   g.v0 = v0;
   g.v1 = v1;
-  if (v0 == 0 && p.n_zero > 0) {
-    g.zero0 = g.zero1 = 64;
-    g.keep0 = 40;
-    g.keep1 = 64;
-  }
   g.n_head = p.d_lm_head ? (p.Hp + kTileN - 1) / kTileN : 0;
   g.n_markov = p.d_w2 ? (p.rp + kTileN - 1) / kTileN : 0;
   const long long tiles = (long long)((v1 - v0 + 255) / 256) * (g.n_head + g.n_markov);

@@ -121,9 +121,8 @@ int loss_simt_splits(int T, int Kx, int cols);
 cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stats, bool store);
 cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first);
 cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1);
-// k_loss_tc.cu (bf16, on the tensor cores).  The logits with statistics, the first dX and the
-// first dW also write the plan's zeros, each a share (masked rows come with a d_lm_head, so
-// with a dW).
+// k_loss_tc.cu (bf16, on the tensor cores).  The logits with statistics and the first dX also
+// write the plan's zeros, each a share (all in the logits when there is no dX).
 int loss_tc_splits(int T, int Hp, int rp);   // the most that may be chosen
 cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats, bool store);
 cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first);

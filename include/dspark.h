@@ -414,9 +414,9 @@ typedef enum dspark_reduction {
 
 /* Sizes and knobs of dspark_head_loss. */
 typedef struct dspark_loss_config {
-  int32_t T;             /* rows (slots of all blocks), >= 1 */
-  int32_t H;             /* hidden size, >= 1 (multiple of 8 for bf16) */
-  int32_t V;             /* vocabulary: token ids are in [0, V) */
+  int32_t T;             /* rows (slots of all blocks), 1 .. 2^20 */
+  int32_t H;             /* hidden size, 1 .. 2^16 (multiple of 8 for bf16) */
+  int32_t V;             /* vocabulary, at most 2^24: token ids are in [0, V) */
   int32_t r;             /* Markov rank, 1 .. 512; 0: a head without the Markov term */
   int32_t dtype;         /* dspark_dtype of hidden, the head's weights and the gradients */
   int32_t reduction;     /* dspark_reduction */
@@ -467,14 +467,15 @@ size_t dspark_head_loss_workspace_size(const dspark_loss_config* cfg,
  * The head's lm_head, lm_bias, d2t, V_head, markov_w1 and markov_w2 are read (the last
  * two NULL when r = 0); w_conf, b_conf and prepared are not.  Masked head rows take no
  * part: their probability is 0, their gradients are 0, and their weights are not read.
- * lm_bias itself gets no gradient.  A label at or above V, or a prev outside [0, V) on a
+ * lm_bias itself gets no gradient.  For bf16, lm_head, markov_w2 and the gradients of the
+ * weights are 16-byte aligned.  A label at or above V, or a prev outside [0, V) on a
  * row with a loss, drops the row and raises the error word (dspark_device_status).
  *
  * bf16: products on the tensor cores with fp32 accumulation; the softmax statistics,
- * losses and sums are fp32 or wider; the gradient of the logits is rounded to bf16 once
- * before the two gradient products, each gradient once on output.  No atomics decide an
- * order of summation: the same call gives the same bits.  Not reentrant on one
- * workspace.  Can be captured into a CUDA graph.
+ * losses and sums are fp32; the gradient of the logits is rounded to bf16 before the
+ * gradient products (d_hidden and d_markov_w1 get back what the label's entry lost), each
+ * gradient once on output.  No atomics decide an order of summation: the same call gives
+ * the same bits.  Not reentrant on one workspace.  Can be captured into a CUDA graph.
  */
 dspark_status dspark_head_loss(const dspark_loss_config* cfg, const dspark_head* head,
                                const void* hidden, const int32_t* prev,
@@ -484,7 +485,7 @@ dspark_status dspark_head_loss(const dspark_loss_config* cfg, const dspark_head*
 
 /* Sizes and knobs of dspark_block_norm and its gradient. */
 typedef struct dspark_norm_config {
-  int32_t T;             /* rows (tokens), >= 1 */
+  int32_t T;             /* rows (tokens), 1 .. 2^30 */
   int32_t H;             /* features, 1 .. 8192 */
   int32_t dtype;         /* dspark_dtype of every tensor */
   int32_t gate_span;     /* consecutive rows that share one gate row, >= 1 */

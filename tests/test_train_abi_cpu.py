@@ -60,7 +60,7 @@ def test_struct_layouts_match_c():
     ({}, dict(markov_w2=None), {}, I), ({}, dict(V_head=999), {}, I),
     ({}, dict(V_head=1001, d2t=0x10), {}, I), ({}, dict(V_head=0, d2t=0x10), {}, I),
     (dict(r=0), {}, dict(d_markov_w1=0x9000), I), (dict(r=0), {}, dict(d_markov_w2=0x9000), I),
-    (dict(r=513), {}, {}, U), (dict(T=(1 << 20) + 1), {}, {}, U),
+    (dict(r=513), {}, {}, U), (dict(T=(1 << 20) + 1), {}, {}, U), (dict(H=(1 << 16) + 8), {}, {}, U),
     (dict(dtype=1, H=60), {}, {}, U),
     (dict(dtype=1), dict(V_head=999, d2t=0x10), {}, U),
     (dict(dtype=1), {}, dict(d_lm_head=0x9008), I), (dict(dtype=1), {}, dict(d_markov_w1=0x9008), I),
@@ -114,7 +114,7 @@ def _norm(**kw):
     (dict(T=0), I), (dict(H=0), I), (dict(gate_span=0), I), (dict(dtype=2), I),
     (dict(eps=0.0), I), (dict(eps=float("nan")), I), (dict(eps=float("inf")), I),
     (dict(residual_scale=float("inf")), I), (dict(weight_offset=float("nan")), I),
-    (dict(H=8193), U)])
+    (dict(H=8193), U), (dict(T=(1 << 30) + 1), U)])
 def test_norm_refusals(kw, status):
     c = _norm(**kw)
     assert ds.dspark_block_norm_workspace_size(c) == 0
