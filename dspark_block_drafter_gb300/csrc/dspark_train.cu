@@ -137,14 +137,14 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
       p->dxp = (float*)take(sizeof(float) * p->splits * Tp * p->Kx);
     }
   }
-  auto zero = [&](void* g, size_t bytes, const int32_t* keep, size_t row_bytes) {
-    if (g) p->zero[p->n_zero++] = {(char*)g, bytes, keep, (int)row_bytes};
+  auto zero = [&](void* g, size_t bytes, const int32_t* keep, size_t row_bytes, bool early) {
+    if (g) p->zero[p->n_zero++] = {(char*)g, bytes, keep, (int)row_bytes, early};
   };
-  zero(p->d_w1, es * c->V * c->r, nullptr, 0);
+  zero(p->d_w1, es * c->V * c->r, nullptr, 0, false);
   if (h->lm_bias) {
     // (fp32: all of it, by a memset)
-    zero(p->d_lm_head, es * Vh * c->H, tc ? p->vinv : nullptr, es * c->H);
-    zero(p->d_w2, es * Vh * c->r, nullptr, 0);
+    zero(p->d_lm_head, es * Vh * c->H, tc ? p->vinv : nullptr, es * c->H, false);
+    zero(p->d_w2, es * Vh * c->r, nullptr, 0, true);
   }
   return off;
 }
@@ -152,24 +152,21 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
 static cudaError_t run_loss(const LossPlan& p) {
   const bool tc = p.dtype == DSPARK_BF16;
   const auto logits = tc ? launch_loss_logits_tc : launch_loss_logits_simt;
-  const auto product_dx = tc ? launch_loss_dx_tc : launch_loss_dx_simt;
-  const auto product_dw = tc ? launch_loss_dw_tc : launch_loss_dw_simt;
+  const auto grads = tc ? launch_loss_grads_tc : launch_loss_grads_simt;
   cudaError_t e = launch_loss_plan(p);
   if (e != cudaSuccess) return e;
   const bool keep = p.grads && p.pieces == 1;
   e = logits(p, 0, p.Vh, true, keep);
   if (e == cudaSuccess) e = launch_loss_rows(p);
   if (e != cudaSuccess || !p.grads) return e;
-  const bool dx = p.d_hidden || p.d_w1, dw = p.d_lm_head || p.d_w2;
   for (int c = 0; c < p.pieces; ++c) {
     const int v0 = c * p.piece_cols, v1 = std::min(p.Vh, v0 + p.piece_cols);
     if (!keep) e = logits(p, v0, v1, false, true);
     if (e == cudaSuccess && (keep || !tc)) e = launch_loss_dz(p, v0, v1);
-    if (e == cudaSuccess && dx) e = product_dx(p, v0, v1, c == 0);
-    if (e == cudaSuccess && dw) e = product_dw(p, v0, v1);
+    if (e == cudaSuccess) e = grads(p, v0, v1, c == 0);
     if (e != cudaSuccess) return e;
   }
-  return dx ? launch_loss_dx(p) : cudaSuccess;
+  return p.dxp ? launch_loss_dx(p) : cudaSuccess;
 }
 
 // ------------------------------------------------------------------ block norm

@@ -145,20 +145,25 @@ __device__ __forceinline__ int loss_label_row(const LossPlan& p, int t) {
 // bf16: a unit (a tile of dX over one split) costs its K-blocks of 64, about 12 K-blocks'
 // time for filling the pipeline and writing its partial result, and that result's traffic
 // (256 KB written and read: 0.23 K-blocks' time of the whole GPU); CTAs (pairs above 128
-// rows) take the units in waves.  The count with the least total is taken.  Measured with
-// 512 rows of the 151936 x 4096 head, dX and its sum: 2 splits 409 us (chosen), 1 698 us,
-// 3 530 us, 5 501 us, 13 442 us; with 3686 rows: 5 splits 2993 us, 2 2977 us, 3 3110 us.
+// rows) take the units in waves, and pairs the tiles of dW after them, which even out an
+// incomplete wave.  The count with the least total is taken.  Measured for dX and its sum
+// alone, 512 rows of the 151936 x 4096 head: 2 splits 409 us (chosen), 1 698 us, 3 530 us,
+// 5 501 us, 13 442 us.
 __device__ __forceinline__ int loss_pick_splits(const LossPlan& p, int n_tok, int n_voc, int lane) {
   if (p.dtype == 0) return p.splits;
   const bool pairs = p.T > 128;
-  const int nt = (p.d_hidden ? (p.Hp + 255) / 256 : 0) + (p.d_w1 ? (p.rp + 255) / 256 : 0);
-  const int tiles = max(1, (n_tok + 255) / 256) * nt, ctas = pairs ? 76 : 152;
-  const int nkb = (min(p.piece_cols, n_voc) + 63) / 64;
+  const int cols = min(p.piece_cols, n_voc), head = (p.Hp + 255) / 256, markov = (p.rp + 255) / 256;
+  const int tiles = max(1, (n_tok + 255) / 256) * ((p.d_hidden ? head : 0) + (p.d_w1 ? markov : 0));
+  const int ctas = pairs ? 76 : 152, nkb = (cols + 63) / 64;
+  const int n_dw = pairs ? (cols + 255) / 256 * ((p.d_lm_head ? head : 0) + (p.d_w2 ? markov : 0)) : 0;
+  const float dw = (float)n_dw * fmaxf((float)((n_tok + 63) / 64) + 2.f, 11.f);
   float cost = INFINITY;
   int best = 1;
   for (int s = 1 + lane; s <= p.splits && (s == 1 || s * 8 <= nkb); s += 32) {
-    const float c = (float)((tiles * s + ctas - 1) / ctas) * ((float)nkb / (float)s + 12.f) +
-                    0.23f * (float)(tiles * s);
+    const float unit = (float)nkb / (float)s + 12.f;
+    const float waves = (float)((tiles * s + ctas - 1) / ctas) * unit;
+    const float even = ((float)(tiles * s) * unit + dw) / (float)ctas;
+    const float c = fmaxf(waves, even) + 0.23f * (float)(tiles * s);
     if (c < cost) {
       cost = c;
       best = s;

@@ -248,15 +248,18 @@ cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stat
                       stats, store);
 }
 
-cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first) {
-  const bool few = p.T <= 16;
-  const dim3 grid(p.Kx / kTile, few ? 1 : (p.T + kTile - 1) / kTile, p.splits);
-  return launch_after(few ? loss_dx<1> : loss_dx<4>, grid, 256, 0, p.stream, p, v0, v1, first);
-}
-
-cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1) {
-  const dim3 grid(p.Kx / kTile, (v1 - v0 + kTile - 1) / kTile);
-  return launch_after(loss_dw, grid, 256, 0, p.stream, p, v0, v1);
+cudaError_t launch_loss_grads_simt(const LossPlan& p, int v0, int v1, bool first) {
+  cudaError_t e = cudaSuccess;
+  if (p.dxp) {
+    const bool few = p.T <= 16;
+    const dim3 grid(p.Kx / kTile, few ? 1 : (p.T + kTile - 1) / kTile, p.splits);
+    e = launch_after(few ? loss_dx<1> : loss_dx<4>, grid, 256, 0, p.stream, p, v0, v1, first);
+  }
+  if (e == cudaSuccess && (p.d_lm_head || p.d_w2)) {
+    const dim3 grid(p.Kx / kTile, (v1 - v0 + kTile - 1) / kTile);
+    e = launch_after(loss_dw, grid, 256, 0, p.stream, p, v0, v1);
+  }
+  return e;
 }
 
 }  // namespace dspark

@@ -62,16 +62,23 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kBarBytes = 512;
 constexpr long long kWaitBudget = 2000000000ll;      // ~1 s of SM clocks
 
-enum : int { kLogits = 0, kDx = 1, kDw = 2 };
+// (kGrads: dX and dW in one launch, each pair its units of the first, then of the second)
+enum : int { kLogits = 0, kDx = 1, kDw = 2, kGrads = 3 };
 // what the logits' epilogue makes: the statistics, the stored distances from the tile's
 // maximum, or (with the log-sum-exp known) the gradient of the logits
 enum : int { kWantStats = 1, kWantGap = 2, kWantGrad = 4 };
 
-// The operands as a product reads them: A, B, and the Markov part's B.  K-major ones in one
-// box a K-block, MN-major ones in one box of several 64-column chunks (or, where rows are
-// not whole chunks, in one box for each chunk).
+// The operands as a product reads them: A, B, and the Markov part's B of the logits or dX; A
+// and B of dW.  K-major ones in one box a K-block, MN-major ones in one box of several
+// 64-column chunks (or, where rows are not whole chunks, in one box for each chunk).
 struct Maps {
-  CUtensorMap a, b, b2;
+  CUtensorMap a, b, b2, wa, wb;
+};
+
+// 256-column tiles of X's two parts that a gradient is computed for.
+struct Columns {
+  int head, markov;
+  __host__ __device__ int all() const { return head + markov; }
 };
 
 struct TcArgs {
@@ -79,73 +86,138 @@ struct TcArgs {
   int v0, v1;          // compact head rows of this piece
   int want;            // kWant...
   int first;           // dX: the first piece (later ones add)
-  int n_head, n_markov;  // 256-column tiles of X's two parts that are computed
+  Columns dx, dw;
   int chunked;         // dX: lm_head rows are whole 64-column chunks
   int zero0, zero1;    // the share of the plan's zeros this launch writes, in 1/64
 };
 
+constexpr int kZeroShare = 34;    // of the zeros the logits write, in 1/64; dX the others
+constexpr int kRowGroup = 24;     // M tiles whose rows of X are kept in L2 together
+
 // One unit of work: a tile of the result and a range of K-blocks.
 struct Unit {
-  int m, n;            // first row of the tile (of M), tile index of N
+  int m, c0;           // first row (of M) and column (of N) of the tile
+  int wide;            // its columns are 256, not 128
+  bool markov, dw;
   int kb0, kb1;
   int split;
 };
 
+// The units of one CTA (or pair), in order.
 template <int MODE, int CG>
-__device__ __forceinline__ int unit_count(const TcArgs& g, int n_tok, int n_voc,
-                                          int splits) {
-  const int mt = (n_tok + kTileM * CG - 1) / (kTileM * CG);
-  const int cols = max(0, min(g.v1, n_voc) - g.v0);
-  const int nt = g.n_head + g.n_markov;
-  if (MODE == kLogits) return mt * ((cols + kTileN - 1) / kTileN);
-  if (MODE == kDx) return mt * nt * splits;
-  return (cols + kTileM * CG - 1) / (kTileM * CG) * nt;
-}
+struct Sequence {
+  static constexpr int kRows = kTileM * CG;
+  int me, ctas;                 // this CTA (pair) among all
+  int mt, vt, nkb, tkb;         // row tiles, head-row tiles, K-blocks of head rows, of rows
+  int splits, n_dx, n_dw;       // units of dX, dW
+  int mine_dx, common, spare;   // kGrads: see below
+  int Hp, Kx, units;
+  Columns cx, cw;
 
-constexpr int kZeroShare = 34;    // of the zeros the logits write, in 1/64; dX the others
-constexpr int kRowGroup = 24;     // M tiles whose rows of X are kept in L2 together
+  __device__ __forceinline__ Sequence(const TcArgs& g, int n_tok, int n_voc, int splits_, int me_,
+                                      int ctas_)
+      : me(me_), ctas(ctas_), splits(splits_), Hp(g.p.Hp), Kx(g.p.Kx), cx(g.dx), cw(g.dw) {
+    const int cols = max(0, min(g.v1, n_voc) - g.v0);
+    mt = (n_tok + kRows - 1) / kRows;
+    vt = (cols + (MODE == kLogits ? kTileN : kRows) - 1) / (MODE == kLogits ? kTileN : kRows);
+    nkb = (cols + kBlockK - 1) / kBlockK;
+    tkb = (n_tok + kBlockK - 1) / kBlockK;
+    n_dx = mt * cx.all() * splits;
+    n_dw = vt * cw.all();
+    units = MODE == kLogits ? mt * vt : MODE == kDx ? n_dx : n_dw;
+    if (MODE != kGrads) return;
+    // dX first, in turn; `more` CTAs have one unit of it more than the others.  Then dW: the
+    // first `common` rounds go to everyone, and the rest to those with fewer units of dX, so
+    // that all end together.  Costs in 1/16 K-blocks: 12 blocks for a partial result of dX; a
+    // tile of dW takes 11 at least (measured from 1 to 12 K-blocks: 6 to 13).
+    const int more = n_dx % ctas;
+    mine_dx = n_dx / ctas + (me < more ? 1 : 0);
+    spare = ctas - more;
+    common = (n_dw + ctas - 1) / ctas;
+    if (more > 0) {
+      // (in integers, so that every warp and CTA finds the same)
+      const long long cost_x = 16ll * nkb / splits + 192, cost_w = max(16 * tkb + 32, 176);
+      const long long each = (n_dx * cost_x + n_dw * cost_w) / ctas;
+      const long long left = each - (n_dx / ctas + 1) * cost_x;
+      // the rounds that fit before the average end, or one more: whichever ends first
+      const int c = (int)min((long long)common, max(0ll, left / cost_w));
+      auto end_of = [&](int rounds) {
+        const long long rest = max(0ll, (long long)n_dw - (long long)rounds * ctas);
+        return max(cost_x + rounds * cost_w, (rounds + (rest + spare - 1) / spare) * cost_w);
+      };
+      common = min(common, end_of(c) <= end_of(c + 1) ? c : c + 1);
+    }
+  }
 
-template <int MODE, int CG>
-__device__ __forceinline__ Unit unit_at(const TcArgs& g, int u, int n_tok, int n_voc,
-                                        int splits) {
-  Unit t;
-  const int mt = (n_tok + kTileM * CG - 1) / (kTileM * CG);
-  const int cols = max(0, min(g.v1, n_voc) - g.v0);
-  const int nt = g.n_head + g.n_markov;
-  t.kb0 = 0;
-  t.split = 0;
-  if (MODE == kLogits) {
-    // head-row tiles in order, all M tiles of a group for each: the head streams once for
-    // every group
-    const int vt = (cols + kTileN - 1) / kTileN;
-    const int grp = u / (kRowGroup * vt), in = u - grp * kRowGroup * vt;
-    const int rows = min(kRowGroup, mt - grp * kRowGroup);
-    t.m = (grp * kRowGroup + in % rows) * kTileM * CG;
-    t.n = in / rows;
-    t.kb1 = g.p.Kx / kBlockK;
-  } else if (MODE == kDx) {
+  __device__ __forceinline__ Unit dx(int u) const {
     // splits of K in order, so that the CTAs at work share their operands' K range in L2
-    const int nkb = (cols + kBlockK - 1) / kBlockK;
+    Unit t;
+    const int nt = cx.all();
+    t.dw = false;
     t.split = u / (mt * nt);
     const int in = u % (mt * nt);
-    t.m = in / nt * kTileM * CG;
-    t.n = in % nt;
+    t.m = in / nt * kRows;
+    columns(t, cx, in % nt);
     t.kb0 = (int)((long long)nkb * t.split / splits);
     t.kb1 = (int)((long long)nkb * (t.split + 1) / splits);
-  } else {
-    t.m = u / nt * kTileM * CG;
-    t.n = u % nt;
-    t.kb1 = (n_tok + kBlockK - 1) / kBlockK;
+    return t;
   }
-  return t;
-}
+  __device__ __forceinline__ Unit dw(int u) const {
+    Unit t;
+    const int nt = cw.all();
+    t.dw = true;
+    t.split = 0;
+    t.m = u / nt * kRows;
+    columns(t, cw, u % nt);
+    t.kb0 = 0;
+    t.kb1 = tkb;
+    return t;
+  }
+  // N tile n: the head's columns, then the Markov part's; the last tile of a part may be narrow
+  __device__ __forceinline__ void columns(Unit& t, const Columns& c, int n) const {
+    t.markov = n >= c.head;
+    t.c0 = t.markov ? Hp + (n - c.head) * kTileN : n * kTileN;
+    t.wide = (t.markov ? Kx : Hp) - t.c0 > kTileN / 2;
+  }
+  __device__ __forceinline__ Unit logits(int u) const {
+    // head-row tiles in order, all M tiles of a group for each: the head streams once for
+    // every group
+    Unit t;
+    const int grp = u / (kRowGroup * vt), in = u - grp * kRowGroup * vt;
+    const int rows = min(kRowGroup, mt - grp * kRowGroup);
+    t.m = (grp * kRowGroup + in % rows) * kRows;
+    t.c0 = in / rows * kTileN;
+    t.wide = 1;
+    t.markov = t.dw = false;
+    t.kb0 = 0;
+    t.kb1 = Kx / kBlockK;
+    t.split = 0;
+    return t;
+  }
 
-// Column of X at which N tile n starts, and whether it is of the Markov part.
-__device__ __forceinline__ bool column_tile(const TcArgs& g, int n, int* c0) {
-  const bool markov = n >= g.n_head;
-  *c0 = markov ? g.p.Hp + (n - g.n_head) * kTileN : n * kTileN;
-  return markov;
-}
+  // this CTA's i-th unit; false past the last
+  __device__ __forceinline__ bool get(int i, Unit& t) const {
+    if (MODE == kGrads) {
+      if (i < mine_dx) {
+        t = dx(me + i * ctas);
+        return true;
+      }
+      const int j = i - mine_dx;
+      int u = me + j * ctas;
+      if (j >= common) {
+        if (me < ctas - spare) return false;
+        u = common * ctas + (j - common) * spare + me - (ctas - spare);
+      }
+      if (u >= n_dw) return false;
+      t = dw(u);
+      return true;
+    }
+    const int u = me + i * ctas;
+    if (u >= units) return false;
+    t = MODE == kLogits ? logits(u) : MODE == kDx ? dx(u) : dw(u);
+    return true;
+  }
+};
 
 template <int CG>
 __device__ __forceinline__ void load_2d(uint8_t* dst, const CUtensorMap* m, uint64_t* bar,
@@ -166,6 +238,7 @@ __device__ __forceinline__ void load_chunks(uint8_t* dst, const CUtensorMap* m, 
 }
 
 // This CTA's part of the zeros of a launch, by one warp.
+template <int MODE>
 __device__ __forceinline__ void write_zeros(const TcArgs& g, int lane) {
   const uint4 none = make_uint4(0, 0, 0, 0);
   const int parts = (int)gridDim.x, part = (int)blockIdx.x;
@@ -173,7 +246,9 @@ __device__ __forceinline__ void write_zeros(const TcArgs& g, int lane) {
     const LossZero& q = g.p.zero[z];
     // items: rows, or 16-byte vectors (and the odd bytes, all fewer than 16, at the end)
     const long long items = q.keep ? (long long)(q.bytes / q.row_bytes) : (long long)(q.bytes / 16);
-    const long long lo = items * g.zero0 / 64, n = items * g.zero1 / 64 - lo;
+    const int z0 = q.early ? (MODE == kLogits ? 0 : 64) : g.zero0;
+    const int z1 = q.early ? 64 : g.zero1;
+    const long long lo = items * z0 / 64, n = items * z1 / 64 - lo;
     const long long a = lo + n * part / parts, b = lo + n * (part + 1) / parts;
     if (q.keep) {
       const int per = q.row_bytes / 16;
@@ -189,7 +264,7 @@ __device__ __forceinline__ void write_zeros(const TcArgs& g, int lane) {
       uint4* v = reinterpret_cast<uint4*>(q.p);
 #pragma unroll 4
       for (long long k = a + lane; k < b; k += 32) v[k] = none;
-      if (g.zero1 == 64 && part == 0 && lane < (int)(q.bytes % 16)) q.p[items * 16 + lane] = 0;
+      if (z0 < 64 && z1 == 64 && part == 0 && lane < (int)(q.bytes % 16)) q.p[items * 16 + lane] = 0;
     }
   }
 }
@@ -247,9 +322,8 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
   pdl_wait();
   pdl_signal();
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc];
-  const int splits = MODE == kDx ? (int)p.ctrl[kLossSplits] : 1;
-  const int units = unit_count<MODE, CG>(g, n_tok, n_voc, splits);
-  const int u0 = blockIdx.x / CG, step = gridDim.x / CG;
+  const int splits = MODE == kDx || MODE == kGrads ? (int)p.ctrl[kLossSplits] : 1;
+  const Sequence<MODE, CG> seq(g, n_tok, n_voc, splits, blockIdx.x / CG, gridDim.x / CG);
 
   auto give_up = [&]() {
     *abort_flag = 1;
@@ -279,12 +353,12 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
           }
         }
       };
-      for (int u = u0; u < units && ok; u += step) {
-        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc, splits);
+      Unit t;
+      for (int i = 0; ok && seq.get(i, t); ++i) {
         const int ma = t.m + (int)rank * kTileM;             // this CTA's rows of M
-        const int half = (int)rank * (kTileN / CG);          // and its share of N
+        const int half = (int)rank * (kTileN / CG) >> (t.wide ? 0 : 1);   // and its share of N
         if (MODE == kLogits) {
-          const int v = g.v0 + t.n * kTileN + half, hb = p.Hp / kBlockK;
+          const int v = g.v0 + t.c0 + half, hb = p.Hp / kBlockK;
           run(t.kb0, hb, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
             load_2d<CG>(a, &maps.a, bar, lead, k, ma);
             load_2d<CG>(b, &maps.b, bar, lead, k, v);
@@ -295,24 +369,28 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             for (int j = 0; j < kBoxB; ++j)
               load_2d<CG>(b + j * kBox, &maps.b2, bar, lead, v + 64 * j, k - p.Hp);
           });
-        } else if (MODE == kDx) {
-          int c0;
-          const bool markov = column_tile(g, t.n, &c0);
+        } else if (MODE == kDw || (MODE == kGrads && t.dw)) {
+          const int ca = ma / 64, cb = (t.c0 + half) / 64;
+          run(t.kb0, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
+            load_chunks<CG>(a, &maps.wa, bar, lead, k, ca);
+            load_chunks<CG>(b, &maps.wb, bar, lead, k, cb);
+          });
+        } else {
           const int v0 = g.v0;
-          if (markov) {
-            const int c = c0 - p.Hp + half;
+          if (t.markov) {
+            const int c = t.c0 - p.Hp + half;
             run(t.kb0, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
               load_2d<CG>(a, &maps.a, bar, lead, k, ma);
               load_2d<CG>(b, &maps.b2, bar, lead, v0 + k, c);
             });
           } else if (g.chunked) {
-            const int c = (c0 + half) / 64;
+            const int c = (t.c0 + half) / 64;
             run(t.kb0, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
               load_2d<CG>(a, &maps.a, bar, lead, k, ma);
               load_chunks<CG>(b, &maps.b, bar, lead, v0 + k, c);
             });
           } else {
-            const int c = c0 + half;
+            const int c = t.c0 + half;
             run(t.kb0, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
               load_2d<CG>(a, &maps.a, bar, lead, k, ma);
 #pragma unroll
@@ -320,14 +398,6 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
                 load_2d<CG>(b + j * kBox, &maps.b, bar, lead, c + 64 * j, v0 + k);
             });
           }
-        } else {
-          int c0;
-          column_tile(g, t.n, &c0);
-          const int ca = ma / 64, cb = (c0 + half) / 64;
-          run(t.kb0, t.kb1, [&](int k, uint8_t* a, uint8_t* b, uint64_t* bar, uint32_t lead) {
-            load_chunks<CG>(a, &maps.a, bar, lead, k, ca);
-            load_chunks<CG>(b, &maps.b, bar, lead, k, cb);
-          });
         }
       }
       if (!ok) {
@@ -351,9 +421,12 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       bool ok = true;
       const uint32_t base = ptx::smem_u32(smem);
       uint32_t d = 0, accum = 0;
+      Unit t;
       auto run = [&](auto a_mn_c, auto b_mn_c, int blocks) {
         constexpr bool a_mn = decltype(a_mn_c)::value, b_mn = decltype(b_mn_c)::value;
-        constexpr uint32_t idesc = ptx::idesc_bf16_f32(kTileM * CG, kTileN, a_mn, b_mn);
+        constexpr uint32_t wide = ptx::idesc_bf16_f32(kTileM * CG, kTileN, a_mn, b_mn);
+        constexpr uint32_t narrow = ptx::idesc_bf16_f32(kTileM * CG, kTileN / 2, a_mn, b_mn);
+        const uint32_t idesc = MODE == kLogits || t.wide ? wide : narrow;
         const uint64_t da0 = a_mn ? ptx::desc_mnmajor_sw128(base, kBox, 1024)
                                   : ptx::desc_kmajor_sw128(base);
         const uint64_t db0 = b_mn ? ptx::desc_mnmajor_sw128(base + kStageA, kBox, 1024)
@@ -387,10 +460,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       };
       using Mn = std::true_type;
       using K = std::false_type;
-      for (int u = u0; u < units; u += step) {
-        const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc, splits);
-        int c0 = 0;
-        const bool markov = MODE != kLogits && column_tile(g, t.n, &c0);
+      for (int i = 0; seq.get(i, t); ++i) {
         for (int kb = t.kb0, part = 0; part == 0 || kb < t.kb1; ++part, ++local) {
           const int end = MODE == kLogits ? min(t.kb1, kb + kSumBlocks<CG>) : t.kb1;
           const uint32_t acc = local & 1, aph = (local >> 1) & 1;
@@ -406,13 +476,12 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             const int head = max(0, min(end, p.Hp / kBlockK) - kb);
             run(K{}, K{}, head);
             if (ok) run(K{}, Mn{}, end - kb - head);
-          } else if (MODE == kDx) {
-            if (markov)
-              run(K{}, K{}, end - kb);
-            else
-              run(K{}, Mn{}, end - kb);
-          } else {
+          } else if (MODE == kDw || (MODE == kGrads && t.dw)) {
             run(Mn{}, Mn{}, end - kb);
+          } else if (t.markov) {
+            run(K{}, K{}, end - kb);
+          } else {
+            run(K{}, Mn{}, end - kb);
           }
           kb = end;
           if (!ok) break;
@@ -431,7 +500,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       ptx::mbar_wait(drain, 0, kWaitBudget, nullptr);
     }
   } else if (warp == kEpiWarps + 2) {
-    if (MODE != kDw && g.zero1 > g.zero0) write_zeros(g, lane);
+    if (MODE != kDw && g.zero1 > g.zero0) write_zeros<MODE>(g, lane);
   } else {
     // ---------------------------------------------------------------- epilogue
     const int quad = warp % 4, half = warp / 4;       // lanes and columns of this warp
@@ -460,13 +529,13 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       }
       ++local;
     };
-    for (int u = u0; u < units && ok; u += step) {
-      const Unit t = unit_at<MODE, CG>(g, u, n_tok, n_voc, splits);
+    Unit t;
+    for (int i = 0; ok && seq.get(i, t); ++i) {
       const int m = t.m + (int)rank * kTileM + quad * 32 + lane;   // this thread's row of M
       if (MODE == kLogits) {
         const bool live = m < n_tok;
         const int lab = live ? p.lab[m] : -1;
-        const int v0 = g.v0 + t.n * kTileN + half * 128;     // compact head row of column 0
+        const int v0 = g.v0 + t.c0 + half * 128;             // compact head row of column 0
         const int n_in = n_voc - v0;                          // columns that exist
         float z[128];
         for (int kb = t.kb0; kb < t.kb1; kb += kSumBlocks<CG>) {
@@ -546,10 +615,9 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
         if (!acc_wait()) break;
         const uint32_t at = at0 + (local & 1) * kTileN;
         const bool none = t.kb1 <= t.kb0;             // (nothing was accumulated)
-        int c0;
-        const bool markov = column_tile(g, t.n, &c0);
-        c0 += half * 128;
-        if (MODE == kDx) {
+        const bool markov = t.markov;
+        const int c0 = t.c0 + half * 128;
+        if (MODE == kDx || (MODE == kGrads && !t.dw)) {
           const int width = min(128, (markov ? p.Kx : p.Hp) - c0);
           float* dx = p.dxp + ((size_t)t.split * p.Tp + m) * p.Kx + c0;
 #pragma unroll 1
@@ -704,32 +772,32 @@ bool make_maps(const TcArgs& g, Maps* m) {
   constexpr int share = kTileN / CG;                   // rows of N a CTA stages
   const void* w = p.wc ? p.wc : p.lm_head;
   const void* w2 = p.wc ? p.w2c : p.w2;
-  bool ok;
+  bool ok = true;
   if (MODE == kLogits) {
     ok = map_2d(&m->a, p.x, p.Kx, p.Tp, p.Kx, kTileM) && map_2d(&m->b, w, p.H, p.Vh, p.H, share);
     m->b2 = m->b;
     if (p.r > 0) ok = ok && map_2d(&m->b2, w2, p.Vh, p.r, p.Vh, 64);
-  } else if (MODE == kDx) {
+  }
+  if (MODE == kDx || MODE == kGrads) {
     ok = map_2d(&m->a, p.q, p.ldq, p.Tp, p.ldq, kTileM) &&
          (g.chunked ? map_chunks(&m->b, w, p.H, p.Vh, share / 64)
                     : map_2d(&m->b, w, p.H, p.Vh, p.H, 64));
     m->b2 = m->b;
     if (p.r > 0) ok = ok && map_2d(&m->b2, w2, p.Vh, p.r, p.Vh, share);
-  } else {
-    ok = map_chunks(&m->a, p.q, p.ldq, p.Tp, kTileM / 64) &&
-         map_chunks(&m->b, p.x, p.Kx, p.Tp, share / 64);
-    m->b2 = m->b;
   }
+  if (MODE == kDw || MODE == kGrads)
+    ok = ok && map_chunks(&m->wa, p.q, p.ldq, p.Tp, kTileM / 64) &&
+         map_chunks(&m->wb, p.x, p.Kx, p.Tp, share / 64);
   return ok;
 }
 
 template <int MODE, int CG>
 cudaError_t launch(const TcArgs& g, long long tiles) {
   if (tiles <= 0) return cudaSuccess;
-  Maps maps;
+  Maps maps = {};
   if (!make_maps<MODE, CG>(g, &maps)) return cudaErrorInvalidValue;
   constexpr uint32_t stage = 2 * kBox + kTileN / CG / 64 * kBox;
-  constexpr uint32_t fixed = 1024 + kBarBytes + (MODE == kDw ? kStaging : 0);
+  constexpr uint32_t fixed = 1024 + kBarBytes + (MODE == kDw || MODE == kGrads ? kStaging : 0);
   constexpr int stages = (kSmemMax - fixed) / stage;
   constexpr size_t smem = fixed + (size_t)stages * stage;
   int sms = 0;
@@ -779,32 +847,29 @@ cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats,
   return single(p.T) ? launch<kLogits, 1>(g, tiles) : launch<kLogits, 2>(g, tiles);
 }
 
-cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first) {
+// The two gradient products of columns [v0, v1), in one launch of pairs where both are asked
+// for: alone, each leaves pairs without work at its end (frozen 512-row case 957 -> 935 us, four
+// pieces of 1001 rows 507 -> 446 us).
+cudaError_t launch_loss_grads_tc(const LossPlan& p, int v0, int v1, bool first) {
   TcArgs g{};
   g.p = p;
   g.v0 = v0;
   g.v1 = v1;
   g.first = first;
   g.chunked = p.H % 64 == 0;
-  if (first && p.n_zero > 0) {
+  const int head = (p.Hp + kTileN - 1) / kTileN, markov = (p.rp + kTileN - 1) / kTileN;
+  g.dx = {p.d_hidden ? head : 0, p.d_w1 ? markov : 0};
+  g.dw = {p.d_lm_head ? head : 0, p.d_w2 ? markov : 0};
+  if (first && p.n_zero > 0 && g.dx.all() > 0) {
     g.zero0 = kZeroShare;
     g.zero1 = 64;
   }
-  g.n_head = p.d_hidden ? (p.Hp + kTileN - 1) / kTileN : 0;
-  g.n_markov = p.d_w1 ? (p.rp + kTileN - 1) / kTileN : 0;
-  const long long tiles = (long long)row_tiles(p.T) * (g.n_head + g.n_markov) * p.splits;
-  return single(p.T) ? launch<kDx, 1>(g, tiles) : launch<kDx, 2>(g, tiles);
-}
-
-cudaError_t launch_loss_dw_tc(const LossPlan& p, int v0, int v1) {
-  TcArgs g{};
-  g.p = p;
-  g.v0 = v0;
-  g.v1 = v1;
-  g.n_head = p.d_lm_head ? (p.Hp + kTileN - 1) / kTileN : 0;
-  g.n_markov = p.d_w2 ? (p.rp + kTileN - 1) / kTileN : 0;
-  const long long tiles = (long long)((v1 - v0 + 255) / 256) * (g.n_head + g.n_markov);
-  return launch<kDw, 2>(g, tiles);
+  const long long n_dx = (long long)row_tiles(p.T) * g.dx.all() * p.splits;
+  const long long n_dw = (long long)((v1 - v0 + 255) / 256) * g.dw.all();
+  if (n_dx > 0 && n_dw > 0 && !single(p.T)) return launch<kGrads, 2>(g, n_dx + n_dw);
+  cudaError_t e = single(p.T) ? launch<kDx, 1>(g, n_dx) : launch<kDx, 2>(g, n_dx);
+  if (e == cudaSuccess) e = launch<kDw, 2>(g, n_dw);
+  return e;
 }
 
 }  // namespace dspark

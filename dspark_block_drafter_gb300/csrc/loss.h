@@ -26,12 +26,14 @@ enum : int {
 };
 
 // Gradient memory that no product writes: `bytes` from `p` on, or, with `keep`, the rows of
-// `row_bytes` whose keep entry is negative.
+// `row_bytes` whose keep entry is negative.  `early`: dW writes there too, so the zeros come
+// before it.
 struct LossZero {
   char* p;
   size_t bytes;
   const int32_t* keep;
   int row_bytes;
+  bool early;
 };
 
 struct LossPlan {
@@ -119,13 +121,11 @@ cudaError_t launch_loss_dx(const LossPlan& p);           // d_hidden and d_w1 fr
 // k_loss_simt.cu (fp32, on the CUDA cores)
 int loss_simt_splits(int T, int Kx, int cols);
 cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stats, bool store);
-cudaError_t launch_loss_dx_simt(const LossPlan& p, int v0, int v1, bool first);
-cudaError_t launch_loss_dw_simt(const LossPlan& p, int v0, int v1);
+cudaError_t launch_loss_grads_simt(const LossPlan& p, int v0, int v1, bool first);   // dX, dW
 // k_loss_tc.cu (bf16, on the tensor cores).  The logits with statistics and the first dX also
-// write the plan's zeros, each a share (all in the logits when there is no dX).
+// write the plan's zeros, each a share (all in the logits when there is no dX, or early).
 int loss_tc_splits(int T, int Hp, int rp);   // the most that may be chosen
 cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats, bool store);
-cudaError_t launch_loss_dx_tc(const LossPlan& p, int v0, int v1, bool first);
-cudaError_t launch_loss_dw_tc(const LossPlan& p, int v0, int v1);
+cudaError_t launch_loss_grads_tc(const LossPlan& p, int v0, int v1, bool first);   // dX, dW
 
 }  // namespace dspark
