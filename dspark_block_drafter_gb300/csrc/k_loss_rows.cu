@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
   if (i >= n_tok) return;
   uint4* q = (uint4*)((uint16_t*)p.q + (size_t)i * p.ldq);
   const float2* st = p.stat + (size_t)i * p.n_stat;
-  const float lse = p.lse[i], w = p.wrow[i];
+  const float lse = p.lse[i], w = p.wrow[i], log2_w = log2f(w);   // (w = 0: -inf, e = 0)
   const int lab = p.lab[i], end = (n_voc + 255) / 256 * 32, tiles = (n_voc + 127) / 128;
   const int step = gridDim.y * blockDim.x;
   for (int c0 = blockIdx.y * blockDim.x + threadIdx.x; c0 < end; c0 += 2 * step) {
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
       if (c >= end) break;
       x[h] = q[c];
       // (a tile past the last is all far)
-      s[h] = (st[min(c / 16, tiles - 1)].x - lse) * 1.44269504f;
+      s[h] = fmaf(st[min(c / 16, tiles - 1)].x - lse, 1.44269504f, log2_w);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -402,15 +402,14 @@ __global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const __nv_bfloat162 b =
-            __floats2bfloat162_rn(w * loss_gap_exp(g[j] & 0xFFFFu, s[h]),
-                                  w * loss_gap_exp(g[j] >> 16, s[h]));
+            __floats2bfloat162_rn(loss_gap_exp(g[j] & 0xFFFFu, s[h]), loss_gap_exp(g[j] >> 16, s[h]));
         o[j] = *reinterpret_cast<const uint32_t*>(&b);
       }
       q[c] = make_uint4(o[0], o[1], o[2], o[3]);
       if (lab / 8 == c) {
         const uint32_t gap = (g[lab % 8 / 2] >> (16 * (lab & 1))) & 0xFFFFu;
         reinterpret_cast<__nv_bfloat16*>(q)[lab] =
-            loss_label_grad(p, i, w * loss_gap_exp(gap, s[h]) - w);
+            loss_label_grad(p, i, loss_gap_exp(gap, s[h]) - w);
       }
     }
   }

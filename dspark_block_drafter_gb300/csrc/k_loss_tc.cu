@@ -581,7 +581,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
           ref = top > -INFINITY ? top : 0.f;      // (a NaN passes the maximum, not the sum)
           float sum[4] = {};
 #pragma unroll
-          for (int j = 0; j < 128; ++j) sum[j % 4] += __expf(z[j] - ref);
+          for (int j = 0; j < 128; ++j) sum[j % 4] += loss_exp(z[j] - ref);
           if (live && n_in > 0)
             p.stat[(size_t)m * p.n_stat + v0 / 128] =
                 make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -598,7 +598,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             for (int j = 0; j < 16; j += 2) {
               const float d0 = z[c + j] - ref, d1 = z[c + j + 1] - ref;
               if (g.want & kWantGrad) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(wt * __expf(d0), wt * __expf(d1));
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(wt * loss_exp(d0), wt * loss_exp(d1));
                 o[j / 2] = *reinterpret_cast<const uint32_t*>(&b2);
               } else {
                 o[j / 2] = __byte_perm(loss_gap(-d0), loss_gap(-d1), 0x5410);
@@ -609,7 +609,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
           }
           if ((g.want & kWantGrad) && here)       // (after this thread's vector store)
             reinterpret_cast<__nv_bfloat16*>(qrow)[lab - v0] =
-                loss_label_grad(p, m, wt * __expf(zl - ref) - wt);
+                loss_label_grad(p, m, wt * loss_exp(zl - ref) - wt);
         }
       } else {
         if (!acc_wait()) break;

@@ -102,10 +102,18 @@ __device__ __forceinline__ uint32_t loss_gap(float d) {
   const float t = fminf(fmaf(d, kLossSteps, 8388608.f), 8388608.f + 65535.f);
   return __float_as_uint(t) & 0xFFFFu;
 }
+// 2^x and e^x of the hardware, results below 2^-126 taken as 0 (to keep those takes three more
+// instructions, for probabilities that no bf16 gradient shows)
+__device__ __forceinline__ float loss_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float loss_exp(float x) { return loss_exp2(x * 1.44269504f); }
 // scale * exp(-distance), given log2(scale)
 __device__ __forceinline__ float loss_gap_exp(uint32_t gap, float log2_scale) {
   const float d = __uint_as_float(0x4B000000u | gap) - 8388608.f;
-  const float e = exp2f(fmaf(d, -1.44269504f / kLossSteps, log2_scale));
+  const float e = loss_exp2(fmaf(d, -1.44269504f / kLossSteps, log2_scale));
   return gap == kLossFar ? 0.f : e;
 }
 
