@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(256) loss_dz_f32(const LossPlan p, int v0, int
   const float lse = p.lse[i], w = p.wrow[i];
   const int lab = p.lab[i];
   for (int v = v0 + blockIdx.y * blockDim.x + threadIdx.x; v < end; v += gridDim.y * blockDim.x)
-    q[v - v0] = w * (__expf(q[v - v0] - lse) - (v == lab ? 1.f : 0.f));
+    q[v - v0] = v == lab ? loss_label_entry(p, i) : w * __expf(q[v - v0] - lse);
 }
 
 // The same in bf16 from the stored distances (one piece: v0 = 0), over whole 256-column
@@ -406,11 +406,7 @@ __global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
         o[j] = *reinterpret_cast<const uint32_t*>(&b);
       }
       q[c] = make_uint4(o[0], o[1], o[2], o[3]);
-      if (lab / 8 == c) {
-        const uint32_t gap = (g[lab % 8 / 2] >> (16 * (lab & 1))) & 0xFFFFu;
-        reinterpret_cast<__nv_bfloat16*>(q)[lab] =
-            loss_label_grad(p, i, loss_gap_exp(gap, s[h]) - w);
-      }
+      if (lab / 8 == c) reinterpret_cast<__nv_bfloat16*>(q)[lab] = loss_label_entry_bf16(p, i);
     }
   }
 }

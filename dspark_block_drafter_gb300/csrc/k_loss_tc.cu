@@ -565,11 +565,12 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             if (j >= n_in) z[j] = -INFINITY;
         }
         const bool here = lab >= v0 && lab < v0 + 128;
-        float zl = 0.f;                           // the label's logit
-        if (__any_sync(0xFFFFFFFFu, here)) {
+        if ((g.want & kWantStats) && __any_sync(0xFFFFFFFFu, here)) {
+          float zl = 0.f;                         // the label's logit
 #pragma unroll
           for (int j = 0; j < 128; ++j)
             if (lab == v0 + j) zl = z[j];
+          if (here) p.zlab[m] = zl;
         }
         float ref = 0.f, wt = 0.f;
         if (g.want & kWantStats) {
@@ -577,7 +578,6 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
 #pragma unroll
           for (int j = 0; j < 128; ++j) mx[j % 4] = fmaxf(mx[j % 4], z[j]);
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (here) p.zlab[m] = zl;
           ref = top > -INFINITY ? top : 0.f;      // (a NaN passes the maximum, not the sum)
           float sum[4] = {};
 #pragma unroll
@@ -608,8 +608,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             ptx::st_global_v8(qrow + c, o);
           }
           if ((g.want & kWantGrad) && here)       // (after this thread's vector store)
-            reinterpret_cast<__nv_bfloat16*>(qrow)[lab - v0] =
-                loss_label_grad(p, m, wt * loss_exp(zl - ref) - wt);
+            reinterpret_cast<__nv_bfloat16*>(qrow)[lab - v0] = loss_label_entry_bf16(p, m);
         }
       } else {
         if (!acc_wait()) break;

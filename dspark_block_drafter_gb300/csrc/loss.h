@@ -78,11 +78,17 @@ struct LossPlan {
   cudaStream_t stream;
 };
 
-// The label's entry of row i of q, rounded to bf16; what the rounding lost is kept for the
-// gradient of X (this entry, about -w, makes up most of it).
-__device__ __forceinline__ float loss_label_grad(const LossPlan& p, int i, float x) {
-  const float b = __bfloat162float(__float2bfloat16(x));
-  p.qres[i] = x - b;
+// The label's entry of row i of q: w (p - 1) = w expm1(-loss), which loses no digits where p
+// is nearly 1.
+__device__ __forceinline__ float loss_label_entry(const LossPlan& p, int i) {
+  return p.wrow[i] * expm1f(-p.loss[p.tok[i]]);
+}
+// The same rounded to bf16; what the rounding lost is kept for the gradient of X (this entry
+// makes up most of it).
+__device__ __forceinline__ __nv_bfloat16 loss_label_entry_bf16(const LossPlan& p, int i) {
+  const float x = loss_label_entry(p, i);
+  const __nv_bfloat16 b = __float2bfloat16(x);
+  p.qres[i] = x - __bfloat162float(b);
   return b;
 }
 
