@@ -142,7 +142,7 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
   };
   zero(p->d_w1, es * c->V * c->r, nullptr, 0, false);
   if (h->lm_bias) {
-    // (fp32: all of it, by a memset)
+    // (fp32: all of it)
     zero(p->d_lm_head, es * Vh * c->H, tc ? p->vinv : nullptr, es * c->H, false);
     zero(p->d_w2, es * Vh * c->r, nullptr, 0, true);
   }
@@ -157,12 +157,12 @@ static cudaError_t run_loss(const LossPlan& p) {
   if (e != cudaSuccess) return e;
   const bool keep = p.grads && p.pieces == 1;
   e = logits(p, 0, p.Vh, true, keep);
-  if (e == cudaSuccess) e = launch_loss_rows(p);
+  if (e == cudaSuccess) e = launch_loss_rows(p, keep);
   if (e != cudaSuccess || !p.grads) return e;
   for (int c = 0; c < p.pieces; ++c) {
     const int v0 = c * p.piece_cols, v1 = std::min(p.Vh, v0 + p.piece_cols);
     if (!keep) e = logits(p, v0, v1, false, true);
-    if (e == cudaSuccess && (keep || !tc)) e = launch_loss_dz(p, v0, v1);
+    if (e == cudaSuccess && !keep && !tc) e = launch_loss_dz_f32(p, v0, v1);
     if (e == cudaSuccess) e = grads(p, v0, v1, c == 0);
     if (e != cudaSuccess) return e;
   }

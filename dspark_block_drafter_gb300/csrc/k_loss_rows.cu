@@ -261,128 +261,202 @@ __global__ void __launch_bounds__(kPlanThreads) loss_tokens(const LossPlan p) {
   }
 }
 
-// CTA t: row t's part of X (or its zero outputs, when it carries no loss), and X's padding
-// row t.
+// fp32: the plan's zeros, by all CTAs of the launch (bf16 writes them beside its products).
 template <typename E>
-__global__ void __launch_bounds__(256) loss_gather(const LossPlan p) {
-  pdl_wait();
-  pdl_signal();
-  const int t = blockIdx.x;
-  E* x = (E*)p.x;
-  if (t >= (int)p.ctrl[kLossTok]) zero_row(x + (size_t)t * p.Kx, p.Kx);
-  if (t >= p.T) return;
-  const int i = p.pos[t];
+__device__ __forceinline__ void zero_outputs(const LossPlan& p) {
+  if (sizeof(E) != 4) return;
+  for (int z = 0; z < p.n_zero; ++z) {
+    float* f = (float*)p.zero[z].p;
+    const size_t n = p.zero[z].bytes / 4;
+    for (size_t k = (size_t)blockIdx.x * blockDim.x + threadIdx.x; k < n;
+         k += (size_t)gridDim.x * blockDim.x)
+      f[k] = 0.f;
+  }
+}
+
+// Row t's part of X as compact row i, or its zero outputs when it carries no loss (i < 0).
+template <typename E>
+__device__ __forceinline__ void gather_row(const LossPlan& p, int t, int i, int prev) {
   if (i < 0) {
     if (threadIdx.x == 0) p.loss[t] = 0.f;
     if (p.d_hidden) zero_row((E*)p.d_hidden + (size_t)t * p.H, p.H);
     return;
   }
-  E* xi = x + (size_t)i * p.Kx;
+  E* xi = (E*)p.x + (size_t)i * p.Kx;
   copy_row(xi, (const E*)p.hidden + (size_t)t * p.H, p.H);
   if (p.H < p.Hp) zero_row(xi + p.H, p.Hp - p.H);
   if (p.rp) {
-    copy_row(xi + p.Hp, (const E*)p.w1 + (size_t)p.prevc[i] * p.r, p.r);
+    copy_row(xi + p.Hp, (const E*)p.w1 + (size_t)prev * p.r, p.r);
     if (p.r < p.rp) zero_row(xi + p.Hp + p.r, p.rp - p.r);
   }
 }
 
-// CTA i: joins row i's statistics over the vocabulary tiles into its log-sum-exp and its
-// loss; the last CTA to finish sums the losses.
-constexpr int kRowsThreads = 256;
-__global__ void __launch_bounds__(kRowsThreads) loss_rows(const LossPlan p) {
+// CTA t: row t's part of X, and X's padding row t.
+template <typename E>
+__global__ void __launch_bounds__(256) loss_gather(const LossPlan p) {
   pdl_wait();
   pdl_signal();
-  __shared__ float2 s_w[32];
-  __shared__ bool s_last;
-  const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc];
-  const int i = blockIdx.x, tid = threadIdx.x;
-  if (i < n_tok) {
-    const int n = (n_voc + p.stat_cols - 1) / p.stat_cols;
-    const float2* st = p.stat + (size_t)i * p.n_stat;
-    // running maximum and sum over sweeps of eight tiles a thread (a maximum of -inf: all
-    // its logits are, and its sum is 0)
-    float m = -INFINITY, s = 0.f;
-    for (int j0 = tid; j0 < n; j0 += 8 * kRowsThreads) {
-      float2 a[8];
-      float mm = m;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int j = j0 + q * kRowsThreads;
-        a[q] = j < n ? st[j] : make_float2(-INFINITY, 0.f);
-        mm = fmaxf(mm, a[q].x);
-      }
-      const float ref = mm > -INFINITY ? mm : 0.f;
-      s *= __expf(m - ref);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) s += a[q].y * __expf(a[q].x - ref);
-      m = mm;
-    }
-    // joined over the CTA: the maxima, then the sums at the common maximum
-    float mx = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    if (tid % 32 == 0) s_w[tid / 32].x = mx;
-    __syncthreads();
-    mx = s_w[0].x;
-#pragma unroll
-    for (int w = 1; w < kRowsThreads / 32; ++w) mx = fmaxf(mx, s_w[w].x);
-    const float ref = mx > -INFINITY ? mx : 0.f;
-    Sum2 v;
-    v.s = s * __expf(m - ref);
-    __syncthreads();
-    const Sum2 sum = block_sum(v, s_w);
-    if (tid == 0) {
-      const float l = logf(sum.value());
-      p.lse[i] = mx + l;
-      p.loss[p.tok[i]] = (mx - p.zlab[i]) + l;
-    }
-  }
-  if (tid == 0) {
-    __threadfence();
-    s_last = atomicAdd(p.ctrl + kLossDone, 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  Sum2 a;
-  for (int j = tid; j < n_tok; j += blockDim.x) {
-    // the product's rounding error goes into the sum too
-    const float w = p.wrow[j], x = __ldcg(p.loss + p.tok[j]), y = w * x;
-    a.add(y);
-    a.c += fmaf(w, x, -y);
-  }
-  const Sum2 t = block_sum(a, s_w);
-  if (tid == 0) *p.total = n_tok > 0 ? __uint_as_float(p.ctrl[kLossScale]) * t.value() : 0.f;
+  zero_outputs<E>(p);
+  const int t = blockIdx.x;
+  if (t >= (int)p.ctrl[kLossTok]) zero_row((E*)p.x + (size_t)t * p.Kx, p.Kx);
+  if (t >= p.T) return;
+  const int i = p.pos[t];
+  gather_row<E>(p, t, i, i >= 0 ? p.prevc[i] : 0);
 }
 
-// q = w (softmax - onehot) in place, columns [v0, v1): fp32 from stored logits.
-__global__ void __launch_bounds__(256) loss_dz_f32(const LossPlan p, int v0, int v1) {
+// loss_tokens and loss_gather in one launch, for few rows: every CTA looks at every row for
+// its own place among them, and CTA 0 writes down what loss_tokens does.  (Rows times rows of
+// work: taken up to kPlanFew rows, and not with a d2t map, whose searches would be repeated.)
+constexpr int kPlanFew = 512;
+template <typename E>
+__global__ void __launch_bounds__(256) loss_plan_few(const LossPlan p) {
   pdl_wait();
   pdl_signal();
-  const int n_tok = (int)p.ctrl[kLossTok], i = blockIdx.x;
-  if (i >= n_tok) return;
-  const int end = min(v1, (int)p.ctrl[kLossVoc]);
+  __shared__ int s_before[8], s_all[8];
+  __shared__ float2 s_w[32];
+  const int me = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const bool lead = me == 0;
+  if (lead) {
+    if (tid < 64 && tid != kLossVoc) p.ctrl[tid] = 0;
+    if (tid == 64 && !p.vlist) p.ctrl[kLossVoc] = (uint32_t)p.Vh;
+    __syncthreads();
+  }
+  int before = 0, all = 0;                        // rows with a loss: before `me`, in all
+  int mine = -1, prev = 0;                        // this CTA's own row
+  Sum2 wsum;
+  for (int t = tid; t < p.T; t += 256) {
+    int j = p.labels[t];
+    const int pv = p.r > 0 ? p.prev[t] : 0;
+    if (j >= p.V) {
+      if (lead) flag_error(p.ctrl, kErrBadToken);
+      j = -1;
+    }
+    if (j >= 0) j = loss_label_row(p, j);
+    if (j >= 0 && p.r > 0 && (pv < 0 || pv >= p.V)) {
+      if (lead) flag_error(p.ctrl, kErrBadToken);
+      j = -1;
+    }
+    all += j >= 0;
+    before += j >= 0 && t < me;
+    if (t == me) {
+      mine = j;
+      prev = pv;
+    }
+    if (lead && j >= 0) wsum.add(p.weights ? p.weights[t] : 1.f);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+    all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+  }
+  if (lane == 0) {
+    s_before[warp] = before;
+    s_all[warp] = all;
+  }
+  __shared__ int s_mine, s_prev;
+  if (tid == 0) s_mine = -1;
+  __syncthreads();
+  if (me < p.T && tid == me % 256) {              // (the thread that looked at row `me`)
+    s_mine = mine;
+    s_prev = prev;
+  }
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    before += s_before[w];
+    all += s_all[w];
+  }
+  const int label = s_mine;
+  zero_outputs<E>(p);
+  if (lead) {
+    if (warp == 0 && p.dxp) {
+      const int best = loss_pick_splits(p, all, (int)p.ctrl[kLossVoc], lane);
+      if (lane == 0) p.ctrl[kLossSplits] = (uint32_t)best;
+    }
+    const float w = block_sum(wsum, s_w).value();
+    if (tid == 0) {
+      p.ctrl[kLossTok] = (uint32_t)all;
+      float k = p.loss_scale;
+      if (p.reduction == 1) k = w > 0.f ? p.loss_scale / w : 0.f;
+      p.ctrl[kLossScale] = __float_as_uint(k);
+      if (p.n_rows) *p.n_rows = all;
+    }
+  }
+  if (me >= all) zero_row((E*)p.x + (size_t)me * p.Kx, p.Kx);
+  if (me >= p.T) return;
+  if (label >= 0 && tid == 0) {
+    p.tok[before] = me;
+    p.lab[before] = label;
+    p.prevc[before] = s_prev;
+    p.wrow[before] = p.weights ? p.weights[me] : 1.f;
+  }
+  gather_row<E>(p, me, label >= 0 ? before : -1, label >= 0 ? s_prev : 0);
+}
+
+// Row i's log-sum-exp and loss, from its statistics over the vocabulary tiles (thread 0 has
+// them; the CTA takes part).
+constexpr int kRowsThreads = 256;
+__device__ __forceinline__ float2 join_row(const LossPlan& p, int i, int n_voc, float2* s_w) {
+  const int tid = threadIdx.x, n = (n_voc + p.stat_cols - 1) / p.stat_cols;
+  const float2* st = p.stat + (size_t)i * p.n_stat;
+  // running maximum and sum over sweeps of eight tiles a thread (a maximum of -inf: all its
+  // logits are, and its sum is 0)
+  float m = -INFINITY, s = 0.f;
+  for (int j0 = tid; j0 < n; j0 += 8 * kRowsThreads) {
+    float2 a[8];
+    float mm = m;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int j = j0 + q * kRowsThreads;
+      a[q] = j < n ? st[j] : make_float2(-INFINITY, 0.f);
+      mm = fmaxf(mm, a[q].x);
+    }
+    const float ref = mm > -INFINITY ? mm : 0.f;
+    s *= __expf(m - ref);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s += a[q].y * __expf(a[q].x - ref);
+    m = mm;
+  }
+  // joined over the CTA: the maxima, then the sums at the common maximum
+  float mx = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+  if (tid % 32 == 0) s_w[tid / 32].x = mx;
+  __syncthreads();
+  mx = s_w[0].x;
+#pragma unroll
+  for (int w = 1; w < kRowsThreads / 32; ++w) mx = fmaxf(mx, s_w[w].x);
+  const float ref = mx > -INFINITY ? mx : 0.f;
+  Sum2 v;
+  v.s = s * __expf(m - ref);
+  __syncthreads();
+  const float l = logf(block_sum(v, s_w).value());
+  return make_float2(mx + l, (mx - p.zlab[i]) + l);
+}
+
+// q = w (softmax - onehot) of row i in place, fp32 from stored logits: columns [v0, v1), every
+// `parts`-th run of 256 of them from run `part` on.
+__device__ __forceinline__ void row_dz_f32(const LossPlan& p, int i, int v0, int v1, float lse,
+                                           float loss, int part, int parts) {
   float* q = (float*)p.q + (size_t)i * p.ldq;
-  const float lse = p.lse[i], w = p.wrow[i];
+  const float w = p.wrow[i];
   const int lab = p.lab[i];
-  for (int v = v0 + blockIdx.y * blockDim.x + threadIdx.x; v < end; v += gridDim.y * blockDim.x)
-    q[v - v0] = v == lab ? loss_label_entry(p, i) : w * __expf(q[v - v0] - lse);
+  for (int v = v0 + part * blockDim.x + threadIdx.x; v < v1; v += parts * blockDim.x)
+    q[v - v0] = v == lab ? loss_label_entry(w, loss) : w * __expf(q[v - v0] - lse);
 }
 
 // The same in bf16 from the stored distances (one piece: v0 = 0), over whole 256-column
 // tiles: columns past the vocabulary become 0.  Two vectors of eight columns a thread and
 // sweep; the thread that has the label's column writes it again.
-__global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
-  pdl_wait();
-  pdl_signal();
-  const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc], i = blockIdx.x;
-  if (i >= n_tok) return;
+__device__ __forceinline__ void row_dz_bf16(const LossPlan& p, int i, int n_voc, float lse,
+                                            float loss, int part, int parts) {
   uint4* q = (uint4*)((uint16_t*)p.q + (size_t)i * p.ldq);
   const float2* st = p.stat + (size_t)i * p.n_stat;
-  const float lse = p.lse[i], w = p.wrow[i], log2_w = log2f(w);   // (w = 0: -inf, e = 0)
+  const float w = p.wrow[i], log2_w = log2f(w);              // (w = 0: -inf, e = 0)
   const int lab = p.lab[i], end = (n_voc + 255) / 256 * 32, tiles = (n_voc + 127) / 128;
-  const int step = gridDim.y * blockDim.x;
-  for (int c0 = blockIdx.y * blockDim.x + threadIdx.x; c0 < end; c0 += 2 * step) {
+  const int step = parts * blockDim.x;
+  for (int c0 = part * blockDim.x + threadIdx.x; c0 < end; c0 += 2 * step) {
     uint4 x[2];
     float s[2];
 #pragma unroll
@@ -406,21 +480,96 @@ __global__ void __launch_bounds__(256) loss_dz_bf16(const LossPlan p) {
         o[j] = *reinterpret_cast<const uint32_t*>(&b);
       }
       q[c] = make_uint4(o[0], o[1], o[2], o[3]);
-      if (lab / 8 == c) reinterpret_cast<__nv_bfloat16*>(q)[lab] = loss_label_entry_bf16(p, i);
+      if (lab / 8 == c)
+        reinterpret_cast<__nv_bfloat16*>(q)[lab] =
+            loss_label_entry_bf16(p, i, loss_label_entry(w, loss));
     }
   }
 }
 
-// The compact head of a bias-form bf16 head: its rows (a warp each), then zeros up to a
-// multiple of 256, and below its columns of markov_w2.
-__global__ void __launch_bounds__(256) loss_gather_head(const LossPlan p) {
+// CTAs (i, 0 .. ): each joins row i's statistics, the first writes them down, and with DZ each
+// makes its part of the row's q (1: bf16, 2: fp32; one piece).  The last CTA to finish a row
+// sums the losses.
+template <int DZ>
+__global__ void __launch_bounds__(kRowsThreads) loss_rows(const LossPlan p) {
   pdl_wait();
   pdl_signal();
-  const int n = (int)p.ctrl[kLossVoc];
-  const int end = min(p.Vh, (n + 255) / 256 * 256), per = p.H / 8, lane = threadIdx.x % 32;
+  __shared__ float2 s_w[32];
+  __shared__ float2 s_row;
+  __shared__ bool s_last;
+  const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc];
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const bool first = blockIdx.y == 0;
+  if (i < n_tok) {
+    const float2 r = join_row(p, i, n_voc, s_w);
+    if (tid == 0) {
+      s_row = r;
+      if (first) {
+        p.lse[i] = r.x;
+        p.loss[p.tok[i]] = r.y;
+      }
+    }
+  }
+  if (first && tid == 0) {
+    __threadfence();
+    s_last = atomicAdd(p.ctrl + kLossDone, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (first && s_last) {
+    __threadfence();
+    Sum2 a;
+    for (int j = tid; j < n_tok; j += blockDim.x) {
+      // the product's rounding error goes into the sum too
+      const float w = p.wrow[j], x = __ldcg(p.loss + p.tok[j]), y = w * x;
+      a.add(y);
+      a.c += fmaf(w, x, -y);
+    }
+    const Sum2 t = block_sum(a, s_w);
+    if (tid == 0) *p.total = n_tok > 0 ? __uint_as_float(p.ctrl[kLossScale]) * t.value() : 0.f;
+  }
+  if (i >= n_tok) return;
+  const float2 r = s_row;
+  if (DZ == 1) row_dz_bf16(p, i, n_voc, r.x, r.y, blockIdx.y, gridDim.y);
+  if (DZ == 2) row_dz_f32(p, i, 0, n_voc, r.x, r.y, blockIdx.y, gridDim.y);
+}
+
+// q of columns [v0, v1) from stored logits, once the rows' log-sum-exps are known (pieces).
+__global__ void __launch_bounds__(256) loss_dz_f32(const LossPlan p, int v0, int v1) {
+  pdl_wait();
+  pdl_signal();
+  const int i = blockIdx.x;
+  if (i >= (int)p.ctrl[kLossTok]) return;
+  row_dz_f32(p, i, v0, min(v1, (int)p.ctrl[kLossVoc]), p.lse[i], p.loss[p.tok[i]], blockIdx.y,
+             gridDim.y);
+}
+
+// The compact head of a bias-form bf16 head, with zeros up to a multiple of 256: its rows, a
+// warp each, and behind the first `row_ctas` CTAs its columns of markov_w2, 256 columns x 8
+// rows a CTA.
+__global__ void __launch_bounds__(256) loss_gather_head(const LossPlan p, int row_ctas) {
+  pdl_wait();
+  pdl_signal();
+  const int n = (int)p.ctrl[kLossVoc], end = min(p.Vh, (n + 255) / 256 * 256);
+  if ((int)blockIdx.x >= row_ctas) {
+    const int b = blockIdx.x - row_ctas, groups = (p.r + 7) / 8;
+    const int j = b / groups * 256 + threadIdx.x, k0 = b % groups * 8;
+    if (j >= end) return;
+    const __nv_bfloat16* w2 = (const __nv_bfloat16*)p.w2;
+    __nv_bfloat16* w2c = (__nv_bfloat16*)p.w2c;
+    const int v = j < n ? p.vlist[j] : -1;
+    __nv_bfloat16 x[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      x[q] = v >= 0 && k0 + q < p.r ? w2[(size_t)(k0 + q) * p.Vh + v] : __float2bfloat16(0.f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (k0 + q < p.r) w2c[(size_t)(k0 + q) * p.Vh + j] = x[q];
+    return;
+  }
+  const int per = p.H / 8, lane = threadIdx.x % 32;
   const uint4* w = (const uint4*)p.lm_head;
   uint4* wc = (uint4*)p.wc;
-  for (int j = blockIdx.x * 8 + threadIdx.x / 32; j < end; j += gridDim.x * 8) {
+  for (int j = blockIdx.x * 8 + threadIdx.x / 32; j < end; j += row_ctas * 8) {
     const bool in = j < n;
     const size_t from = in ? (size_t)p.vlist[j] * per : 0;
     for (int k0 = lane; k0 < per; k0 += 8 * 32) {
@@ -434,29 +583,6 @@ __global__ void __launch_bounds__(256) loss_gather_head(const LossPlan p) {
       for (int q = 0; q < 8; ++q)
         if (k0 + 32 * q < per) wc[(size_t)j * per + k0 + 32 * q] = x[q];
     }
-  }
-}
-
-// CTA (x, y): 256 compact columns, rows 8 y ... of markov_w2.
-__global__ void __launch_bounds__(256) loss_gather_w2(const LossPlan p) {
-  pdl_wait();
-  pdl_signal();
-  const int n = (int)p.ctrl[kLossVoc], end = min(p.Vh, (n + 255) / 256 * 256);
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  if (j >= end) return;
-  const __nv_bfloat16* w2 = (const __nv_bfloat16*)p.w2;
-  __nv_bfloat16* w2c = (__nv_bfloat16*)p.w2c;
-  const int v = j < n ? p.vlist[j] : -1;
-  __nv_bfloat16 x[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int k = blockIdx.y * 8 + q;
-    x[q] = v >= 0 && k < p.r ? w2[(size_t)k * p.Vh + v] : __float2bfloat16(0.f);
-  }
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int k = blockIdx.y * 8 + q;
-    if (k < p.r) w2c[(size_t)k * p.Vh + j] = x[q];
   }
 }
 
@@ -564,41 +690,41 @@ __global__ void __launch_bounds__(256) loss_w1_rows(const LossPlan p) {
 cudaError_t launch_loss_plan(const LossPlan& p) {
   const bool f32 = p.dtype == 0;
   cudaError_t e = cudaSuccess;
-  if (f32)
-    for (int z = 0; z < p.n_zero && e == cudaSuccess; ++z)
-      e = cudaMemsetAsync(p.zero[z].p, 0, p.zero[z].bytes, p.stream);
   if (p.vlist) {
     int chunks = 0;
-    if (e == cudaSuccess)
-      e = cudaMemsetAsync(p.vinv, 0xFF, sizeof(int32_t) * (size_t)p.Vh, p.stream);
+    e = cudaMemsetAsync(p.vinv, 0xFF, sizeof(int32_t) * (size_t)p.Vh, p.stream);
     if (e == cudaSuccess) e = launch_emit_rows(p.bias, p.Vh, p.vchunk, p.vlist, &chunks, p.stream);
     if (e == cudaSuccess)
       e = launch_after(loss_vocab, std::min(256, (p.Vh + 255) / 256), 256, 0, p.stream, p, chunks);
-    if (e == cudaSuccess && p.wc)
-      e = launch_after(loss_gather_head, std::min(1216, (p.Vh + 7) / 8), 256, 0, p.stream, p);
-    if (e == cudaSuccess && p.wc && p.r > 0)
-      e = launch_after(loss_gather_w2, dim3((p.Vh + 255) / 256, (p.r + 7) / 8), 256, 0, p.stream,
-                       p);
+    if (e == cudaSuccess && p.wc) {
+      const int rows = std::min(1216, (p.Vh + 7) / 8);
+      const int cols = (p.Vh + 255) / 256 * ((p.r + 7) / 8);
+      e = launch_after(loss_gather_head, rows + cols, 256, 0, p.stream, p, rows);
+    }
   }
-  if (e == cudaSuccess)
-    e = launch_after(loss_tokens, 1, std::min(kPlanThreads, (p.T + 31) / 32 * 32), 0, p.stream, p);
+  if (e != cudaSuccess) return e;
+  if (p.T <= kPlanFew && !p.d2t)
+    return launch_after(f32 ? loss_plan_few<float> : loss_plan_few<__nv_bfloat16>, p.Tp, 256, 0,
+                        p.stream, p);
+  e = launch_after(loss_tokens, 1, std::min(kPlanThreads, (p.T + 31) / 32 * 32), 0, p.stream, p);
   if (e == cudaSuccess)
     e = launch_after(f32 ? loss_gather<float> : loss_gather<__nv_bfloat16>, p.Tp, 256, 0, p.stream,
                      p);
   return e;
 }
 
-cudaError_t launch_loss_rows(const LossPlan& p) {
-  return launch_after(loss_rows, p.T, kRowsThreads, 0, p.stream, p);
+cudaError_t launch_loss_rows(const LossPlan& p, bool dz) {
+  if (!dz) return launch_after(loss_rows<0>, p.T, kRowsThreads, 0, p.stream, p);
+  // CTAs of a row: enough to fill the GPU, each with some sweeps to do
+  const int most = p.dtype == 0 ? (p.Vh + 255) / 256 : (p.Vh + 4095) / 4096;
+  const unsigned parts = (unsigned)std::max(1, std::min({16, most, (2 * 1216 + p.T - 1) / p.T}));
+  return launch_after(p.dtype == 0 ? loss_rows<2> : loss_rows<1>, dim3((unsigned)p.T, parts),
+                      kRowsThreads, 0, p.stream, p);
 }
 
-cudaError_t launch_loss_dz(const LossPlan& p, int v0, int v1) {
-  if (p.dtype == 0) {
-    const unsigned blocks = (unsigned)std::min(64, (v1 - v0 + 255) / 256);
-    return launch_after(loss_dz_f32, dim3((unsigned)p.T, blocks), 256, 0, p.stream, p, v0, v1);
-  }
-  const unsigned blocks = (unsigned)std::min(16, (p.Vh + 2047) / 2048);
-  return launch_after(loss_dz_bf16, dim3((unsigned)p.T, blocks), 256, 0, p.stream, p);
+cudaError_t launch_loss_dz_f32(const LossPlan& p, int v0, int v1) {
+  const unsigned blocks = (unsigned)std::min(64, (v1 - v0 + 255) / 256);
+  return launch_after(loss_dz_f32, dim3((unsigned)p.T, blocks), 256, 0, p.stream, p, v0, v1);
 }
 
 cudaError_t launch_loss_dx(const LossPlan& p) {

@@ -153,16 +153,15 @@ loss_logits(const LossPlan p, int v0, int v1, bool stats, bool store) {
   }
 }
 
-// dX of vocabulary columns [v0, v1): split blockIdx.z of their range.
+// dX of vocabulary columns [v0, v1): tile (bx, by), split bz of their range.
 template <int R>
-__global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1, bool first) {
-  pdl_wait();
-  pdl_signal();
+__device__ __forceinline__ void dx_tile(const LossPlan& p, int v0, int v1, bool first, int bx,
+                                        int by, int bz) {
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
-  const int m0 = blockIdx.y * 16 * R, c0 = blockIdx.x * kTile;
+  const int m0 = by * 16 * R, c0 = bx * kTile;
   if (m0 >= n_tok) return;
-  const int share = ((v1 - v0 + (int)gridDim.z - 1) / (int)gridDim.z + kShare - 1) / kShare * kShare;
-  const int ja = v0 + (int)blockIdx.z * share, jb = min(n_voc, ja + share);
+  const int share = ((v1 - v0 + p.splits - 1) / p.splits + kShare - 1) / kShare * kShare;
+  const int ja = v0 + bz * share, jb = min(n_voc, ja + share);
   const float* q = (const float*)p.q;
   const float* w = (const float*)p.lm_head;
   const float* w2 = (const float*)p.w2;
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1,
                          head ? (size_t)row * p.H + c : (size_t)c * p.Vh + row);
         });
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float* dx = p.dxp + (size_t)blockIdx.z * p.Tp * p.Kx;
+  float* dx = p.dxp + (size_t)bz * p.Tp * p.Kx;
 #pragma unroll
   for (int a = 0; a < R; ++a)
 #pragma unroll
@@ -195,12 +194,10 @@ __global__ void __launch_bounds__(256) loss_dx(const LossPlan p, int v0, int v1,
     }
 }
 
-// dW of vocabulary columns [v0, v1).
-__global__ void __launch_bounds__(256) loss_dw(const LossPlan p, int v0, int v1) {
-  pdl_wait();
-  pdl_signal();
+// dW of vocabulary columns [v0, v1): tile (bx, by).
+__device__ __forceinline__ void dw_tile(const LossPlan& p, int v0, int v1, int bx, int by) {
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = min(v1, (int)p.ctrl[kLossVoc]);
-  const int j0 = v0 + blockIdx.y * kTile, c0 = blockIdx.x * kTile;
+  const int j0 = v0 + by * kTile, c0 = bx * kTile;
   const bool head = c0 < p.Hp;
   if (j0 >= n_voc || (head ? !p.d_lm_head : !p.d_w2)) return;
   const float* q = (const float*)p.q;
@@ -232,6 +229,23 @@ __global__ void __launch_bounds__(256) loss_dw(const LossPlan p, int v0, int v1)
     }
 }
 
+// Both: the first `n_dx` CTAs make dX, the others dW.
+template <int R>
+__global__ void __launch_bounds__(256)
+loss_grads(const LossPlan p, int v0, int v1, bool first, int n_dx) {
+  pdl_wait();
+  pdl_signal();
+  const int across = p.Kx / kTile;
+  int b = blockIdx.x;
+  if (b < n_dx) {
+    const int rows = (p.T + 16 * R - 1) / (16 * R);
+    dx_tile<R>(p, v0, v1, first, b % across, b / across % rows, b / across / rows);
+  } else {
+    b -= n_dx;
+    dw_tile(p, v0, v1, b % across, b / across);
+  }
+}
+
 }  // namespace
 
 // Splits of the vocabulary for dX: enough CTAs to fill the GPU when rows are few.
@@ -249,17 +263,14 @@ cudaError_t launch_loss_logits_simt(const LossPlan& p, int v0, int v1, bool stat
 }
 
 cudaError_t launch_loss_grads_simt(const LossPlan& p, int v0, int v1, bool first) {
-  cudaError_t e = cudaSuccess;
-  if (p.dxp) {
-    const bool few = p.T <= 16;
-    const dim3 grid(p.Kx / kTile, few ? 1 : (p.T + kTile - 1) / kTile, p.splits);
-    e = launch_after(few ? loss_dx<1> : loss_dx<4>, grid, 256, 0, p.stream, p, v0, v1, first);
-  }
-  if (e == cudaSuccess && (p.d_lm_head || p.d_w2)) {
-    const dim3 grid(p.Kx / kTile, (v1 - v0 + kTile - 1) / kTile);
-    e = launch_after(loss_dw, grid, 256, 0, p.stream, p, v0, v1);
-  }
-  return e;
+  const bool few = p.T <= 16;
+  const int across = p.Kx / kTile, rows = few ? 1 : (p.T + kTile - 1) / kTile;
+  const long long n_dx = p.dxp ? (long long)across * rows * p.splits : 0;
+  const long long n_dw =
+      p.d_lm_head || p.d_w2 ? (long long)across * ((v1 - v0 + kTile - 1) / kTile) : 0;
+  if (n_dx + n_dw > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  return launch_after(few ? loss_grads<1> : loss_grads<4>, (unsigned)(n_dx + n_dw), 256, 0,
+                      p.stream, p, v0, v1, first, (int)n_dx);
 }
 
 }  // namespace dspark

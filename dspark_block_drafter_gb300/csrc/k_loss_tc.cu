@@ -608,7 +608,8 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             ptx::st_global_v8(qrow + c, o);
           }
           if ((g.want & kWantGrad) && here)       // (after this thread's vector store)
-            reinterpret_cast<__nv_bfloat16*>(qrow)[lab - v0] = loss_label_entry_bf16(p, m);
+            reinterpret_cast<__nv_bfloat16*>(qrow)[lab - v0] =
+                loss_label_entry_bf16(p, m, loss_label_entry(wt, p.loss[p.tok[m]]));
         }
       } else {
         if (!acc_wait()) break;

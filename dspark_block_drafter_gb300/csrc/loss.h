@@ -78,15 +78,14 @@ struct LossPlan {
   cudaStream_t stream;
 };
 
-// The label's entry of row i of q: w (p - 1) = w expm1(-loss), which loses no digits where p
-// is nearly 1.
-__device__ __forceinline__ float loss_label_entry(const LossPlan& p, int i) {
-  return p.wrow[i] * expm1f(-p.loss[p.tok[i]]);
+// The label's entry of a row of q: w (p - 1) = w expm1(-loss), which loses no digits where p is
+// nearly 1.
+__device__ __forceinline__ float loss_label_entry(float w, float loss) {
+  return w * expm1f(-loss);
 }
-// The same rounded to bf16; what the rounding lost is kept for the gradient of X (this entry
-// makes up most of it).
-__device__ __forceinline__ __nv_bfloat16 loss_label_entry_bf16(const LossPlan& p, int i) {
-  const float x = loss_label_entry(p, i);
+// That of row i rounded to bf16; what the rounding lost is kept for the gradient of X (this
+// entry makes up most of it).
+__device__ __forceinline__ __nv_bfloat16 loss_label_entry_bf16(const LossPlan& p, int i, float x) {
   const __nv_bfloat16 b = __float2bfloat16(x);
   p.qres[i] = x - __bfloat162float(b);
   return b;
@@ -125,12 +124,13 @@ __device__ __forceinline__ float loss_gap_exp(uint32_t gap, float log2_scale) {
 
 // k_loss_rows.cu: everything but the products
 cudaError_t launch_loss_plan(const LossPlan& p);         // compaction, X, zeroed outputs
-cudaError_t launch_loss_rows(const LossPlan& p);         // lse, losses, total
-cudaError_t launch_loss_dz(const LossPlan& p, int v0, int v1);   // q from what is stored
+cudaError_t launch_loss_rows(const LossPlan& p, bool dz);   // lse, losses, total, and with `dz`
+                                                          // q of the one piece
+cudaError_t launch_loss_dz_f32(const LossPlan& p, int v0, int v1);   // q from stored logits
 cudaError_t launch_loss_dx(const LossPlan& p);           // d_hidden and d_w1 from dxp
 
 // the products of columns [v0, v1) of the compact vocabulary.  Logits: with `stats` their
-// statistics, and with `store` what launch_loss_dz needs; without `stats` q's input again
+// statistics, and with `store` what q is made from; without `stats` q's input again
 // (fp32) or q itself (bf16).  dX: `first` overwrites dxp, otherwise it is added to.
 // k_loss_simt.cu (fp32, on the CUDA cores)
 int loss_simt_splits(int T, int Kx, int cols);
