@@ -274,21 +274,30 @@ __device__ __forceinline__ void zero_outputs(const LossPlan& p) {
   }
 }
 
-// Row t's part of X as compact row i, or its zero outputs when it carries no loss (i < 0).
+// Row t's part of X as compact row i (and with `low` once more), or its zero outputs when it
+// carries no loss (i < 0).
 template <typename E>
-__device__ __forceinline__ void gather_row(const LossPlan& p, int t, int i, int prev) {
+__device__ __forceinline__ void gather_row(const LossPlan& p, int t, int i, int prev, bool low) {
   if (i < 0) {
     if (threadIdx.x == 0) p.loss[t] = 0.f;
     if (p.d_hidden) zero_row((E*)p.d_hidden + (size_t)t * p.H, p.H);
     return;
   }
-  E* xi = (E*)p.x + (size_t)i * p.Kx;
-  copy_row(xi, (const E*)p.hidden + (size_t)t * p.H, p.H);
-  if (p.H < p.Hp) zero_row(xi + p.H, p.Hp - p.H);
-  if (p.rp) {
+  for (int row = i; row <= i + (low ? kLossLow : 0); row += kLossLow) {
+    E* xi = (E*)p.x + (size_t)row * p.Kx;
+    copy_row(xi, (const E*)p.hidden + (size_t)t * p.H, p.H);
+    if (p.H < p.Hp) zero_row(xi + p.H, p.Hp - p.H);
+    if (p.rp == 0) continue;
     copy_row(xi + p.Hp, (const E*)p.w1 + (size_t)prev * p.r, p.r);
     if (p.r < p.rp) zero_row(xi + p.Hp + p.r, p.rp - p.r);
   }
+}
+
+// Row t of X after the compact rows: zeros, unless a low row's copy goes there.
+template <typename E>
+__device__ __forceinline__ void pad_row(const LossPlan& p, int t, int n_tok) {
+  if (t < n_tok || (loss_low(p, n_tok) && t >= kLossLow && t < kLossLow + n_tok)) return;
+  zero_row((E*)p.x + (size_t)t * p.Kx, p.Kx);
 }
 
 // CTA t: row t's part of X, and X's padding row t.
@@ -297,11 +306,11 @@ __global__ void __launch_bounds__(256) loss_gather(const LossPlan p) {
   pdl_wait();
   pdl_signal();
   zero_outputs<E>(p);
-  const int t = blockIdx.x;
-  if (t >= (int)p.ctrl[kLossTok]) zero_row((E*)p.x + (size_t)t * p.Kx, p.Kx);
+  const int t = blockIdx.x, n_tok = (int)p.ctrl[kLossTok];
+  pad_row<E>(p, t, n_tok);
   if (t >= p.T) return;
   const int i = p.pos[t];
-  gather_row<E>(p, t, i, i >= 0 ? p.prevc[i] : 0);
+  gather_row<E>(p, t, i, i >= 0 ? p.prevc[i] : 0, loss_low(p, n_tok));
 }
 
 // loss_tokens and loss_gather in one launch, for few rows: every CTA looks at every row for
@@ -383,7 +392,7 @@ __global__ void __launch_bounds__(256) loss_plan_few(const LossPlan p) {
       if (p.n_rows) *p.n_rows = all;
     }
   }
-  if (me >= all) zero_row((E*)p.x + (size_t)me * p.Kx, p.Kx);
+  pad_row<E>(p, me, all);
   if (me >= p.T) return;
   if (label >= 0 && tid == 0) {
     p.tok[before] = me;
@@ -391,7 +400,7 @@ __global__ void __launch_bounds__(256) loss_plan_few(const LossPlan p) {
     p.prevc[before] = s_prev;
     p.wrow[before] = p.weights ? p.weights[me] : 1.f;
   }
-  gather_row<E>(p, me, label >= 0 ? before : -1, label >= 0 ? s_prev : 0);
+  gather_row<E>(p, me, label >= 0 ? before : -1, label >= 0 ? s_prev : 0, loss_low(p, all));
 }
 
 // Row i's log-sum-exp and loss, from its statistics over the vocabulary tiles (thread 0 has
@@ -449,8 +458,8 @@ __device__ __forceinline__ void row_dz_f32(const LossPlan& p, int i, int v0, int
 // The same in bf16 from the stored distances (one piece: v0 = 0), over whole 256-column
 // tiles: columns past the vocabulary become 0.  Two vectors of eight columns a thread and
 // sweep; the thread that has the label's column writes it again.
-__device__ __forceinline__ void row_dz_bf16(const LossPlan& p, int i, int n_voc, float lse,
-                                            float loss, int part, int parts) {
+__device__ __forceinline__ void row_dz_bf16(const LossPlan& p, int i, int n_voc, bool low,
+                                            float lse, float loss, int part, int parts) {
   uint4* q = (uint4*)((uint16_t*)p.q + (size_t)i * p.ldq);
   const float2* st = p.stat + (size_t)i * p.n_stat;
   const float w = p.wrow[i], log2_w = log2f(w);              // (w = 0: -inf, e = 0)
@@ -472,17 +481,23 @@ __device__ __forceinline__ void row_dz_bf16(const LossPlan& p, int i, int n_voc,
       const int c = c0 + h * step;
       if (c >= end) break;
       const uint32_t g[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
-      uint32_t o[4];
+      uint32_t o[4], r[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 b =
-            __floats2bfloat162_rn(loss_gap_exp(g[j] & 0xFFFFu, s[h]), loss_gap_exp(g[j] >> 16, s[h]));
+        const float e0 = loss_gap_exp(g[j] & 0xFFFFu, s[h]), e1 = loss_gap_exp(g[j] >> 16, s[h]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
         o[j] = *reinterpret_cast<const uint32_t*>(&b);
+        if (low) {
+          const __nv_bfloat162 l =
+              __floats2bfloat162_rn(e0 - __low2float(b), e1 - __high2float(b));
+          r[j] = *reinterpret_cast<const uint32_t*>(&l);
+        }
       }
       q[c] = make_uint4(o[0], o[1], o[2], o[3]);
+      if (low) q[kLossLow * p.ldq / 8 + c] = make_uint4(r[0], r[1], r[2], r[3]);
       if (lab / 8 == c)
-        reinterpret_cast<__nv_bfloat16*>(q)[lab] =
-            loss_label_entry_bf16(p, i, loss_label_entry(w, loss));
+        loss_put_label(p, i, low, reinterpret_cast<__nv_bfloat16*>(q) + lab,
+                       loss_label_entry(w, loss));
     }
   }
 }
@@ -529,7 +544,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows(const LossPlan p) {
   }
   if (i >= n_tok) return;
   const float2 r = s_row;
-  if (DZ == 1) row_dz_bf16(p, i, n_voc, r.x, r.y, blockIdx.y, gridDim.y);
+  if (DZ == 1) row_dz_bf16(p, i, n_voc, loss_low(p, n_tok), r.x, r.y, blockIdx.y, gridDim.y);
   if (DZ == 2) row_dz_f32(p, i, 0, n_voc, r.x, r.y, blockIdx.y, gridDim.y);
 }
 
@@ -600,6 +615,7 @@ __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
   const int splits = (int)p.ctrl[kLossSplits];
   float4* x = (float4*)(p.dxp + (size_t)i * p.Kx);
   const float lost = p.qres ? p.qres[i] : 0.f;
+  const bool low = loss_low(p, (int)p.ctrl[kLossTok]);
   const size_t row = (size_t)loss_head_row(p, p.lab[i]);
   E* dh = p.d_hidden ? (E*)p.d_hidden + (size_t)p.tok[i] * p.H : nullptr;
   // four columns a thread (Hp and Kx are multiples of 64)
@@ -616,6 +632,11 @@ __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
         a[0] += y[s].x; a[1] += y[s].y; a[2] += y[s].z; a[3] += y[s].w;
       }
     }
+    if (low)
+      for (int s = 0; s < splits; ++s) {
+        const float4 y = x[(size_t)kLossLow * p.Kx / 4 + s * step + c4];
+        a[0] += y.x; a[1] += y.y; a[2] += y.z; a[3] += y.w;
+      }
     const int c = 4 * c4;
     const bool head = c < p.Hp;
     if (p.qres) {                             // (bf16: H is a multiple of 8)

@@ -121,7 +121,8 @@ struct Sequence {
     mt = (n_tok + kRows - 1) / kRows;
     vt = (cols + (MODE == kLogits ? kTileN : kRows) - 1) / (MODE == kLogits ? kTileN : kRows);
     nkb = (cols + kBlockK - 1) / kBlockK;
-    tkb = (n_tok + kBlockK - 1) / kBlockK;
+    tkb = loss_low(g.p, n_tok) && n_tok > 0 ? 2 * kLossLow / kBlockK
+                                            : (n_tok + kBlockK - 1) / kBlockK;
     n_dx = mt * cx.all() * splits;
     n_dw = vt * cw.all();
     units = MODE == kLogits ? mt * vt : MODE == kDx ? n_dx : n_dw;
@@ -534,6 +535,9 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       const int m = t.m + (int)rank * kTileM + quad * 32 + lane;   // this thread's row of M
       if (MODE == kLogits) {
         const bool live = m < n_tok;
+        // (the low rows of q: written with their rows' gradients, before that zeros)
+        const bool low = (g.want & kWantGrad) && loss_low(p, n_tok);
+        const bool mine = !low || live || (m < kLossLow || m >= kLossLow + n_tok);
         const int lab = live ? p.lab[m] : -1;
         const int v0 = g.v0 + t.c0 + half * 128;             // compact head row of column 0
         const int n_in = n_voc - v0;                          // columns that exist
@@ -593,23 +597,30 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
           uint16_t* qrow = (uint16_t*)p.q + (size_t)m * p.ldq + (v0 - g.v0);
 #pragma unroll
           for (int c = 0; c < 128; c += 16) {
-            uint32_t o[8];
+            uint32_t o[8], l[8];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
               const float d0 = z[c + j] - ref, d1 = z[c + j + 1] - ref;
               if (g.want & kWantGrad) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(wt * loss_exp(d0), wt * loss_exp(d1));
+                const float e0 = wt * loss_exp(d0), e1 = wt * loss_exp(d1);
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
                 o[j / 2] = *reinterpret_cast<const uint32_t*>(&b2);
+                if (CG == 1) {
+                  const __nv_bfloat162 l2 =
+                      __floats2bfloat162_rn(e0 - __low2float(b2), e1 - __high2float(b2));
+                  l[j / 2] = *reinterpret_cast<const uint32_t*>(&l2);
+                }
               } else {
                 o[j / 2] = __byte_perm(loss_gap(-d0), loss_gap(-d1), 0x5410);
               }
               if (!live) o[j / 2] = 0u;
             }
-            ptx::st_global_v8(qrow + c, o);
+            if (CG == 2 || mine) ptx::st_global_v8(qrow + c, o);
+            if (CG == 1 && low && live) ptx::st_global_v8(qrow + kLossLow * p.ldq + c, l);
           }
           if ((g.want & kWantGrad) && here)       // (after this thread's vector store)
-            reinterpret_cast<__nv_bfloat16*>(qrow)[lab - v0] =
-                loss_label_entry_bf16(p, m, loss_label_entry(wt, p.loss[p.tok[m]]));
+            loss_put_label(p, m, CG == 1 && low, reinterpret_cast<__nv_bfloat16*>(qrow) + (lab - v0),
+                           loss_label_entry(wt, p.loss[p.tok[m]]));
         }
       } else {
         if (!acc_wait()) break;
@@ -625,7 +636,9 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             uint32_t r[32];
             ptx::tmem_ld_32x32b_x32(at + c, r);
             ptx::tmem_ld_wait();
-            if (m >= n_tok) continue;
+            if (m >= n_tok &&
+                !(CG == 1 && loss_low(p, n_tok) && m >= kLossLow && m < kLossLow + n_tok))
+              continue;
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
               float x[8];

@@ -78,17 +78,29 @@ struct LossPlan {
   cudaStream_t stream;
 };
 
+constexpr int kLossLow = 64;        // see loss_low
+
 // The label's entry of a row of q: w (p - 1) = w expm1(-loss), which loses no digits where p is
 // nearly 1.
 __device__ __forceinline__ float loss_label_entry(float w, float loss) {
   return w * expm1f(-loss);
 }
-// That of row i rounded to bf16; what the rounding lost is kept for the gradient of X (this
-// entry makes up most of it).
-__device__ __forceinline__ __nv_bfloat16 loss_label_entry_bf16(const LossPlan& p, int i, float x) {
+// That of row i rounded to bf16 at q; what the rounding lost goes to the low row, or is kept for
+// the gradient of X (this entry makes up most of it).
+__device__ __forceinline__ void loss_put_label(const LossPlan& p, int i, bool low, __nv_bfloat16* q,
+                                               float x) {
   const __nv_bfloat16 b = __float2bfloat16(x);
-  p.qres[i] = x - __bfloat162float(b);
-  return b;
+  const float lost = x - __bfloat162float(b);
+  *q = b;
+  if (low) q[kLossLow * p.ldq] = __float2bfloat16(lost);
+  p.qres[i] = low ? 0.f : lost;
+}
+
+// bf16, up to kLossLow compact rows: row kLossLow + i of q holds what rounding row i of it lost
+// (and row kLossLow + i of X is row i again), so that the gradient products see q with 16 bits.
+// Few rows do not average their roundings out, and within one 128-row tile this costs nothing.
+__device__ __forceinline__ bool loss_low(const LossPlan& p, int n_tok) {
+  return p.dtype == 1 && p.T <= 2 * kLossLow && n_tok <= kLossLow;
 }
 
 // compact -> head row, for kernels that read the head's own arrays

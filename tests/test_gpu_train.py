@@ -102,6 +102,18 @@ def check_loss(out, o, dtype):
                   + 1e-30, name)
 
 
+def check_few_rows(out, o):
+    """bf16, up to 64 rows: the products see the gradient of the logits with 16 bits, so that
+    only the kept numerators' 2^-10.8 stays besides the output's own rounding."""
+    mag = o["mag"]
+    eps = 2.0 ** -10.7 + 2 * (mag["z"] * 2.0 ** -21 + 2.0 ** -20) + 2.0 ** -20
+    for name in ("d_hidden", "d_lm_head", "d_markov_w1", "d_markov_w2"):
+        g = getattr(out, name)
+        if g is not None:
+            _near(g, o[name], 2.0 ** -8 * np.abs(o[name]) + eps * mag[name] * (1 + 2.0 ** -8)
+                  + 1e-30, name)
+
+
 LOSS_CASES = [
     # one row, one tile, and past tile edges in every dimension
     dict(T=1, H=64, V=128, r=8), dict(T=1, H=8, V=8, r=1), dict(T=2, H=72, V=256, r=0),
@@ -136,6 +148,14 @@ LOSS_CASES = [
 def test_loss(case, dtype):
     out, o, _ = run_loss(dtype=dtype, seed=len(str(case)), **case)
     check_loss(out, o, dtype)
+
+
+@pytest.mark.parametrize("pieces", [1, 3])
+@pytest.mark.parametrize("T,ignored", [(1, 0), (5, 0), (64, 0), (90, 26), (128, 64)])
+def test_loss_of_few_rows_rounds_only_its_outputs(T, ignored, pieces):
+    out, o, _ = run_loss(T, 192, 1544, 24, "bf16", ignored=ignored, pieces=pieces, weighted=True,
+                         prev_range=9)
+    check_few_rows(out, o)
 
 
 @pytest.mark.parametrize("case", [
