@@ -209,6 +209,8 @@ static size_t plan_norm(const dspark_norm_config* c, char* ws, NormArgs* a) {
   return off;
 }
 
+static bool norm_f32(const dspark_norm_config* c) { return c->dtype == DSPARK_F32; }
+
 static void fill_norm(const dspark_norm_config* c, NormArgs* a) {
   a->T = c->T; a->H = c->H; a->dtype = c->dtype; a->span = c->gate_span;
   a->eps = c->eps; a->scale = c->residual_scale; a->offset = c->weight_offset;
@@ -289,7 +291,7 @@ dspark_status dspark_block_norm(const dspark_norm_config* cfg, const void* x, co
   a.x_out = x_out;
   a.h = h;
   a.stream = (cudaStream_t)stream;
-  const cudaError_t e = launch_block_norm(a);
+  const cudaError_t e = norm_f32(cfg) ? launch_norm_f32(a, false) : launch_norm_bf16(a, false);
   if (e != cudaSuccess) return cuda_fail(e, "block norm kernel");
   return DSPARK_OK;
 }
@@ -324,7 +326,7 @@ dspark_status dspark_block_norm_backward(const dspark_norm_config* cfg, const vo
   a.d_h = d_h; a.d_x_out = d_x_out; a.d_x = d_x; a.d_y = d_y; a.d_gate = d_gate;
   a.d_w_post = d_w_post; a.d_w_pre = d_w_pre;
   a.stream = (cudaStream_t)stream;
-  const cudaError_t e = launch_block_norm_backward(a);
+  const cudaError_t e = norm_f32(cfg) ? launch_norm_f32(a, true) : launch_norm_bf16(a, true);
   if (e != cudaSuccess) return cuda_fail(e, "block norm gradient kernels");
   return DSPARK_OK;
 }

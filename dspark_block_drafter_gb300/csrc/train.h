@@ -26,8 +26,8 @@ constexpr int kNormMaxH = 8192;      // 16 elements for each of 512 threads
 
 int norm_max_ctas(int H);              // CTAs of the gradient kernel, at most
 int norm_span_parts(int T, int span);  // parts of the rows that share a gate row
-cudaError_t launch_block_norm(const NormArgs& a);
-cudaError_t launch_block_norm_backward(const NormArgs& a);
+cudaError_t launch_norm_f32(const NormArgs& a, bool grad);    // grad: the backward pass
+cudaError_t launch_norm_bf16(const NormArgs& a, bool grad);
 
 constexpr int kClipMaxCtas = 1216;   // CTAs of one pass over the gradients, at most
 constexpr int kClipList = 96;        // gradients of one launch

@@ -330,6 +330,29 @@ def test_block_norm_unaligned_and_without_upstream(dtype):
     run_norm(12, 512, dtype, up=False)
 
 
+# rows made of vectors of 16, 8, 4 and 2 bytes, more of them than run at once
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H,span", [(1500, 520, 5), (1500, 516, 1), (1500, 514, 0),
+                                      (1500, 513, 5), (700, 2100, 7), (700, 2101, 1),
+                                      (350, 4098, 3), (350, 5001, 0)])
+def test_block_norm_rows_of_every_vector(T, H, span, dtype):
+    tio, cfg, x, y, w_pre, h, xo, kw = run_norm(T, H, dtype, span=span)
+    # in place, next to values that must neither count nor change
+    edge = 3
+    around = [torch.full((T * H + 2 * edge,), float("nan"), dtype=x.dtype, device="cuda")
+              for _ in range(2)]
+    inner = [b[edge:-edge].view(T, H) for b in around]
+    for b, v in zip(inner, (x, y)):
+        b.copy_(v)
+    tio.block_norm(cfg, inner[0], inner[1], w_pre, inner[1], x_out=inner[0], **kw)
+    u = 2 * OUT[dtype] + 2.0 ** -17         # (other vectors, other orders of the sums)
+    _near(inner[0], _np(xo), u * (np.abs(_np(x)) + np.abs(_np(xo))), "x_out in place")
+    top = np.abs(_np(h)).max(1, keepdims=True)
+    _near(inner[1], _np(h), u * (np.abs(_np(h)) + top), "h in place")
+    for b in around:
+        assert torch.isnan(b[:edge]).all() and torch.isnan(b[-edge:]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_block_norm_in_place_and_zero_rows(dtype):
     tio, cfg, x, y, w_pre, h, xo, kw = run_norm(12, 768, dtype)
