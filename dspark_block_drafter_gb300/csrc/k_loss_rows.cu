@@ -403,8 +403,11 @@ __global__ void __launch_bounds__(256) loss_plan_few(const LossPlan p) {
   gather_row<E>(p, me, label >= 0 ? before : -1, label >= 0 ? s_prev : 0, loss_low(p, all));
 }
 
-// Row i's log-sum-exp and loss, from its statistics over the vocabulary tiles (thread 0 has
-// them; the CTA takes part).
+// Row i's log-sum-exp and loss, from its label's logit and the statistics of the others over
+// the vocabulary tiles (thread 0 has them; the CTA takes part).  Where the label's logit z is
+// the largest, the loss is log1p(sum of the others' e^(z_j - z)): a small loss keeps its digits
+// (as the difference of log-sum-exp and z, one of 1e-5 was off by 0.6%, and so was the label's
+// entry of the gradient).
 constexpr int kRowsThreads = 256;
 __device__ __forceinline__ float2 join_row(const LossPlan& p, int i, int n_voc, float2* s_w) {
   const int tid = threadIdx.x, n = (n_voc + p.stat_cols - 1) / p.stat_cols;
@@ -440,8 +443,14 @@ __device__ __forceinline__ float2 join_row(const LossPlan& p, int i, int n_voc, 
   Sum2 v;
   v.s = s * __expf(m - ref);
   __syncthreads();
-  const float l = logf(block_sum(v, s_w).value());
-  return make_float2(mx + l, (mx - p.zlab[i]) + l);
+  const float sum = block_sum(v, s_w).value(), zl = p.zlab[i];
+  if (zl >= mx) {
+    // (z - z: an infinite z is no loss of 0)
+    const float l = log1pf(mx > -INFINITY ? sum * expf(mx - zl) : 0.f) + (zl - zl);
+    return make_float2(zl + l, l);
+  }
+  const float l = logf(sum + expf(zl - ref));
+  return make_float2(mx + l, (mx - zl) + l);
 }
 
 // q = w (softmax - onehot) of row i in place, fp32 from stored logits: columns [v0, v1), every

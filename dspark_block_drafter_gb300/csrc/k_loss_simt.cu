@@ -103,18 +103,21 @@ __device__ __forceinline__ void finish_logits(const LossPlan& p, int i, int n_to
                                               int n_voc, int tx, float (&acc)[4], bool stats,
                                               bool store) {
   float m = -INFINITY;
+  const int lab = stats && i < n_tok ? p.lab[i] : -1;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const int j = j0 + 4 * tx + b;
     float z = acc[b];
     if (j < n_voc && p.vlist) z += p.biasc[j];
-    acc[b] = z;
-    if (j < n_voc) {
-      // (a NaN logit stays NaN in the maximum)
-      m = z != z || m != m ? m + z : fmaxf(m, z);
-      if (store && i < n_tok) ((float*)p.q)[(size_t)i * p.ldq + (j - v0)] = z;
-      if (stats && i < n_tok && j == p.lab[i]) p.zlab[i] = z;
+    if (j < n_voc && store && i < n_tok) ((float*)p.q)[(size_t)i * p.ldq + (j - v0)] = z;
+    if (j == lab) {                           // (kept out of the statistics)
+      p.zlab[i] = z;
+      z = -INFINITY;
     }
+    if (j >= n_voc) z = -INFINITY;
+    acc[b] = z;
+    // (a NaN logit stays NaN in the maximum)
+    m = z != z || m != m ? m + z : fmaxf(m, z);
   }
   if (!stats) return;
 #pragma unroll
@@ -125,7 +128,7 @@ __device__ __forceinline__ void finish_logits(const LossPlan& p, int i, int n_to
   float s = 0.f;
 #pragma unroll
   for (int b = 0; b < 4; ++b)
-    if (j0 + 4 * tx + b < n_voc && m > -INFINITY) s += expf(acc[b] - m);
+    if (m > -INFINITY) s += expf(acc[b] - m);
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   if (m != m) s = m;                          // (NaN for the whole row)

@@ -573,7 +573,10 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
           float zl = 0.f;                         // the label's logit
 #pragma unroll
           for (int j = 0; j < 128; ++j)
-            if (lab == v0 + j) zl = z[j];
+            if (lab == v0 + j) {                  // (kept out of the statistics)
+              zl = z[j];
+              z[j] = -INFINITY;
+            }
           if (here) p.zlab[m] = zl;
         }
         float ref = 0.f, wt = 0.f;

@@ -158,6 +158,31 @@ def test_loss_of_few_rows_rounds_only_its_outputs(T, ignored, pieces):
     check_few_rows(out, o)
 
 
+@pytest.mark.parametrize("pieces", [1, 3])
+@pytest.mark.parametrize("T,H,V", [(1, 192, 1504), (7, 192, 1504), (100, 192, 1504),
+                                   (300, 128, 4096)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_small_losses_keep_their_digits(dtype, T, H, V, pieces):
+    """Rows whose label has nearly all the probability: losses down to 1e-9, and gradients as
+    small, to the same relative precision as large ones."""
+    from dspark_block_drafter_gb300 import torch_io as tio
+    out, _, args = run_loss(T, H, V, 0, dtype, pieces=pieces)
+    cfg, head, hidden, _, labels, _, ws, _ = args
+    W, lab = _np(head.lm_head), labels.cpu().numpy()
+    much = np.linspace(26, 13, T)[:, None]
+    hidden.copy_(torch.from_numpy((W[lab] * much).astype(np.float32)))
+    tio.head_loss(*args)
+    torch.cuda.synchronize()
+    o = to.head_loss(_np(hidden), W, lab, V=V)
+    assert o["loss"].min() < 1e-4
+    dz = o["mag"]["z"] * 2.0 ** -21 + 2.0 ** -20
+    _near(out.loss, o["loss"], o["loss"] * (2 * dz + 2.0 ** -18), "loss")
+    _near(float(out.total), o["total"], o["total"] * (2 * dz + 2.0 ** -18), "total")
+    check_loss(out, o, dtype)
+    if dtype == "bf16" and T <= 64:
+        check_few_rows(out, o)
+
+
 @pytest.mark.parametrize("case", [
     dict(T=3, H=7, V=13, r=3), dict(T=65, H=33, V=131, r=5), dict(T=97, H=129, V=1001, r=17),
     dict(T=31, H=65, V=777, r=9, form="bias", n_emit=101),
