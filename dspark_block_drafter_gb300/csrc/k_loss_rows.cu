@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(256) loss_gather_head(const LossPlan p, int ro
   }
 }
 
-// CTA i: row i of the gradient of X, summed over the splits of the vocabulary (and, in
+// CTAs (i, 0 .. ): row i of the gradient of X, summed over the splits of the vocabulary (and, in
 // bf16, with what q lost at the label), times the scale: d_hidden's row, and the gradient of
 // markov_w1's row prev (left in split 0).
 template <typename E>
@@ -629,23 +629,24 @@ __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
   E* dh = p.d_hidden ? (E*)p.d_hidden + (size_t)p.tok[i] * p.H : nullptr;
   // four columns a thread (Hp and Kx are multiples of 64)
   const int from = p.d_hidden ? 0 : p.Hp / 4, to = p.d_w1 ? p.Kx / 4 : p.Hp / 4;
-  for (int c4 = from + threadIdx.x; c4 < to; c4 += blockDim.x) {
+  for (int c4 = from + blockIdx.y * blockDim.x + threadIdx.x; c4 < to;
+       c4 += gridDim.y * blockDim.x) {
     float a[4] = {};
-    for (int s0 = 0; s0 < splits; s0 += 8) {
+    const int parts = low ? 2 * splits : splits;       // (the splits, then the low row's)
+    const size_t low0 = (size_t)kLossLow * p.Kx / 4;
+    for (int s0 = 0; s0 < parts; s0 += 8) {
       float4 y[8];
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        y[s] = s0 + s < splits ? __ldcs(x + (s0 + s) * step + c4) : make_float4(0, 0, 0, 0);
+      for (int b = 0; b < 8; ++b) {
+        const int s = s0 + b;
+        y[b] = s < parts ? __ldcs(x + (s < splits ? s * step : low0 + (s - splits) * step) + c4)
+                         : make_float4(0, 0, 0, 0);
+      }
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        a[0] += y[s].x; a[1] += y[s].y; a[2] += y[s].z; a[3] += y[s].w;
+      for (int b = 0; b < 8; ++b) {
+        a[0] += y[b].x; a[1] += y[b].y; a[2] += y[b].z; a[3] += y[b].w;
       }
     }
-    if (low)
-      for (int s = 0; s < splits; ++s) {
-        const float4 y = x[(size_t)kLossLow * p.Kx / 4 + s * step + c4];
-        a[0] += y.x; a[1] += y.y; a[2] += y.z; a[3] += y.w;
-      }
     const int c = 4 * c4;
     const bool head = c < p.Hp;
     if (p.qres) {                             // (bf16: H is a multiple of 8)
@@ -759,8 +760,11 @@ cudaError_t launch_loss_dz_f32(const LossPlan& p, int v0, int v1) {
 
 cudaError_t launch_loss_dx(const LossPlan& p) {
   const bool f32 = p.dtype == 0;
-  cudaError_t e = launch_after(f32 ? loss_dx_rows<float> : loss_dx_rows<__nv_bfloat16>, p.T, 256,
-                               0, p.stream, p);
+  // several CTAs a row where rows alone do not fill the GPU: 37 rows of 2304 columns take 14 us
+  // with one CTA each, 7 with three
+  const unsigned y = (unsigned)std::max(1, std::min((p.Kx / 4 + 255) / 256, 1216 / p.T));
+  cudaError_t e = launch_after(f32 ? loss_dx_rows<float> : loss_dx_rows<__nv_bfloat16>,
+                               dim3((unsigned)p.T, y), 256, 0, p.stream, p);
   if (e == cudaSuccess && p.d_w1)
     e = launch_after(f32 ? loss_w1_rows<float> : loss_w1_rows<__nv_bfloat16>, p.T, 256,
                      sizeof(float) * 8 * (size_t)p.rp, p.stream, p);
