@@ -411,6 +411,7 @@ __global__ void __launch_bounds__(256) loss_plan_few(const LossPlan p) {
 constexpr int kRowsThreads = 256;
 __device__ __forceinline__ float2 join_row(const LossPlan& p, int i, int n_voc, float2* s_w) {
   const int tid = threadIdx.x, n = (n_voc + p.stat_cols - 1) / p.stat_cols;
+  const float zl = p.zlab[i];
   const float2* st = p.stat + (size_t)i * p.n_stat;
   // running maximum and sum over sweeps of eight tiles a thread (a maximum of -inf: all its
   // logits are, and its sum is 0)
@@ -443,7 +444,7 @@ __device__ __forceinline__ float2 join_row(const LossPlan& p, int i, int n_voc, 
   Sum2 v;
   v.s = s * __expf(m - ref);
   __syncthreads();
-  const float sum = block_sum(v, s_w).value(), zl = p.zlab[i];
+  const float sum = block_sum(v, s_w).value();
   if (zl >= mx) {
     // (z - z: an infinite z is no loss of 0)
     const float l = log1pf(mx > -INFINITY ? sum * expf(mx - zl) : 0.f) + (zl - zl);
@@ -525,36 +526,48 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows(const LossPlan p) {
   const int i = blockIdx.x, tid = threadIdx.x;
   const bool first = blockIdx.y == 0;
   if (i < n_tok) {
-    const float2 r = join_row(p, i, n_voc, s_w);
+    const float2 joined = join_row(p, i, n_voc, s_w);
     if (tid == 0) {
-      s_row = r;
+      s_row = joined;
       if (first) {
-        p.lse[i] = r.x;
-        p.loss[p.tok[i]] = r.y;
+        p.lse[i] = joined.x;
+        p.loss[p.tok[i]] = joined.y;
       }
     }
+    __syncthreads();
+    const float2 r = s_row;
+    if (DZ == 1) row_dz_bf16(p, i, n_voc, loss_low(p, n_tok), r.x, r.y, blockIdx.y, gridDim.y);
+    if (DZ == 2) row_dz_f32(p, i, 0, n_voc, r.x, r.y, blockIdx.y, gridDim.y);
   }
-  if (first && tid == 0) {
+  if (!first) return;
+  if (tid == 0) {
     __threadfence();
     s_last = atomicAdd(p.ctrl + kLossDone, 1u) == gridDim.x - 1;
   }
   __syncthreads();
-  if (first && s_last) {
+  if (s_last) {
     __threadfence();
     Sum2 a;
-    for (int j = tid; j < n_tok; j += blockDim.x) {
-      // the product's rounding error goes into the sum too
-      const float w = p.wrow[j], x = __ldcg(p.loss + p.tok[j]), y = w * x;
-      a.add(y);
-      a.c += fmaf(w, x, -y);
+    constexpr int kAt = 8;                    // (rows of a thread at once)
+    for (int j0 = tid; j0 < n_tok; j0 += kAt * kRowsThreads) {
+      float w[kAt], x[kAt];
+#pragma unroll
+      for (int q = 0; q < kAt; ++q) {
+        const int j = j0 + q * kRowsThreads;
+        w[q] = j < n_tok ? p.wrow[j] : 0.f;
+        x[q] = j < n_tok ? __ldcg(p.loss + p.tok[j]) : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < kAt; ++q) {
+        // the product's rounding error goes into the sum too
+        const float y = w[q] * x[q];
+        a.add(y);
+        a.c += fmaf(w[q], x[q], -y);
+      }
     }
     const Sum2 t = block_sum(a, s_w);
     if (tid == 0) *p.total = n_tok > 0 ? __uint_as_float(p.ctrl[kLossScale]) * t.value() : 0.f;
   }
-  if (i >= n_tok) return;
-  const float2 r = s_row;
-  if (DZ == 1) row_dz_bf16(p, i, n_voc, loss_low(p, n_tok), r.x, r.y, blockIdx.y, gridDim.y);
-  if (DZ == 2) row_dz_f32(p, i, 0, n_voc, r.x, r.y, blockIdx.y, gridDim.y);
 }
 
 // q of columns [v0, v1) from stored logits, once the rows' log-sum-exps are known (pieces).

@@ -184,6 +184,17 @@ def test_small_losses_keep_their_digits(dtype, T, H, V, pieces):
 
 
 @pytest.mark.parametrize("case", [
+    dict(H=33, V=1, dtype="f32"), dict(H=33, V=500, dtype="f32", form="bias", n_emit=1),
+    dict(H=64, V=512, dtype="bf16", form="bias", n_emit=1)], ids=str)
+@pytest.mark.parametrize("T", [1, 20, 200])
+def test_loss_of_one_head_row_is_zero(case, T):
+    out, _, _ = run_loss(T=T, r=8, ignored=T // 4, **case)
+    assert int(out.n_rows) == T - T // 4
+    for name in ("loss", "total", "d_hidden", "d_lm_head", "d_markov_w1", "d_markov_w2"):
+        assert not getattr(out, name).any(), name
+
+
+@pytest.mark.parametrize("case", [
     dict(T=3, H=7, V=13, r=3), dict(T=65, H=33, V=131, r=5), dict(T=97, H=129, V=1001, r=17),
     dict(T=31, H=65, V=777, r=9, form="bias", n_emit=101),
     dict(T=31, H=65, V=777, r=9, form="d2t", n_emit=101, pieces=2)], ids=str)
