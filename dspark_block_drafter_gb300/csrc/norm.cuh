@@ -126,7 +126,8 @@ struct Part {
 // The current and the next row of N tensors in shared memory, and the two weight vectors
 // (w_post, w_pre).  Vectors of 16, 8 or 4 bytes go to the thread's own places (so no barrier is
 // needed).  bf16 rows that are not whole words (H odd, or an odd address) are copied word by
-// word as they lie, and their threads meet at a barrier before they read single elements.
+// word as they lie, and their threads meet at a barrier before they read single elements (a
+// word may hold half a neighbouring row's element: in place it may be changing, and is not used).
 template <typename E, int VEC, int N, int kPer>
 struct Rows {
   static constexpr int kBytes = VEC * (int)sizeof(E);
