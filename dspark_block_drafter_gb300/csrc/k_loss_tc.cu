@@ -30,9 +30,10 @@
 // care.
 //
 // The logits are never stored.  Their epilogue has one row per thread: it takes the maximum
-// and the sum of exponentials of each 128-column tile, and, when gradients follow, stores
-// how far each logit lies below its tile's maximum as a 16-bit fixed-point number (see
-// loss.h), from which the gradient is made once the row's log-sum-exp is known.
+// and the sum of exponentials of each 128-column tile, the label's column aside, and, when
+// gradients follow, stores how far each logit lies below its tile's maximum as a 16-bit
+// fixed-point number (see loss.h), from which the gradient is made once the row's log-sum-exp
+// is known.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

@@ -60,8 +60,8 @@ struct LossPlan {
   void *wc, *w2c;                     // bf16 bias form: the compact head [Vh][H], [r][Vh]
                                       // (zeros up to a multiple of 256 rows past n_voc)
   void* x;                            // [Tp][Kx]
-  float2* stat;                       // [Tp][n_stat] per vocabulary tile: the maximum of
-                                      // z, and the sum of exp(z - maximum)
+  float2* stat;                       // [Tp][n_stat] per vocabulary tile, the label aside: the
+                                      // maximum of z, and the sum of exp(z - maximum)
   int n_stat, stat_cols;
   float *zlab, *lse;                  // [Tp]
   void* q;                            // [Tp][ldq]; fp32: logits, then their gradient; bf16:
