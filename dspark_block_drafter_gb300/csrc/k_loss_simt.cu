@@ -351,8 +351,8 @@ loss_grads_few(const LossPlan p, int v0, int v1, bool first, int n_dx) {
   if (!dx) b -= n_dx;
   const int c0 = b % across * kTile, part = b / across;
   const bool head = c0 < p.Hp;
-  if (n_tok == 0) return;
   if (dx) {
+    if (n_tok == 0) return;                   // (no row of dX; dW is zero and is written)
     const float* w = (const float*)(head ? p.lm_head : p.w2);
     const int share = ((v1 - v0 + p.splits - 1) / p.splits + kShare - 1) / kShare * kShare;
     const int ja = v0 + part * share, jb = min(n_voc, ja + share);
