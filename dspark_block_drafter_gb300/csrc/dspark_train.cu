@@ -212,7 +212,8 @@ static size_t plan_norm(const dspark_norm_config* c, char* ws, NormArgs* a) {
 static bool norm_f32(const dspark_norm_config* c) { return c->dtype == DSPARK_F32; }
 
 static void fill_norm(const dspark_norm_config* c, NormArgs* a) {
-  a->T = c->T; a->H = c->H; a->dtype = c->dtype; a->span = c->gate_span;
+  a->T = c->T; a->H = c->H; a->dtype = c->dtype;
+  a->span = std::min(c->gate_span, c->T);     // (the same grouping; T + span stays an int)
   a->eps = c->eps; a->scale = c->residual_scale; a->offset = c->weight_offset;
 }
 

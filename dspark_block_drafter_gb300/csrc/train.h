@@ -11,7 +11,7 @@
 namespace dspark {
 
 struct NormArgs {
-  int T, H, dtype, span;
+  int T, H, dtype, span;       // span: gate_span, at most T
   float eps, scale, offset;
   const void *x, *y, *gate, *w_post, *w_pre, *d_h, *d_x_out;
   void *x_out, *h;

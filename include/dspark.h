@@ -488,7 +488,8 @@ typedef struct dspark_norm_config {
   int32_t T;             /* rows (tokens), 1 .. 2^30 */
   int32_t H;             /* features, 1 .. 8192 */
   int32_t dtype;         /* dspark_dtype of every tensor */
-  int32_t gate_span;     /* consecutive rows that share one gate row, >= 1 */
+  int32_t gate_span;     /* consecutive rows that share one gate row, >= 1; T or more: all
+                            rows share one */
   float eps;             /* > 0 */
   float residual_scale;  /* s below; finite */
   float weight_offset;   /* added to the norm weights (1 for weights stored about 0) */
