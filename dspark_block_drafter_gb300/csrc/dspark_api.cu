@@ -21,6 +21,7 @@ dspark_status fail(dspark_status s, const std::string& msg) {
 }
 
 dspark_status cuda_fail(cudaError_t e, const char* where) {
+  cudaGetLastError();    // (reported here: the next call's launches must not find it again)
   g_last_error = std::string(where) + ": " + cudaGetErrorString(e);
   return DSPARK_ERR_CUDA;
 }
