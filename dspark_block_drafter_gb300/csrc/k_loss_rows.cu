@@ -473,6 +473,7 @@ __device__ __forceinline__ void row_dz_bf16(const LossPlan& p, int i, int n_voc,
   uint4* q = (uint4*)((uint16_t*)p.q + (size_t)i * p.ldq);
   const float2* st = p.stat + (size_t)i * p.n_stat;
   const float w = p.wrow[i], log2_w = log2f(w);              // (w = 0: -inf, e = 0)
+  const float far = lse - lse;     // 0; NaN in every column when a logit of the row is NaN or +inf
   const int lab = p.lab[i], end = (n_voc + 255) / 256 * 32, tiles = (n_voc + 127) / 128;
   const int step = parts * blockDim.x;
   for (int c0 = part * blockDim.x + threadIdx.x; c0 < end; c0 += 2 * step) {
@@ -494,7 +495,8 @@ __device__ __forceinline__ void row_dz_bf16(const LossPlan& p, int i, int n_voc,
       uint32_t o[4], r[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float e0 = loss_gap_exp(g[j] & 0xFFFFu, s[h]), e1 = loss_gap_exp(g[j] >> 16, s[h]);
+        const float e0 = loss_gap_exp(g[j] & 0xFFFFu, s[h], far);
+        const float e1 = loss_gap_exp(g[j] >> 16, s[h], far);
         const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
         o[j] = *reinterpret_cast<const uint32_t*>(&b);
         if (low) {

@@ -111,7 +111,7 @@ __device__ __forceinline__ int loss_head_row(const LossPlan& p, int j) {
 // A logit's distance d >= 0 below its tile's maximum in 16 bits: steps of 1 / 896, so that a
 // probability is off by at most 0.06% (a bf16 rounding: 0.39%) down to e^-73 of the tile's
 // largest, below every fp32 gradient that sums to anything; kLossFar from there on (and for
-// anything that is not a number).
+// anything that is not a number: the row's log-sum-exp is none either, and says so).
 constexpr float kLossSteps = 896.f;
 constexpr uint32_t kLossFar = 0xFFFFu;
 __device__ __forceinline__ uint32_t loss_gap(float d) {
@@ -127,11 +127,11 @@ __device__ __forceinline__ float loss_exp2(float x) {
   return y;
 }
 __device__ __forceinline__ float loss_exp(float x) { return loss_exp2(x * 1.44269504f); }
-// scale * exp(-distance), given log2(scale)
-__device__ __forceinline__ float loss_gap_exp(uint32_t gap, float log2_scale) {
+// scale * exp(-distance), given log2(scale); `far` for kLossFar
+__device__ __forceinline__ float loss_gap_exp(uint32_t gap, float log2_scale, float far) {
   const float d = __uint_as_float(0x4B000000u | gap) - 8388608.f;
   const float e = loss_exp2(fmaf(d, -1.44269504f / kLossSteps, log2_scale));
-  return gap == kLossFar ? 0.f : e;
+  return gap == kLossFar ? far : e;
 }
 
 // k_loss_rows.cu: everything but the products
