@@ -26,8 +26,11 @@
 // therefore read every few K-blocks and the parts are added in fp32 registers (which hold the
 // tile's 128 columns of a row until it is complete).  Pairs read it every 12 K-blocks (losses
 // off by 5e-7, the logits of 4096 rows 6% slower than in one sum; every 8: 2e-7, 11%), single
-// CTAs, which wait for memory anyway, every 4.  The gradients, rounded to bf16, need no such
-// care.
+// CTAs, which wait for memory anyway, every 4.  The gradients are rounded to bf16, and need such
+// care only where a sum is long: each step of 16 loses near 1e-7 of a sum of terms of one sign
+// (T = 2^20 rows: dW short by 0.6%; signs mixed, 0.1%).  dX adds to its partial result in memory
+// every 1024 K-blocks, and dW sums more than 256 K-blocks in registers, in a kernel of its own
+// (the registers cost the common case spills): a loss of 1e-4 in dW and 4e-4 in dX at most.
 //
 // The logits are never stored.  Their epilogue has one row per thread: it takes the maximum
 // and the sum of exponentials of each 128-column tile, the label's column aside, and, when
@@ -59,6 +62,8 @@ constexpr uint32_t kRowBytes = 128;                  // dW: a row's part of a st
 constexpr uint32_t kStaging = kEpiWarps * 32 * kRowBytes;
 template <int CG>
 constexpr int kSumBlocks = CG == 2 ? 12 : 4;         // K-blocks of one part of a logit's sum
+constexpr int kDxBlocks = 1024;                      // K-blocks of one part of a sum of dX,
+constexpr int kDwBlocks = 256;                       // and of dW where T is above that
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kBarBytes = 512;
 constexpr long long kWaitBudget = 2000000000ll;      // ~1 s of SM clocks
@@ -271,7 +276,8 @@ __device__ __forceinline__ void write_zeros(const TcArgs& g, int lane) {
   }
 }
 
-template <int MODE, int CG>
+// LONG: the rows may be more than kDwBlocks K-blocks (kDw, kGrads).
+template <int MODE, int CG, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g, int stages) {
   constexpr int kBoxB = kTileN / CG / 64;              // boxes of N this CTA stages
@@ -326,6 +332,12 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
   const int n_tok = (int)p.ctrl[kLossTok], n_voc = (int)p.ctrl[kLossVoc];
   const int splits = MODE == kDx || MODE == kGrads ? (int)p.ctrl[kLossSplits] : 1;
   const Sequence<MODE, CG> seq(g, n_tok, n_voc, splits, blockIdx.x / CG, gridDim.x / CG);
+  // where the part of a unit's sum that starts at K-block kb ends
+  auto part_end = [&](const Unit& t, int kb) {
+    if (MODE == kLogits) return min(t.kb1, kb + kSumBlocks<CG>);
+    if (MODE == kDx || (MODE == kGrads && !t.dw)) return min(t.kb1, kb + kDxBlocks);
+    return LONG ? min(t.kb1, kb + kDwBlocks) : t.kb1;
+  };
 
   auto give_up = [&]() {
     *abort_flag = 1;
@@ -464,7 +476,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
       using K = std::false_type;
       for (int i = 0; seq.get(i, t); ++i) {
         for (int kb = t.kb0, part = 0; part == 0 || kb < t.kb1; ++part, ++local) {
-          const int end = MODE == kLogits ? min(t.kb1, kb + kSumBlocks<CG>) : t.kb1;
+          const int end = part_end(t, kb);
           const uint32_t acc = local & 1, aph = (local >> 1) & 1;
           if (!ptx::mbar_wait(&acc_empty[acc], aph ^ 1, kWaitBudget, abort_flag)) {
             ok = false;
@@ -627,41 +639,69 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
                            loss_label_entry(wt, p.loss[p.tok[m]]));
         }
       } else {
-        if (!acc_wait()) break;
-        const uint32_t at = at0 + (local & 1) * kTileN;
         const bool none = t.kb1 <= t.kb0;             // (nothing was accumulated)
         const bool markov = t.markov;
         const int c0 = t.c0 + half * 128;
         if (MODE == kDx || (MODE == kGrads && !t.dw)) {
           const int width = min(128, (markov ? p.Kx : p.Hp) - c0);
           float* dx = p.dxp + ((size_t)t.split * p.Tp + m) * p.Kx + c0;
+          bool add = !g.first;
+          for (int kb = t.kb0, end; ok; kb = end, add = true) {
+            end = part_end(t, kb);
+            if (!acc_wait()) break;
+            const uint32_t at = at0 + (local & 1) * kTileN;
 #pragma unroll 1
-          for (int c = 0; c < width; c += 32) {
-            uint32_t r[32];
-            ptx::tmem_ld_32x32b_x32(at + c, r);
-            ptx::tmem_ld_wait();
-            if (m >= n_tok &&
-                !(CG == 1 && loss_low(p, n_tok) && m >= kLossLow && m < kLossLow + n_tok))
-              continue;
+            for (int c = 0; c < width; c += 32) {
+              uint32_t r[32];
+              ptx::tmem_ld_32x32b_x32(at + c, r);
+              ptx::tmem_ld_wait();
+              if (m >= n_tok &&
+                  !(CG == 1 && loss_low(p, n_tok) && m >= kLossLow && m < kLossLow + n_tok))
+                continue;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              float x[8];
+              for (int j = 0; j < 32; j += 8) {
+                float x[8];
 #pragma unroll
-              for (int b = 0; b < 8; ++b) x[b] = none ? 0.f : __uint_as_float(r[j + b]);
-              if (!g.first) {
-                const float4 y0 = *reinterpret_cast<const float4*>(dx + c + j);
-                const float4 y1 = *reinterpret_cast<const float4*>(dx + c + j + 4);
-                x[0] += y0.x; x[1] += y0.y; x[2] += y0.z; x[3] += y0.w;
-                x[4] += y1.x; x[5] += y1.y; x[6] += y1.z; x[7] += y1.w;
+                for (int b = 0; b < 8; ++b) x[b] = none ? 0.f : __uint_as_float(r[j + b]);
+                if (add) {
+                  const float4 y0 = *reinterpret_cast<const float4*>(dx + c + j);
+                  const float4 y1 = *reinterpret_cast<const float4*>(dx + c + j + 4);
+                  x[0] += y0.x; x[1] += y0.y; x[2] += y0.z; x[3] += y0.w;
+                  x[4] += y1.x; x[5] += y1.y; x[6] += y1.z; x[7] += y1.w;
+                }
+                ptx::st_global_v8(dx + c + j, x);
               }
-              ptx::st_global_v8(dx + c + j, x);
             }
+            acc_free();
+            if (end >= t.kb1) break;
           }
+          if (!ok) break;
         } else {
           const int j0 = g.v0 + m;                            // compact head row
           const bool live = j0 < min(g.v1, n_voc);
           const size_t row = live ? (size_t)loss_head_row(p, j0) : 0;
           const int width = min(128, markov ? p.r - (c0 - p.Hp) : p.H - c0);
+          float z[LONG ? 128 : 1];                            // the parts before the last
+          if (LONG) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) z[c] = 0.f;
+            for (int kb = t.kb0, end = part_end(t, kb); end < t.kb1; kb = end, end = part_end(t, kb)) {
+              if (!acc_wait()) break;
+              const uint32_t at = at0 + (local & 1) * kTileN;
+#pragma unroll
+              for (int c = 0; c < 128; c += 32) {
+                uint32_t r[32];
+                ptx::tmem_ld_32x32b_x32(at + c, r);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) z[c + j] += __uint_as_float(r[j]);
+              }
+              acc_free();
+            }
+            if (!ok) break;
+          }
+          if (!acc_wait()) break;
+          const uint32_t at = at0 + (local & 1) * kTileN;
           uint32_t o[64];                                     // 128 columns, in pairs
 #pragma unroll
           for (int c = 0; c < 128; c += 32) {
@@ -670,9 +710,13 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(
-                  none ? 0.f : __uint_as_float(r[j]) * scale,
-                  none ? 0.f : __uint_as_float(r[j + 1]) * scale);
+              float x0 = __uint_as_float(r[j]), x1 = __uint_as_float(r[j + 1]);
+              if (LONG) {
+                x0 += z[c + j];
+                x1 += z[c + j + 1];
+              }
+              const __nv_bfloat162 b2 =
+                  __floats2bfloat162_rn(none ? 0.f : x0 * scale, none ? 0.f : x1 * scale);
               o[(c + j) / 2] = *reinterpret_cast<const uint32_t*>(&b2);
             }
           }
@@ -724,9 +768,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
               }
             }
           }
-          continue;
         }
-        acc_free();
       }
     }
   }
@@ -808,7 +850,7 @@ bool make_maps(const TcArgs& g, Maps* m) {
   return ok;
 }
 
-template <int MODE, int CG>
+template <int MODE, int CG, bool LONG = false>
 cudaError_t launch(const TcArgs& g, long long tiles) {
   if (tiles <= 0) return cudaSuccess;
   Maps maps = {};
@@ -819,7 +861,7 @@ cudaError_t launch(const TcArgs& g, long long tiles) {
   constexpr size_t smem = fixed + (size_t)stages * stage;
   int sms = 0;
   cudaError_t e = device_sms(&sms);
-  if (e == cudaSuccess) e = raise_smem_limit((const void*)loss_product<MODE, CG>, smem);
+  if (e == cudaSuccess) e = raise_smem_limit((const void*)loss_product<MODE, CG, LONG>, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<long long>(tiles, std::max(1, sms / CG)) * CG);
@@ -835,7 +877,7 @@ cudaError_t launch(const TcArgs& g, long long tiles) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, loss_product<MODE, CG>, maps, g, stages);
+  return cudaLaunchKernelEx(&cfg, loss_product<MODE, CG, LONG>, maps, g, stages);
 }
 
 // Single CTAs (128-row tiles) when the rows fit one tile, pairs (256) otherwise.
@@ -883,9 +925,11 @@ cudaError_t launch_loss_grads_tc(const LossPlan& p, int v0, int v1, bool first) 
   }
   const long long n_dx = (long long)row_tiles(p.T) * g.dx.all() * p.splits;
   const long long n_dw = (long long)((v1 - v0 + 255) / 256) * g.dw.all();
-  if (n_dx > 0 && n_dw > 0 && !single(p.T)) return launch<kGrads, 2>(g, n_dx + n_dw);
+  const bool lengthy = p.T > kDwBlocks * kBlockK;
+  if (n_dx > 0 && n_dw > 0 && !single(p.T))
+    return lengthy ? launch<kGrads, 2, true>(g, n_dx + n_dw) : launch<kGrads, 2>(g, n_dx + n_dw);
   cudaError_t e = single(p.T) ? launch<kDx, 1>(g, n_dx) : launch<kDx, 2>(g, n_dx);
-  if (e == cudaSuccess) e = launch<kDw, 2>(g, n_dw);
+  if (e == cudaSuccess) e = lengthy ? launch<kDw, 2, true>(g, n_dw) : launch<kDw, 2>(g, n_dw);
   return e;
 }
 

@@ -1,0 +1,73 @@
+"""Gradients that are sums of very many terms of one sign.
+
+The tensor core cuts its partial sums toward zero: each step of 16 terms loses a unit in the last
+place or so of the partial sum, near 1e-7 of the final one.  A sum over 2^20 rows or columns in one
+accumulator is short by 0.6%.  The bounds allow the loss 2^-24 a step over 2^16 rows and over 2^18
+columns.  The other errors have no sign and average out over the many elements of a gradient: the
+output's rounding, 2^-9 / sqrt(3) of an element (uniform within half a unit), and those of the
+gradient of the logits, as large and averaged over the terms too: five standard deviations of
+both."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+ROUNDING = 2.0 ** -9 / 3 ** 0.5
+
+
+def _make(T, H, V, dtype, gen, hidden_std, head):
+    from dspark_block_drafter_gb300 import torch_io as tio
+    hidden = (torch.randn(T, H, generator=gen, device="cuda").abs() * hidden_std).to(dtype)
+    cfg = tio.make_loss_config(T, H, V, 0, "bf16" if dtype is torch.bfloat16 else "f32",
+                               reduction="sum", vocab_pieces=1)
+    return tio, hidden, cfg, tio.Head(head, None, None)
+
+
+def _rows_off(T, dtype):
+    """Relative errors of d_lm_head's rows that no label names: sums of positive terms."""
+    H, V, labelled = 64, 256, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    head = (torch.randn(V, H, generator=g, device="cuda") * 0.02).to(dtype)
+    tio, hidden, cfg, head = _make(T, H, V, dtype, g, 1.0, head)
+    labels = torch.randint(labelled, (T,), generator=g, device="cuda").int()
+    out = tio.LossOutputs.allocate(cfg, head, d_hidden=False)
+    ws = tio.loss_workspace_for(cfg, head, out)
+    tio.head_loss(cfg, head, hidden, None, labels, out, ws)
+    assert tio.device_status(ws) == 0
+    want = torch.zeros(V - labelled, H, dtype=torch.float64, device="cuda")
+    for a in range(0, T, 1 << 16):
+        x = hidden[a:a + (1 << 16)].double()
+        q = torch.softmax(x @ head.lm_head.double().t(), 1)
+        want += q[:, labelled:].t() @ x
+    return (out.d_lm_head[labelled:].double() - want) / want
+
+
+@pytest.mark.parametrize("T", [4000, 70000, 2 ** 20 - 3])
+def test_head_gradient_over_many_rows(T):
+    off = _rows_off(T, torch.bfloat16)
+    lost = min(T, 1 << 16) / 16 * 2.0 ** -24
+    assert abs(off.mean().item()) < lost + 5 * ROUNDING * (2 / off.numel()) ** 0.5
+
+
+def test_hidden_gradient_over_many_columns():
+    T, H, V = 4096, 2048, 2 ** 20
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    w = torch.empty(V, H, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, V, 1 << 16):
+        w[a:a + (1 << 16)] = torch.randn(1 << 16, H, generator=g, device="cuda").abs() * 0.02
+    w[:4] = 0                                   # the labels' rows: nothing is taken off the sum
+    tio, hidden, cfg, head = _make(T, H, V, torch.bfloat16, g, 1.0, w)
+    labels = torch.randint(4, (T,), generator=g, device="cuda").int()
+    out = tio.LossOutputs.allocate(cfg, head)     # (with d_lm_head: one split of the columns)
+    ws = tio.loss_workspace_for(cfg, head, out)
+    tio.head_loss(cfg, head, hidden, None, labels, out, ws)
+    assert tio.device_status(ws) == 0
+    x = hidden[:8].double()
+    z = torch.cat([x @ w[a:a + (1 << 16)].double().t() for a in range(0, V, 1 << 16)], 1)
+    q = torch.softmax(z, 1)
+    want = sum(q[:, a:a + (1 << 16)] @ w[a:a + (1 << 16)].double() for a in range(0, V, 1 << 16))
+    off = (out.d_hidden[:8].double() - want) / want
+    lost = 2 ** 18 / 16 * 2.0 ** -24
+    assert abs(off.mean().item()) < lost + 5 * ROUNDING * (2 / off.numel()) ** 0.5
