@@ -26,6 +26,9 @@ namespace {
 constexpr int kTile = 64, kShare = 64;   // (a split of K is a multiple of kShare)
 constexpr int R = 4;                     // a tile's results of a thread: R x 4
 constexpr int kFewRows = 16;             // rows of the kernels for few
+// Terms of one chain of additions in dX and dW; longer sums add such parts up in their output (one
+// chain over 2^20 rows was off by 1.3e-4, over 70000 by 1.6e-5; in parts 1e-6).
+constexpr int kChain = 4096;
 
 // base[at] where `ok`, else 0.  The load itself is unconditional (base[0] stands in), so that
 // a thread's loads are issued together: behind branches they took turns, at a trip to memory
@@ -249,33 +252,39 @@ __device__ __forceinline__ void dx_tile(const LossPlan& p, int v0, int v1, bool 
   const float* q = (const float*)p.q;
   const float* w = (const float*)p.lm_head;
   const float* w2 = (const float*)p.w2;
-  float acc[R][4] = {};
   const bool head = c0 < p.Hp;
-  if (jb > ja)
-    tile_product(
-        acc, jb - ja, true,
-        [&](int m, int k) {
-          const int j = ja + k;
-          return read_if(m0 + m < n_tok && j < jb, q, (size_t)(m0 + m) * p.ldq + (j - v0));
-        },
-        [&](int) { return !head; },
-        [&](int n, int k, bool) {
-          const int j = min(ja + k, jb - 1), row = loss_head_row(p, j);
-          const int c = c0 + n - (head ? 0 : p.Hp);
-          return read_if(ja + k < jb && c < (head ? p.H : p.r), head ? w : w2,
-                         head ? (size_t)row * p.H + c : (size_t)c * p.Vh + row);
-        });
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   float* dx = p.dxp + (size_t)bz * p.Tp * p.Kx;
+  int j0 = ja;
+  do {                                        // (an empty range writes zeros)
+    const int j1 = min(jb, j0 + kChain);
+    float acc[R][4] = {};
+    if (j1 > j0)
+      tile_product(
+          acc, j1 - j0, true,
+          [&](int m, int k) {
+            const int j = j0 + k;
+            return read_if(m0 + m < n_tok && j < j1, q, (size_t)(m0 + m) * p.ldq + (j - v0));
+          },
+          [&](int) { return !head; },
+          [&](int n, int k, bool) {
+            const int j = min(j0 + k, j1 - 1), row = loss_head_row(p, j);
+            const int c = c0 + n - (head ? 0 : p.Hp);
+            return read_if(j0 + k < j1 && c < (head ? p.H : p.r), head ? w : w2,
+                           head ? (size_t)row * p.H + c : (size_t)c * p.Vh + row);
+          });
+    const bool add = !first || j0 > ja;
 #pragma unroll
-  for (int a = 0; a < R; ++a)
+    for (int a = 0; a < R; ++a)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int i = m0 + R * ty + a, c = c0 + 4 * tx + b;
-      if (i >= n_tok) continue;
-      float* d = dx + (size_t)i * p.Kx + c;
-      *d = first ? acc[a][b] : *d + acc[a][b];
-    }
+      for (int b = 0; b < 4; ++b) {
+        const int i = m0 + R * ty + a, c = c0 + 4 * tx + b;
+        if (i >= n_tok) continue;
+        float* d = dx + (size_t)i * p.Kx + c;
+        *d = add ? *d + acc[a][b] : acc[a][b];
+      }
+    j0 += kChain;
+  } while (j0 < jb);
 }
 
 // dW of vocabulary columns [v0, v1): tile (bx, by).
@@ -286,31 +295,36 @@ __device__ __forceinline__ void dw_tile(const LossPlan& p, int v0, int v1, int b
   if (j0 >= n_voc || (head ? !p.d_lm_head : !p.d_w2)) return;
   const float* q = (const float*)p.q;
   const float* x = (const float*)p.x;
-  float acc[R][4] = {};
-  tile_product(
-      acc, n_tok, false,
-      [&](int m, int k) {
-        const int j = j0 + m;
-        return read_if(j < n_voc && k < n_tok, q, (size_t)k * p.ldq + (j - v0));
-      },
-      [](int) { return false; },
-      [&](int n, int k, bool) { return read_if(k < n_tok, x, (size_t)k * p.Kx + c0 + n); });
   const float scale = __uint_as_float(p.ctrl[kLossScale]);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  int i0 = 0;
+  do {                                        // (no rows: zeros)
+    const int i1 = min(n_tok, i0 + kChain);
+    float acc[R][4] = {};
+    tile_product(
+        acc, i1 - i0, false,
+        [&](int m, int k) {
+          const int j = j0 + m;
+          return read_if(j < n_voc && i0 + k < i1, q, (size_t)(i0 + k) * p.ldq + (j - v0));
+        },
+        [](int) { return false; },
+        [&](int n, int k, bool) {
+          return read_if(i0 + k < i1, x, (size_t)(i0 + k) * p.Kx + c0 + n);
+        });
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < 4; ++a)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int j = j0 + 4 * ty + a, c = c0 + 4 * tx + b;
-      if (j >= n_voc) continue;
-      const int row = loss_head_row(p, j);
-      const float g = acc[a][b] * scale;
-      if (head) {
-        if (c < p.H) ((float*)p.d_lm_head)[(size_t)row * p.H + c] = g;
-      } else if (c - p.Hp < p.r) {
-        ((float*)p.d_w2)[(size_t)(c - p.Hp) * p.Vh + row] = g;
+      for (int b = 0; b < 4; ++b) {
+        const int j = j0 + 4 * ty + a, c = c0 + 4 * tx + b;
+        if (j >= n_voc || (head ? c >= p.H : c - p.Hp >= p.r)) continue;
+        const int row = loss_head_row(p, j);
+        float* d = head ? (float*)p.d_lm_head + (size_t)row * p.H + c
+                        : (float*)p.d_w2 + (size_t)(c - p.Hp) * p.Vh + row;
+        const float g = acc[a][b] * scale;
+        *d = i0 > 0 ? *d + g : g;
       }
-    }
+    i0 += kChain;
+  } while (i0 < n_tok);
 }
 
 // Both: the first `n_dx` CTAs make dX, the others dW.
@@ -365,48 +379,53 @@ loss_grads_few(const LossPlan p, int v0, int v1, bool first, int n_dx) {
       in[h] = c < (head ? p.H : p.r);
       at[h] = in[h] ? (head ? (size_t)c : (size_t)c * p.Vh) : 0;
     }
-    float sum[2][NT] = {};
-    for (int j1 = ja; j1 < jb; j1 += kChunk) {
-      const int n = min(kChunk, jb - j1);
+    float(*s_sum)[8][kTile] = reinterpret_cast<float(*)[8][kTile]>(smem);   // [NT]
+    float* out = p.dxp + (size_t)part * p.Tp * p.Kx;
+    int j0 = ja;
+    do {                                      // (an empty range writes zeros)
+      const int end = min(jb, j0 + 8 * kChain);
+      float sum[2][NT] = {};
+      for (int j1 = j0; j1 < end; j1 += kChunk) {
+        const int n = min(kChunk, end - j1);
+        __syncthreads();
+        // (past the range: a row that exists, times zero)
+        const int j = min(tid, n - 1);
+        s_row[tid] = loss_head_row(p, j1 + j);
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+          s_q[tid][m] = read_if(tid < n && m < n_tok, q, (size_t)m * p.ldq + (j1 - v0 + j));
+        __syncthreads();
+        for (int k0 = warp * 16; k0 < n; k0 += 8 * 16) {
+          float y[2][16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) y[h][k] = w[at[h] + s_row[k0 + k] * row_step];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+              const float g = s_q[k0 + k][m];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) sum[h][m] = fmaf(g, y[h][k], sum[h][m]);
+            }
+        }
+      }
       __syncthreads();
-      // (past the range: a row that exists, times zero)
-      const int j = min(tid, n - 1);
-      s_row[tid] = loss_head_row(p, j1 + j);
 #pragma unroll
       for (int m = 0; m < NT; ++m)
-        s_q[tid][m] = read_if(tid < n && m < n_tok, q, (size_t)m * p.ldq + (j1 - v0 + j));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s_sum[m][warp][l + 32 * h] = in[h] ? sum[h][m] : 0.f;
       __syncthreads();
-      for (int k0 = warp * 16; k0 < n; k0 += 8 * 16) {
-        float y[2][16];
+      for (int m = group; m < n_tok; m += 4) {
+        float g = 0.f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) y[h][k] = w[at[h] + s_row[k0 + k] * row_step];
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-          for (int m = 0; m < NT; ++m) {
-            const float g = s_q[k0 + k][m];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) sum[h][m] = fmaf(g, y[h][k], sum[h][m]);
-          }
+        for (int e = 0; e < 8; ++e) g += s_sum[m][e][lane];
+        float* d = out + (size_t)m * p.Kx + c0 + lane;
+        *d = first && j0 == ja ? g : *d + g;
       }
-    }
-    __syncthreads();
-    float(*s_sum)[8][kTile] = reinterpret_cast<float(*)[8][kTile]>(smem);   // [NT]
-#pragma unroll
-    for (int m = 0; m < NT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) s_sum[m][warp][l + 32 * h] = in[h] ? sum[h][m] : 0.f;
-    __syncthreads();
-    float* out = p.dxp + (size_t)part * p.Tp * p.Kx;
-    for (int m = group; m < n_tok; m += 4) {
-      float g = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) g += s_sum[m][e][lane];
-      float* d = out + (size_t)m * p.Kx + c0 + lane;
-      *d = first ? g : *d + g;
-    }
+      j0 += 8 * kChain;
+    } while (j0 < jb);
     return;
   }
   const int j0 = v0 + part * kTile;

@@ -71,3 +71,41 @@ def test_hidden_gradient_over_many_columns():
     off = (out.d_hidden[:8].double() - want) / want
     lost = 2 ** 18 / 16 * 2.0 ** -24
     assert abs(off.mean().item()) < lost + 5 * ROUNDING * (2 / off.numel()) ** 0.5
+
+
+# fp32: chains of up to 4096 additions, then one of the parts.  An addition rounds to nearest, 2^-24
+# of its partial sum at most: 2^-24 / sqrt(3) rms, of a partial sum that is 1 / sqrt(3) of the last
+# (rms); six deviations, and 2^-21 for the gradient of the logits.
+def _chain_bound(n):
+    parts = max(1.0, n / 4096)
+    return 6 * 2.0 ** -24 / 3 * (min(n, 4096) / parts + parts) ** 0.5 + 2.0 ** -21
+
+
+@pytest.mark.parametrize("T", [4000, 70000, 2 ** 20 - 3])
+def test_head_gradient_over_many_rows_f32(T):
+    assert _rows_off(T, torch.float32).abs().max().item() < _chain_bound(T)
+
+
+# (few rows and features: the columns are split among many CTAs; many: hardly; up to 16 rows take
+# other kernels)
+@pytest.mark.parametrize("T,H,V", [(300, 64, 4000), (300, 64, 2 ** 20 + 5), (4100, 256, 2 ** 20 + 5),
+                                   (16, 16384, 2 ** 19 + 3)])
+def test_hidden_gradient_over_many_columns_f32(T, H, V):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(13)
+    w = torch.empty(V, H, device="cuda")
+    for a in range(0, V, 1 << 16):
+        b = min(V, a + (1 << 16))
+        w[a:b] = torch.randn(b - a, H, generator=g, device="cuda").abs() * 0.16 / H ** 0.5
+    w[:4] = 0                                   # the labels' rows: nothing is taken off the sum
+    tio, hidden, cfg, head = _make(T, H, V, torch.float32, g, 1.0, w)
+    out = tio.LossOutputs.allocate(cfg, head, d_lm_head=False)
+    ws = tio.loss_workspace_for(cfg, head, out)
+    labels = torch.randint(4, (T,), generator=g, device="cuda").int()
+    tio.head_loss(cfg, head, hidden, None, labels, out, ws)
+    assert tio.device_status(ws) == 0
+    x = hidden[-64:].double()
+    z = torch.cat([x @ c.double().t() for c in w.split(1 << 16)], 1)
+    q = torch.softmax(z, 1).split(1 << 16, 1)
+    want = sum(a @ c.double() for a, c in zip(q, w.split(1 << 16)))
+    assert ((out.d_hidden[-64:].double() - want) / want).abs().max().item() < _chain_bound(V)
