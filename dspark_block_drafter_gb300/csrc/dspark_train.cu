@@ -2,6 +2,7 @@
 // kernel dispatch.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <string>
 
 #include "../../include/dspark.h"
@@ -17,6 +18,15 @@ static constexpr size_t kAlign = 256;
 static constexpr int kMaxLossRows = 1 << 20;
 
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// Arrays of elements of `size` bytes, NULL where they are absent.
+static dspark_status check_elements(std::initializer_list<const void*> arrays, size_t size) {
+  for (const void* p : arrays)
+    if (!aligned(p, size))
+      return fail(DSPARK_ERR_INVALID_ARG, "an array of " + std::to_string(size) +
+                                              "-byte elements is not aligned to them");
+  return DSPARK_OK;
+}
 
 static dspark_status check_workspace(const void* ws, size_t have, size_t need) {
   if (!ws || !aligned(ws, kAlign))
@@ -65,7 +75,11 @@ static dspark_status validate_loss(const dspark_loss_config* c, const dspark_hea
     if (!aligned(o->d_lm_head, 16) || !aligned(o->d_markov_w1, 16) || !aligned(o->d_markov_w2, 16))
       return fail(DSPARK_ERR_INVALID_ARG, "bf16 weight gradients must be 16-byte aligned");
   }
-  return DSPARK_OK;
+  const dspark_status st =
+      check_elements({h->lm_head, h->markov_w1, h->markov_w2, o->d_hidden, o->d_lm_head,
+                      o->d_markov_w1, o->d_markov_w2}, c->dtype == DSPARK_F32 ? 4 : 2);
+  if (st != DSPARK_OK) return st;
+  return check_elements({h->lm_bias, h->d2t, o->loss, o->total, o->n_rows}, 4);
 }
 
 // Sizes and workspace regions (offsets from `ws`, which is NULL when only the size is
@@ -265,6 +279,9 @@ dspark_status dspark_head_loss(const dspark_loss_config* cfg, const dspark_head*
     return fail(DSPARK_ERR_INVALID_ARG, "hidden, labels and (for r > 0) prev are required");
   if (!out->loss || !out->total)
     return fail(DSPARK_ERR_INVALID_ARG, "outputs loss and total are required");
+  st = check_elements({hidden}, cfg->dtype == DSPARK_F32 ? 4 : 2);
+  if (st == DSPARK_OK) st = check_elements({cfg->r > 0 ? prev : nullptr, labels, weights}, 4);
+  if (st != DSPARK_OK) return st;
   LossPlan p;
   const size_t need = plan_loss(cfg, head, out, (char*)workspace, &p);
   st = check_workspace(workspace, workspace_bytes, need);
@@ -286,6 +303,8 @@ dspark_status dspark_block_norm(const dspark_norm_config* cfg, const void* x, co
   if (st == DSPARK_OK) st = check_norm_inputs(x, y, gate, w_post, w_pre);
   if (st != DSPARK_OK) return st;
   if (!h) return fail(DSPARK_ERR_INVALID_ARG, "h is required");
+  st = check_elements({x, y, gate, w_post, w_pre, x_out, h}, norm_f32(cfg) ? 4 : 2);
+  if (st != DSPARK_OK) return st;
   NormArgs a{};
   fill_norm(cfg, &a);
   a.x = x; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre;
@@ -318,6 +337,9 @@ dspark_status dspark_block_norm_backward(const dspark_norm_config* cfg, const vo
   if (!y != !d_y || !gate != !d_gate || !w_post != !d_w_post)
     return fail(DSPARK_ERR_INVALID_ARG,
                 "d_y, d_gate and d_w_post go with y, gate and w_post: both or neither");
+  st = check_elements({x, y, gate, w_post, w_pre, d_h, d_x_out, d_x, d_y, d_gate, d_w_post, d_w_pre},
+                      norm_f32(cfg) ? 4 : 2);
+  if (st != DSPARK_OK) return st;
   NormArgs a{};
   fill_norm(cfg, &a);
   const size_t need = plan_norm(cfg, (char*)workspace, &a);
@@ -344,6 +366,8 @@ dspark_status dspark_clip_grads(int32_t count, const dspark_grad* grads, float m
   if (st != DSPARK_OK) return st;
   if (!(max_norm >= 0.f)) return fail(DSPARK_ERR_INVALID_ARG, "max_norm must be >= 0");
   if (!norm) return fail(DSPARK_ERR_INVALID_ARG, "norm is required");
+  st = check_elements({norm}, 4);
+  if (st != DSPARK_OK) return st;
   st = check_workspace(workspace, workspace_bytes,
                        align_up(sizeof(float) * clip_partials(count), kAlign));
   if (st != DSPARK_OK) return st;

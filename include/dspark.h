@@ -403,7 +403,8 @@ dspark_status dspark_wait_selftest(void* workspace, size_t workspace_bytes,
  * Training the head.  dspark_block_norm makes the head's inputs from a drafter block's
  * output, dspark_head_loss scores teacher-forced slots and gives the gradients of
  * everything their logits are made of, dspark_block_norm_backward carries them through
- * the norm, and dspark_clip_grads bounds the step.  (The pages describe the head these
+ * the norm, and dspark_clip_grads bounds the step.  Every array is aligned to its elements
+ * at least; a call refuses one that is not.  (The pages describe the head these
  * calls train, not its training: the operators are this library's own.)
  * ------------------------------------------------------------------------------- */
 
