@@ -24,10 +24,11 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, here: Optional[int] = None) -> int:
+    """The stream's handle; None: the current one (of the current GPU, `here` where it is known)."""
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if here is None else here)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -193,6 +194,32 @@ def _checked(name: str, t: Optional[torch.Tensor], shape, dtype) -> Optional[int
     return t.data_ptr()
 
 
+def _here() -> int:
+    """The current GPU, -2 where there is none.  (torch.cuda.current_device takes twice as long.)"""
+    try:
+        return torch._C._cuda_getDevice()
+    except (AttributeError, RuntimeError):
+        return -2
+
+
+def _on_this_gpu(names, *tensors) -> int:
+    """Refuses tensors (None: absent) that are not on the current GPU: the kernels would take their
+    addresses all the same.  Returns the GPU."""
+    here = _here()
+    for t in tensors:
+        if t is not None and t.get_device() != here:         # (-1: not on a GPU)
+            name = [n for n, u in zip(names, tensors) if u is t][0]
+            raise ValueError(f"{name}: need a tensor on the current GPU, got one on {t.device}")
+    return here
+
+
+def _room(workspace: torch.Tensor):
+    """A workspace's address and bytes."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: need a contiguous tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def make_loss_config(T, H, V, r, dtype, reduction="mean", loss_scale=1.0,
                      vocab_pieces=0) -> _abi.dspark_loss_config:
     return _abi.dspark_loss_config(T=T, H=H, V=V, r=r,
@@ -244,22 +271,25 @@ def head_loss(cfg, head: Head, hidden, prev, labels, out: LossOutputs, workspace
     """dspark_head_loss on torch tensors; raises DSparkError on a non-OK status."""
     e, f32, i32 = _TORCH_DT.get(cfg.dtype), torch.float32, torch.int32
     V, r, vh = cfg.V, cfg.r, head.V_head
-    for name, t, shape, dt in (
-            ("lm_head", head.lm_head, (vh, cfg.H), e), ("lm_bias", head.lm_bias, (vh,), f32),
-            ("d2t", head.d2t, (vh,), i32), ("markov_w1", head.markov_w1, (V, r), e),
-            ("markov_w2", head.markov_w2, (r, vh), e), ("loss", out.loss, (cfg.T,), f32),
-            ("total", out.total, (1,), f32), ("n_rows", out.n_rows, (1,), i32),
-            ("d_hidden", out.d_hidden, (cfg.T, cfg.H), e),
-            ("d_lm_head", out.d_lm_head, (vh, cfg.H), e),
-            ("d_markov_w1", out.d_markov_w1, (V, r), e),
-            ("d_markov_w2", out.d_markov_w2, (r, vh), e)):
-        _checked(name, t, shape, dt)
-    _abi.check(_abi.dspark_head_loss(
-        cfg, head.struct(), _checked("hidden", hidden, (cfg.T, cfg.H), e),
-        _checked("prev", prev, (cfg.T,), i32) if r > 0 else None,
-        _checked("labels", labels, (cfg.T,), i32),
-        _checked("weights", weights, (cfg.T,), f32), out.struct(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    tensors = (
+        ("lm_head", head.lm_head, (vh, cfg.H), e), ("lm_bias", head.lm_bias, (vh,), f32),
+        ("d2t", head.d2t, (vh,), i32), ("markov_w1", head.markov_w1, (V, r), e),
+        ("markov_w2", head.markov_w2, (r, vh), e), ("loss", out.loss, (cfg.T,), f32),
+        ("total", out.total, (1,), f32), ("n_rows", out.n_rows, (1,), i32),
+        ("d_hidden", out.d_hidden, (cfg.T, cfg.H), e),
+        ("d_lm_head", out.d_lm_head, (vh, cfg.H), e),
+        ("d_markov_w1", out.d_markov_w1, (V, r), e),
+        ("d_markov_w2", out.d_markov_w2, (r, vh), e))
+    for t in tensors:
+        _checked(*t)
+    prev = prev if r > 0 else None
+    args = (_checked("hidden", hidden, (cfg.T, cfg.H), e), _checked("prev", prev, (cfg.T,), i32),
+            _checked("labels", labels, (cfg.T,), i32), _checked("weights", weights, (cfg.T,), f32))
+    here = _on_this_gpu(
+        [t[0] for t in tensors] + ["hidden", "prev", "labels", "weights", "workspace"],
+        *[t[1] for t in tensors], hidden, prev, labels, weights, workspace)
+    _abi.check(_abi.dspark_head_loss(cfg, head.struct(), *args, out.struct(), *_room(workspace),
+                                     _stream(stream, here)))
 
 
 def make_norm_config(T, H, dtype, eps=1e-6, residual_scale=1.0, weight_offset=0.0,
@@ -304,25 +334,29 @@ def _norm_shapes(cfg):
 def block_norm(cfg, x, y, w_pre, h, x_out=None, gate=None, w_post=None, stream=None) -> None:
     """dspark_block_norm on torch tensors; raises DSparkError on a non-OK status."""
     row, gat, vec, e = _norm_shapes(cfg)
-    _abi.check(_abi.dspark_block_norm(
-        cfg, _checked("x", x, row, e), _checked("y", y, row, e),
-        _checked("gate", gate, gat, e), _checked("w_post", w_post, vec, e),
-        _checked("w_pre", w_pre, vec, e), _checked("x_out", x_out, row, e),
-        _checked("h", h, row, e), _stream(stream)))
+    args = (_checked("x", x, row, e), _checked("y", y, row, e), _checked("gate", gate, gat, e),
+            _checked("w_post", w_post, vec, e), _checked("w_pre", w_pre, vec, e),
+            _checked("x_out", x_out, row, e), _checked("h", h, row, e))
+    here = _on_this_gpu(("x", "y", "gate", "w_post", "w_pre", "x_out", "h"),
+                        x, y, gate, w_post, w_pre, x_out, h)
+    _abi.check(_abi.dspark_block_norm(cfg, *args, _stream(stream, here)))
 
 
 def block_norm_backward(cfg, x, y, w_pre, d_h, out: NormGrads, workspace, d_x_out=None,
                         gate=None, w_post=None, stream=None) -> None:
     """dspark_block_norm_backward on torch tensors; raises DSparkError on a non-OK status."""
     row, gat, vec, e = _norm_shapes(cfg)
-    _abi.check(_abi.dspark_block_norm_backward(
-        cfg, _checked("x", x, row, e), _checked("y", y, row, e),
-        _checked("gate", gate, gat, e), _checked("w_post", w_post, vec, e),
-        _checked("w_pre", w_pre, vec, e), _checked("d_h", d_h, row, e),
-        _checked("d_x_out", d_x_out, row, e), _checked("d_x", out.d_x, row, e),
-        _checked("d_y", out.d_y, row, e), _checked("d_gate", out.d_gate, gat, e),
-        _checked("d_w_post", out.d_w_post, vec, e), _checked("d_w_pre", out.d_w_pre, vec, e),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+    args = (_checked("x", x, row, e), _checked("y", y, row, e), _checked("gate", gate, gat, e),
+            _checked("w_post", w_post, vec, e), _checked("w_pre", w_pre, vec, e),
+            _checked("d_h", d_h, row, e), _checked("d_x_out", d_x_out, row, e),
+            _checked("d_x", out.d_x, row, e), _checked("d_y", out.d_y, row, e),
+            _checked("d_gate", out.d_gate, gat, e), _checked("d_w_post", out.d_w_post, vec, e),
+            _checked("d_w_pre", out.d_w_pre, vec, e))
+    here = _on_this_gpu(
+        ("x", "y", "gate", "w_post", "w_pre", "d_h", "d_x_out", "d_x", "d_y", "d_gate", "d_w_post",
+         "d_w_pre", "workspace"), x, y, gate, w_post, w_pre, d_h, d_x_out, out.d_x, out.d_y,
+        out.d_gate, out.d_w_post, out.d_w_pre, workspace)
+    _abi.check(_abi.dspark_block_norm_backward(cfg, *args, *_room(workspace), _stream(stream, here)))
 
 
 class GradList:
@@ -341,6 +375,7 @@ class GradList:
                 raise ValueError(f"gradient {i}: float32 or bfloat16, not {g.dtype}")
             _checked(f"gradient {i}", g, g.shape, g.dtype)
             _checked(f"outs[{i}]", o, g.shape, g.dtype)
+            _on_this_gpu((f"gradient {i}", f"outs[{i}]"), g, o)
             self.array[i] = _abi.dspark_grad(in_=g.data_ptr(), out=o.data_ptr(), n=g.numel(),
                                              dtype=dt[g.dtype])
 
@@ -357,8 +392,7 @@ def clip_workspace_for(grads: GradList, device="cuda") -> torch.Tensor:
 
 def clip_grads(grads: GradList, max_norm, norm, workspace, stream=None) -> None:
     """dspark_clip_grads on torch tensors; raises DSparkError on a non-OK status."""
-    _abi.check(_abi.dspark_clip_grads(len(grads), grads.array, float(max_norm),
-                                      _checked("norm", norm, (1,), torch.float32),
-                                      workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(),
-                                      _stream(stream)))
+    at = _checked("norm", norm, (1,), torch.float32)
+    here = _on_this_gpu(("norm", "workspace"), norm, workspace)
+    _abi.check(_abi.dspark_clip_grads(len(grads), grads.array, float(max_norm), at,
+                                      *_room(workspace), _stream(stream, here)))
