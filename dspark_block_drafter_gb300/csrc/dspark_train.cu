@@ -16,6 +16,10 @@ namespace dspark {
 
 static constexpr size_t kAlign = 256;
 static constexpr int kMaxLossRows = 1 << 20;
+// bf16: room for the partial gradients of X, where one for every row takes less.  With 4352 columns
+// of X, up to 5120 rows with a loss choose among all splits; more rows fill the GPU with fewer (by
+// the choice's own estimate at most 4% of dX is lost, and the room no longer grows sixfold with T).
+static constexpr size_t kDxBytes = (size_t)1 << 29;
 
 static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -148,7 +152,12 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
     if (p->d_hidden || p->d_w1) {
       p->splits = tc ? loss_tc_splits(p->T, p->d_hidden ? p->Hp : 0, p->d_w1 ? p->rp : 0)
                      : loss_simt_splits(p->T, p->Kx, p->piece_cols);
-      p->dxp = (float*)take(sizeof(float) * p->splits * Tp * p->Kx);
+      p->dx_rows = Tp * p->splits;
+      if (tc) {
+        const size_t room = kDxBytes / (sizeof(float) * p->Kx) / 256 * 256;
+        p->dx_rows = std::min(p->dx_rows, std::max(Tp, room));
+      }
+      p->dxp = (float*)take(sizeof(float) * p->dx_rows * p->Kx);
     }
   }
   auto zero = [&](void* g, size_t bytes, const int32_t* keep, size_t row_bytes, bool early) {

@@ -157,9 +157,10 @@ __device__ __forceinline__ int loss_pick_splits(const LossPlan& p, int n_tok, in
   const int ctas = pairs ? 76 : 152, nkb = (cols + 63) / 64;
   const int n_dw = pairs ? (cols + 255) / 256 * ((p.d_lm_head ? head : 0) + (p.d_w2 ? markov : 0)) : 0;
   const float dw = (float)n_dw * fmaxf((float)((n_tok + 63) / 64) + 2.f, 11.f);
+  const int most = (int)min((size_t)p.splits, p.dx_rows / loss_split_rows(n_tok));
   float cost = INFINITY;
   int best = 1;
-  for (int s = 1 + lane; s <= p.splits && (s == 1 || s * 8 <= nkb); s += 32) {
+  for (int s = 1 + lane; s <= most && (s == 1 || s * 8 <= nkb); s += 32) {
     const float unit = (float)nkb / (float)s + 12.f;
     const float waves = (float)((tiles * s + ctas - 1) / ctas) * unit;
     const float even = ((float)(tiles * s) * unit + dw) / (float)ctas;
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
   const int i = blockIdx.x;
   if (i >= (int)p.ctrl[kLossTok]) return;
   const float k = __uint_as_float(p.ctrl[kLossScale]);
-  const size_t step = (size_t)p.Tp * p.Kx / 4;
+  const size_t step = (size_t)loss_split_rows((int)p.ctrl[kLossTok]) * p.Kx / 4;
   const int splits = (int)p.ctrl[kLossSplits];
   float4* x = (float4*)(p.dxp + (size_t)i * p.Kx);
   const float lost = p.qres ? p.qres[i] : 0.f;

@@ -254,7 +254,7 @@ __device__ __forceinline__ void dx_tile(const LossPlan& p, int v0, int v1, bool 
   const float* w2 = (const float*)p.w2;
   const bool head = c0 < p.Hp;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float* dx = p.dxp + (size_t)bz * p.Tp * p.Kx;
+  float* dx = p.dxp + (size_t)bz * loss_split_rows(n_tok) * p.Kx;
   int j0 = ja;
   do {                                        // (an empty range writes zeros)
     const int j1 = min(jb, j0 + kChain);
@@ -380,7 +380,7 @@ loss_grads_few(const LossPlan p, int v0, int v1, bool first, int n_dx) {
       at[h] = in[h] ? (head ? (size_t)c : (size_t)c * p.Vh) : 0;
     }
     float(*s_sum)[8][kTile] = reinterpret_cast<float(*)[8][kTile]>(smem);   // [NT]
-    float* out = p.dxp + (size_t)part * p.Tp * p.Kx;
+    float* out = p.dxp + (size_t)part * loss_split_rows(n_tok) * p.Kx;
     int j0 = ja;
     do {                                      // (an empty range writes zeros)
       const int end = min(jb, j0 + 8 * kChain);

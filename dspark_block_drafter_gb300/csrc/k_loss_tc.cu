@@ -644,7 +644,7 @@ loss_product(const __grid_constant__ Maps maps, const __grid_constant__ TcArgs g
         const int c0 = t.c0 + half * 128;
         if (MODE == kDx || (MODE == kGrads && !t.dw)) {
           const int width = min(128, (markov ? p.Kx : p.Hp) - c0);
-          float* dx = p.dxp + ((size_t)t.split * p.Tp + m) * p.Kx + c0;
+          float* dx = p.dxp + ((size_t)t.split * loss_split_rows(n_tok) + m) * p.Kx + c0;
           bool add = !g.first;
           for (int kb = t.kb0, end; ok; kb = end, add = true) {
             end = part_end(t, kb);

@@ -70,8 +70,9 @@ struct LossPlan {
   size_t ldq;
   int pieces, piece_cols;             // pieces of the vocabulary, columns of each
   float* qres;                        // [Tp] bf16: what rounding the label's entry of q lost
-  float* dxp;                         // [splits][Tp][Kx] partial gradients of X
+  float* dxp;                         // [splits][loss_split_rows][Kx] partial gradients of X
   int splits;                         // the most; fp32: what is used
+  size_t dx_rows;                     // rows that dxp has room for, over all splits
   bool grads;                         // any gradient asked for
   LossZero zero[3];
   int n_zero;
@@ -102,6 +103,9 @@ __device__ __forceinline__ void loss_put_label(const LossPlan& p, int i, bool lo
 __device__ __forceinline__ bool loss_low(const LossPlan& p, int n_tok) {
   return p.dtype == 1 && p.T <= 2 * kLossLow && n_tok <= kLossLow;
 }
+
+// Rows of one split's part of dxp.
+__device__ __forceinline__ int loss_split_rows(int n_tok) { return max(256, (n_tok + 255) / 256 * 256); }
 
 // compact -> head row, for kernels that read the head's own arrays
 __device__ __forceinline__ int loss_head_row(const LossPlan& p, int j) {

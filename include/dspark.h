@@ -427,7 +427,10 @@ typedef struct dspark_loss_config {
                             (2 bytes each for bf16, 4 for fp32); with more, only a piece's
                             are held, and each piece's logits are computed a second time.
                             At most ceil(V_head / 256) pieces are made.  No effect when no
-                            gradient is asked for: nothing is kept then. */
+                            gradient is asked for: nothing is kept then.  Besides, the rows
+                            of [hidden | markov_w1[prev]] are held once in dtype and, for
+                            d_hidden or d_markov_w1, in fp32 at least once (in bf16 up to
+                            512 MB of partial sums where once takes less). */
   float loss_scale;      /* factor of the total and of every gradient; finite */
 } dspark_loss_config;
 
