@@ -696,7 +696,9 @@ __global__ void __launch_bounds__(256) loss_dx_rows(const LossPlan p) {
 // prev in row order, each warp over its share of the rows, the warps in order.  A warp looks
 // at 128 rows at a time and adds two of them at a time, in registers: common tokens precede many
 // rows.  (4096 rows, rank 256: 18 us, with seven different prev 40; one row at a time into shared
-// memory 49 and 129.)
+// memory 49 and 129.)  Sums of more than kW1Chain rows are sums of such parts: one chain of 131072
+// fp32 additions a warp was off by 4e-6.
+constexpr int kW1Chain = 4096;
 template <typename E>
 __global__ void __launch_bounds__(256) loss_w1_rows(const LossPlan p) {
   pdl_wait();
@@ -720,8 +722,15 @@ __global__ void __launch_bounds__(256) loss_w1_rows(const LossPlan p) {
   const int j0 = i + warp * share, j1 = min(n_tok, j0 + share);
   int* list = s_list[warp];
   for (int c0 = lane; c0 < p.rp; c0 += 256) {          // (256 columns at a time)
-    float acc[8] = {};
+    float acc[8] = {}, sum[8] = {};
     for (int jb = j0; jb < j1; jb += 128) {
+      if (jb > j0 && (jb - j0) % kW1Chain == 0) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          sum[q] += acc[q];
+          acc[q] = 0.f;
+        }
+      }
       bool hit[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -752,7 +761,7 @@ __global__ void __launch_bounds__(256) loss_w1_rows(const LossPlan p) {
     }
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      if (c0 + 32 * q < p.rp) s_acc[(size_t)warp * p.rp + c0 + 32 * q] = acc[q];
+      if (c0 + 32 * q < p.rp) s_acc[(size_t)warp * p.rp + c0 + 32 * q] = sum[q] + acc[q];
   }
   __syncthreads();
   for (int c = tid; c < p.r; c += blockDim.x) {

@@ -109,3 +109,27 @@ def test_hidden_gradient_over_many_columns_f32(T, H, V):
     q = torch.softmax(z, 1).split(1 << 16, 1)
     want = sum(a @ c.double() for a, c in zip(q, w.split(1 << 16)))
     assert ((out.d_hidden[-64:].double() - want) / want).abs().max().item() < _chain_bound(V)
+
+
+@pytest.mark.parametrize("T", [4000, 2 ** 20 - 3])
+def test_markov_gradient_of_one_prev_over_many_rows_f32(T):
+    """markov_w1's row of the token before every slot: eight chains of rows, joined."""
+    from dspark_block_drafter_gb300 import torch_io as tio
+    H, V, r = 16, 64, 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(14)
+    hidden = torch.randn(T, H, generator=g, device="cuda")
+    w, w1 = (torch.randn(V, n, generator=g, device="cuda") * 0.1 for n in (H, r))
+    w2 = torch.rand(r, V, generator=g, device="cuda") + 0.1
+    w2[:, :4] = 0                               # the labels' columns: nothing is taken off the sum
+    labels = torch.randint(4, (T,), generator=g, device="cuda").int()
+    prev = torch.full((T,), 7, device="cuda", dtype=torch.int32)
+    head = tio.Head(w, w1, w2)
+    cfg = tio.make_loss_config(T, H, V, r, "f32", reduction="sum")
+    out = tio.LossOutputs.allocate(cfg, head, d_hidden=False, d_lm_head=False)
+    ws = tio.loss_workspace_for(cfg, head, out)
+    tio.head_loss(cfg, head, hidden, prev, labels, out, ws)
+    assert tio.device_status(ws) == 0
+    z = hidden.double() @ w.double().t() + (w1[7].double() @ w2.double())[None]
+    want = (torch.softmax(z, 1) @ w2.double().t()).sum(0)
+    assert ((out.d_markov_w1[7].double() - want) / want).abs().max().item() < _chain_bound(T / 8)
