@@ -593,7 +593,8 @@ __global__ void __launch_bounds__(1024) column_sums(const float* part, int rows,
   (blockIdx.y == 0 ? out0 : out1)[c] = (E)a;
 }
 
-// d_gate rows of shared gate rows, from their parts in order.
+// d_gate rows of shared gate rows, from their parts in order: 256 of them at a time, then those sums
+// (one chain over 65536 parts was off by 8e-6).
 template <typename E>
 __global__ void __launch_bounds__(128) gate_sums(const float* part, int per_span, int H, E* out) {
   pdl_wait();
@@ -602,8 +603,13 @@ __global__ void __launch_bounds__(128) gate_sums(const float* part, int per_span
   if (c >= H) return;
   const float* p = part + (size_t)blockIdx.x * per_span * H + c;
   float a = 0.f;
+  for (int j0 = 0; j0 < per_span; j0 += 256) {
+    const int j1 = min(per_span, j0 + 256);
+    float part_sum = 0.f;
 #pragma unroll 8
-  for (int j = 0; j < per_span; ++j) a += p[(size_t)j * H];
+    for (int j = j0; j < j1; ++j) part_sum += p[(size_t)j * H];
+    a += part_sum;
+  }
   out[(size_t)blockIdx.x * H + c] = (E)a;
 }
 

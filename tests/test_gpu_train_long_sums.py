@@ -133,3 +133,23 @@ def test_markov_gradient_of_one_prev_over_many_rows_f32(T):
     z = hidden.double() @ w.double().t() + (w1[7].double() @ w2.double())[None]
     want = (torch.softmax(z, 1) @ w2.double().t()).sum(0)
     assert ((out.d_markov_w1[7].double() - want) / want).abs().max().item() < _chain_bound(T / 8)
+
+
+@pytest.mark.parametrize("T", [4000, 2 ** 20 - 3])
+def test_gate_gradient_over_many_rows_f32(T):
+    """One gate row for every row, and no gradient of h: d_gate = s sum d_x_out y."""
+    from dspark_block_drafter_gb300 import torch_io as tio
+    H = 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(15)
+    x, y, up = (torch.rand(T, H, generator=g, device="cuda") + 0.1 for _ in range(3))
+    gate, w = torch.ones(1, H, device="cuda"), torch.ones(H, device="cuda")
+    cfg = tio.make_norm_config(T, H, "f32", gate_span=T)
+    out = tio.NormGrads.allocate(cfg, w_post=False)
+    tio.block_norm_backward(cfg, x, y, w, torch.zeros_like(x), out, tio.norm_workspace_for(cfg),
+                            d_x_out=up, gate=gate)
+    want = (up.double() * y.double()).sum(0)
+    # chains of 16 rows, of 256 of those, and of the rest
+    rest = max(1.0, T / 4096)
+    bound = 6 * 2.0 ** -24 / 3 * (16 + 256 + rest) ** 0.5 + 2.0 ** -23
+    assert ((out.d_gate[0].double() - want) / want).abs().max().item() < bound
