@@ -32,6 +32,11 @@
 // every 1024 K-blocks, and dW sums more than 256 K-blocks in registers, in a kernel of its own
 // (the registers cost the common case spills): a loss of 1e-4 in dW and 4e-4 in dX at most.
 //
+// 352 threads leave 168 registers each.  The logits' epilogue holds its 128 sums in them and spills a
+// few others once a tile (single CTAs 60 words a thread, pairs 20; dX and dW in one launch 14, of more
+// than 16384 rows 60): next to a tile's K loop, some thousand cycles, that does not show (without
+// its 14 the joint launch takes the same 10.26 ms at 4096 rows).
+//
 // The logits are never stored.  Their epilogue has one row per thread: it takes the maximum
 // and the sum of exponentials of each 128-column tile, the label's column aside, and, when
 // gradients follow, stores how far each logit lies below its tile's maximum as a 16-bit
@@ -907,8 +912,8 @@ cudaError_t launch_loss_logits_tc(const LossPlan& p, int v0, int v1, bool stats,
 }
 
 // The two gradient products of columns [v0, v1), in one launch of pairs where both are asked
-// for: alone, each leaves pairs without work at its end (frozen 512-row case 957 -> 935 us, four
-// pieces of 1001 rows 507 -> 446 us).
+// for: alone, each leaves pairs without work at its end (four pieces of 1001 rows 493 -> 421 us for
+// the whole call; the frozen head with 512 rows 1050 us, 4096 rows 9.8 ms, either way).
 cudaError_t launch_loss_grads_tc(const LossPlan& p, int v0, int v1, bool first) {
   TcArgs g{};
   g.p = p;

@@ -98,8 +98,10 @@ __device__ __forceinline__ void loss_put_label(const LossPlan& p, int i, bool lo
 }
 
 // bf16, up to kLossLow compact rows: row kLossLow + i of q holds what rounding row i of it lost
-// (and row kLossLow + i of X is row i again), so that the gradient products see q with 16 bits.
-// Few rows do not average their roundings out, and within one 128-row tile this costs nothing.
+// (and row kLossLow + i of X is row i again), so that the gradient products see q with 16 bits:
+// its label's entry and, with several pieces, all of it; with one piece the other entries come
+// from the kept distances and are good to 11 bits.  Few rows do not average their roundings out,
+// and within one 128-row tile this costs nothing.
 __device__ __forceinline__ bool loss_low(const LossPlan& p, int n_tok) {
   return p.dtype == 1 && p.T <= 2 * kLossLow && n_tok <= kLossLow;
 }

@@ -476,10 +476,18 @@ size_t dspark_head_loss_workspace_size(const dspark_loss_config* cfg,
  * row with a loss, drops the row and raises the error word (dspark_device_status).
  *
  * bf16: products on the tensor cores with fp32 accumulation; the softmax statistics,
- * losses and sums are fp32; the gradient of the logits is rounded to bf16 before the
- * gradient products (d_hidden and d_markov_w1 get back what the label's entry lost), each
- * gradient once on output.  No atomics decide an order of summation: the same call gives
- * the same bits.  Not reentrant on one workspace.  Can be captured into a CUDA graph.
+ * losses and sums are fp32.  With the vocabulary in one piece the logits are kept as 16-bit
+ * distances from a maximum, in steps of 1/896: a probability in the gradient is off by at
+ * most 0.06% (with several pieces they are computed again, and are not).  The gradient of the
+ * logits is rounded to bf16 before the gradient products; d_hidden and d_markov_w1 get back
+ * what the label's entry lost, and when at most 64 of at most 128 rows carry a loss every
+ * entry's rounding is carried along.  Each gradient is rounded once more on output.
+ *
+ * A row whose logits are not all numbers (or are +infinity) has NaN in its loss and its
+ * gradients, and so have the total and the weights' gradients.  No atomics decide an order of
+ * summation: the same call gives the same bits.  d_markov_w1 compares every row's prev with
+ * the earlier ones': with T^2 (0.2 s at 2^20 rows, all different).  Not reentrant on one
+ * workspace.  Can be captured into a CUDA graph.
  */
 dspark_status dspark_head_loss(const dspark_loss_config* cfg, const dspark_head* head,
                                const void* hidden, const int32_t* prev,
