@@ -66,6 +66,26 @@ class dspark_grad(ctypes.Structure):
     _fields_ = [("in_", c_ptr), ("out", c_ptr), ("n", ctypes.c_int64), ("dtype", c_i32)]
 
 
+class dspark_teacher(ctypes.Structure):
+    _fields_ = [("ids", c_ptr), ("logits", c_ptr), ("lse", c_ptr), ("k", c_i32),
+                ("scale", ctypes.c_float)]
+
+
+class dspark_sample_config(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("V", c_i32), ("ld", ctypes.c_int64), ("dtype", c_i32),
+                ("top_k", c_i32), ("temperature", ctypes.c_float), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float)]
+
+
+class dspark_sample_rows(ctypes.Structure):
+    _fields_ = [("top_k", c_ptr), ("temperature", c_ptr), ("top_p", c_ptr), ("min_p", c_ptr)]
+
+
+class dspark_embed_config(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("V", c_i32), ("H", c_i32), ("dtype", c_i32),
+                ("scale", ctypes.c_float)]
+
+
 class DSparkError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"dspark status {status}: {message}")
@@ -123,6 +143,21 @@ SIGNATURES = {
     "dspark_clip_grads_workspace_size": (ctypes.c_size_t, [c_i32, ctypes.POINTER(dspark_grad)]),
     "dspark_clip_grads": (c_i32, [c_i32, ctypes.POINTER(dspark_grad), ctypes.c_float, c_ptr,
                                   c_ptr, ctypes.c_size_t, c_ptr]),
+    "dspark_distill_loss_workspace_size": (ctypes.c_size_t, [
+        ctypes.POINTER(dspark_loss_config), ctypes.POINTER(dspark_head),
+        ctypes.POINTER(dspark_teacher), ctypes.POINTER(dspark_loss_outputs)]),
+    "dspark_distill_loss": (c_i32, [ctypes.POINTER(dspark_loss_config),
+                                    ctypes.POINTER(dspark_head), c_ptr, c_ptr,
+                                    ctypes.POINTER(dspark_teacher), c_ptr,
+                                    ctypes.POINTER(dspark_loss_outputs), c_ptr,
+                                    ctypes.c_size_t, c_ptr]),
+    "dspark_sample": (c_i32, [ctypes.POINTER(dspark_sample_config),
+                              ctypes.POINTER(dspark_sample_rows)] + [c_ptr] * 5),
+    "dspark_top_logits": (c_i32, [c_i32, c_i32, ctypes.c_int64, c_i32, c_i32] + [c_ptr] * 5),
+    "dspark_embed": (c_i32, [ctypes.POINTER(dspark_embed_config)] + [c_ptr] * 4),
+    "dspark_embed_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(dspark_embed_config)]),
+    "dspark_embed_backward": (c_i32, [ctypes.POINTER(dspark_embed_config)] + [c_ptr] * 5
+                              + [ctypes.c_size_t, c_ptr]),
     "dspark_status_string": (ctypes.c_char_p, [c_i32]),
     "dspark_last_error": (ctypes.c_char_p, []),
 }
@@ -303,6 +338,49 @@ def dspark_clip_grads(count: int, grads, max_norm: float, norm: int, workspace: 
                       workspace_bytes: int, stream: int = 0) -> int:
     return lib().dspark_clip_grads(count, grads, max_norm, norm, workspace, workspace_bytes,
                                    stream)
+
+
+def dspark_distill_loss_workspace_size(cfg: dspark_loss_config, head: dspark_head,
+                                       teacher: dspark_teacher,
+                                       out: dspark_loss_outputs) -> int:
+    return lib().dspark_distill_loss_workspace_size(ctypes.byref(cfg), ctypes.byref(head),
+                                                    ctypes.byref(teacher), ctypes.byref(out))
+
+
+def dspark_distill_loss(cfg: dspark_loss_config, head: dspark_head, hidden: int,
+                        prev: int | None, teacher: dspark_teacher, weights: int | None,
+                        out: dspark_loss_outputs, workspace: int, workspace_bytes: int,
+                        stream: int = 0) -> int:
+    return lib().dspark_distill_loss(ctypes.byref(cfg), ctypes.byref(head), hidden, prev,
+                                     ctypes.byref(teacher), weights, ctypes.byref(out),
+                                     workspace, workspace_bytes, stream)
+
+
+def dspark_sample(cfg: dspark_sample_config, rows: dspark_sample_rows | None, logits: int,
+                  uniform: int, tokens: int, logp: int | None, stream: int = 0) -> int:
+    return lib().dspark_sample(ctypes.byref(cfg), None if rows is None else ctypes.byref(rows),
+                               logits, uniform, tokens, logp, stream)
+
+
+def dspark_top_logits(T: int, V: int, ld: int, dtype: int, k: int, logits: int, ids: int,
+                      values: int, lse: int | None, stream: int = 0) -> int:
+    return lib().dspark_top_logits(T, V, ld, dtype, k, logits, ids, values, lse, stream)
+
+
+def dspark_embed(cfg: dspark_embed_config, table: int, ids: int, out: int,
+                 stream: int = 0) -> int:
+    return lib().dspark_embed(ctypes.byref(cfg), table, ids, out, stream)
+
+
+def dspark_embed_workspace_size(cfg: dspark_embed_config) -> int:
+    return lib().dspark_embed_workspace_size(ctypes.byref(cfg))
+
+
+def dspark_embed_backward(cfg: dspark_embed_config, ids: int, d_out: int, add: int | None,
+                          d_table: int, workspace: int, workspace_bytes: int,
+                          stream: int = 0) -> int:
+    return lib().dspark_embed_backward(ctypes.byref(cfg), ids, d_out, add, d_table, workspace,
+                                       workspace_bytes, stream)
 
 
 def dspark_status_string(status: int) -> str:

@@ -7,6 +7,7 @@
 
 #include "../../include/dspark.h"
 #include "common.cuh"
+#include "distill.h"
 #include "kernels.h"
 #include "loss.h"
 #include "status.h"
@@ -172,24 +173,64 @@ static size_t plan_loss(const dspark_loss_config* c, const dspark_head* h,
   return off;
 }
 
-static cudaError_t run_loss(const LossPlan& p) {
+// d: the teacher's listed tokens in the labels' place, or NULL.
+static cudaError_t run_loss(const LossPlan& p, const DistillPlan* d) {
   const bool tc = p.dtype == DSPARK_BF16;
   const auto logits = tc ? launch_loss_logits_tc : launch_loss_logits_simt;
   const auto grads = tc ? launch_loss_grads_tc : launch_loss_grads_simt;
-  cudaError_t e = launch_loss_plan(p);
+  cudaError_t e = d ? launch_distill_targets(*d) : cudaSuccess;
+  if (e == cudaSuccess) e = launch_loss_plan(p);
+  if (e == cudaSuccess && d) e = launch_distill_logits(*d);
   if (e != cudaSuccess) return e;
   const bool keep = p.grads && p.pieces == 1;
   e = logits(p, 0, p.Vh, true, keep);
   if (e == cudaSuccess) e = launch_loss_rows(p, keep);
+  if (e == cudaSuccess && d) e = launch_distill_loss(*d);
   if (e != cudaSuccess || !p.grads) return e;
   for (int c = 0; c < p.pieces; ++c) {
     const int v0 = c * p.piece_cols, v1 = std::min(p.Vh, v0 + p.piece_cols);
     if (!keep) e = logits(p, v0, v1, false, true);
     if (e == cudaSuccess && !keep && !tc) e = launch_loss_dz_f32(p, v0, v1);
+    if (e == cudaSuccess && d) e = launch_distill_entries(*d, v0, v1);
     if (e == cudaSuccess) e = grads(p, v0, v1, c == 0);
     if (e != cudaSuccess) return e;
   }
   return p.dxp ? launch_loss_dx(p) : cudaSuccess;
+}
+
+// ------------------------------------------------------------------ distillation
+static dspark_status validate_teacher(const dspark_teacher* t) {
+  if (!t) return fail(DSPARK_ERR_INVALID_ARG, "teacher is NULL");
+  if (t->k < 1) return fail(DSPARK_ERR_INVALID_ARG, "the teacher lists no tokens (k < 1)");
+  if (!std::isfinite(t->scale))
+    return fail(DSPARK_ERR_INVALID_ARG, "the teacher's scale must be finite");
+  if (t->k > kMaxTargets)
+    return fail(DSPARK_ERR_UNSUPPORTED,
+                "more than " + std::to_string(kMaxTargets) + " listed tokens a row");
+  return DSPARK_OK;
+}
+
+// The head loss's workspace with the teacher's behind it.
+static size_t plan_distill(const dspark_loss_config* c, const dspark_head* h,
+                           const dspark_teacher* t, const dspark_loss_outputs* o, char* ws,
+                           DistillPlan* d) {
+  *d = DistillPlan{};
+  size_t off = plan_loss(c, h, o, ws, &d->p);
+  auto take = [&](size_t bytes) {
+    char* at = ws + off;
+    off = align_up(off + bytes, kAlign);
+    return (void*)at;
+  };
+  const size_t T = (size_t)c->T, Tp = (size_t)d->p.Tp, k = (size_t)t->k;
+  d->k = t->k;
+  d->scale = t->scale;
+  d->label = (int32_t*)take(4 * T);
+  d->row = (int32_t*)take(4 * T * k);
+  d->log_q = (float*)take(4 * T * k);
+  d->mass = (float*)take(4 * T);
+  d->z = (float*)take(4 * Tp * k);
+  d->w = (float*)take(4 * Tp);
+  return off;
 }
 
 // ------------------------------------------------------------------ block norm
@@ -266,6 +307,7 @@ using namespace dspark;
 
 static_assert(sizeof(dspark_loss_config) == 32, "dspark_loss_config layout");
 static_assert(sizeof(dspark_loss_outputs) == 56, "dspark_loss_outputs layout");
+static_assert(sizeof(dspark_teacher) == 32, "dspark_teacher layout");
 static_assert(sizeof(dspark_norm_config) == 28, "dspark_norm_config layout");
 static_assert(sizeof(dspark_grad) == 32, "dspark_grad layout");
 
@@ -300,8 +342,54 @@ dspark_status dspark_head_loss(const dspark_loss_config* cfg, const dspark_head*
   p.labels = labels;
   p.weights = weights;
   p.stream = (cudaStream_t)stream;
-  const cudaError_t e = run_loss(p);
+  const cudaError_t e = run_loss(p, nullptr);
   if (e != cudaSuccess) return cuda_fail(e, "head loss");
+  return DSPARK_OK;
+}
+
+size_t dspark_distill_loss_workspace_size(const dspark_loss_config* cfg,
+                                          const dspark_head* head,
+                                          const dspark_teacher* teacher,
+                                          const dspark_loss_outputs* out) {
+  if (validate_loss(cfg, head, out) != DSPARK_OK || validate_teacher(teacher) != DSPARK_OK)
+    return 0;
+  DistillPlan d;
+  return plan_distill(cfg, head, teacher, out, nullptr, &d);
+}
+
+dspark_status dspark_distill_loss(const dspark_loss_config* cfg, const dspark_head* head,
+                                  const void* hidden, const int32_t* prev,
+                                  const dspark_teacher* teacher, const float* weights,
+                                  const dspark_loss_outputs* out, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  dspark_status st = validate_loss(cfg, head, out);
+  if (st == DSPARK_OK) st = validate_teacher(teacher);
+  if (st != DSPARK_OK) return st;
+  if (!hidden || (cfg->r > 0 && !prev))
+    return fail(DSPARK_ERR_INVALID_ARG, "hidden and (for r > 0) prev are required");
+  if (!teacher->ids || !teacher->logits)
+    return fail(DSPARK_ERR_INVALID_ARG, "the teacher's ids and logits are required");
+  if (!out->loss || !out->total)
+    return fail(DSPARK_ERR_INVALID_ARG, "outputs loss and total are required");
+  st = check_elements({hidden}, cfg->dtype == DSPARK_F32 ? 4 : 2);
+  if (st == DSPARK_OK)
+    st = check_elements({cfg->r > 0 ? prev : nullptr, weights, teacher->ids, teacher->logits,
+                         teacher->lse}, 4);
+  if (st != DSPARK_OK) return st;
+  DistillPlan d;
+  const size_t need = plan_distill(cfg, head, teacher, out, (char*)workspace, &d);
+  st = check_workspace(workspace, workspace_bytes, need);
+  if (st != DSPARK_OK) return st;
+  d.ids = teacher->ids;
+  d.logits = teacher->logits;
+  d.t_lse = teacher->lse;
+  d.p.hidden = hidden;
+  d.p.prev = prev;
+  d.p.labels = d.label;
+  d.p.weights = weights;
+  d.p.stream = (cudaStream_t)stream;
+  const cudaError_t e = run_loss(d.p, &d);
+  if (e != cudaSuccess) return cuda_fail(e, "distillation loss");
   return DSPARK_OK;
 }
 

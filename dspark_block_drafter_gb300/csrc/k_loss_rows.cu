@@ -14,6 +14,7 @@
 #include "kernels.h"
 #include "launch.h"
 #include "loss.h"
+#include "loss_sum.cuh"
 
 namespace dspark {
 
@@ -28,49 +29,6 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16(x);
-}
-
-// An fp32 sum that carries its rounding errors along (Knuth's two-sum).
-struct Sum2 {
-  float s = 0.f, c = 0.f;
-  __device__ __forceinline__ void add(float x) {
-    const float t = s + x, b = t - s;
-    c += (s - (t - b)) + (x - b);
-    s = t;
-  }
-  __device__ __forceinline__ void add(const Sum2& o) {
-    add(o.s);
-    c += o.c;
-  }
-  __device__ __forceinline__ float value() const { return s + c; }
-};
-
-__device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sum2 u;
-    u.s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o);
-    u.c = __shfl_xor_sync(0xFFFFFFFFu, v.c, o);
-    v.add(u);
-  }
-  return v;
-}
-
-// Sum over a CTA, in a fixed order; lane 0 of warp 0 gets it.
-__device__ __forceinline__ Sum2 block_sum(Sum2 v, float2* s_warp) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
-  v = warp_sum(v);
-  if (lane == 0) s_warp[warp] = make_float2(v.s, v.c);
-  __syncthreads();
-  Sum2 u;
-  if (warp == 0) {
-    if (lane < warps) {
-      u.s = s_warp[lane].x;
-      u.c = s_warp[lane].y;
-    }
-    u = warp_sum(u);
-  }
-  return u;
 }
 
 // Copies n elements, sixteen bytes at a time where both sides allow it.
@@ -122,21 +80,8 @@ __global__ void __launch_bounds__(256) loss_vocab(const LossPlan p, int chunks) 
 __device__ __forceinline__ int loss_label_row(const LossPlan& p, int t) {
   int row = t;
   if (p.d2t) {
-    // first entry >= t: seven probes at a time, since each is a trip to memory
-    int lo = 0, hi = p.Vh;
-    while (hi > lo) {
-      const int n = hi - lo;
-      int above = 0;                              // probes whose entry is below t
-#pragma unroll
-      for (int q = 1; q < 8; ++q) above += p.d2t[lo + (int)((long long)n * q / 8)] < t;
-      // entries lo + n q / 8 (q <= above) are below t, the next one is not
-      const int l = lo, h = hi;
-      if (above > 0) lo = l + (int)((long long)n * above / 8) + 1;
-      if (above < 7) hi = l + (int)((long long)n * (above + 1) / 8);
-      else hi = h;
-    }
-    if (lo >= p.Vh || p.d2t[lo] != t) return -1;
-    row = lo;
+    row = loss_d2t_row(p.d2t, p.Vh, t);
+    if (row < 0) return -1;
   }
   return p.vinv ? p.vinv[row] : row;
 }
@@ -550,25 +495,7 @@ __global__ void __launch_bounds__(kRowsThreads) loss_rows(const LossPlan p) {
   __syncthreads();
   if (s_last) {
     __threadfence();
-    Sum2 a;
-    constexpr int kAt = 8;                    // (rows of a thread at once)
-    for (int j0 = tid; j0 < n_tok; j0 += kAt * kRowsThreads) {
-      float w[kAt], x[kAt];
-#pragma unroll
-      for (int q = 0; q < kAt; ++q) {
-        const int j = j0 + q * kRowsThreads;
-        w[q] = j < n_tok ? p.wrow[j] : 0.f;
-        x[q] = j < n_tok ? __ldcg(p.loss + p.tok[j]) : 0.f;
-      }
-#pragma unroll
-      for (int q = 0; q < kAt; ++q) {
-        // the product's rounding error goes into the sum too
-        const float y = w[q] * x[q];
-        a.add(y);
-        a.c += fmaf(w[q], x[q], -y);
-      }
-    }
-    const Sum2 t = block_sum(a, s_w);
+    const Sum2 t = loss_total<kRowsThreads>(p, p.wrow, n_tok, s_w);
     if (tid == 0) *p.total = n_tok > 0 ? __uint_as_float(p.ctrl[kLossScale]) * t.value() : 0.f;
   }
 }

@@ -292,6 +292,59 @@ def head_loss(cfg, head: Head, hidden, prev, labels, out: LossOutputs, workspace
                                      _stream(stream, here)))
 
 
+@dataclasses.dataclass
+class Teacher:
+    """What a teacher says of every row: listed tokens and their logits (see top_logits), its
+    log-sum-exp or None, and the factor of its logits."""
+    ids: torch.Tensor
+    logits: torch.Tensor
+    lse: Optional[torch.Tensor] = None
+    scale: float = 1.0
+
+    def struct(self) -> _abi.dspark_teacher:
+        return _abi.dspark_teacher(ids=_ptr(self.ids), logits=_ptr(self.logits),
+                                   lse=_ptr(self.lse), k=self.ids.shape[-1],
+                                   scale=float(self.scale))
+
+
+def distill_workspace_for(cfg, head: Head, teacher: Teacher, out: LossOutputs,
+                          device="cuda") -> torch.Tensor:
+    n = _abi.dspark_distill_loss_workspace_size(cfg, head.struct(), teacher.struct(),
+                                                out.struct())
+    if n == 0:
+        _abi.check(_abi.DSPARK_ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def distill_loss(cfg, head: Head, teacher: Teacher, hidden, prev, out: LossOutputs, workspace,
+                 weights=None, stream=None) -> None:
+    """dspark_distill_loss on torch tensors; raises DSparkError on a non-OK status."""
+    e, f32, i32 = _TORCH_DT.get(cfg.dtype), torch.float32, torch.int32
+    V, r, vh = cfg.V, cfg.r, head.V_head
+    listed = (cfg.T, teacher.ids.shape[-1] if teacher.ids.dim() == 2 else 0)
+    tensors = (
+        ("lm_head", head.lm_head, (vh, cfg.H), e), ("lm_bias", head.lm_bias, (vh,), f32),
+        ("d2t", head.d2t, (vh,), i32), ("markov_w1", head.markov_w1, (V, r), e),
+        ("markov_w2", head.markov_w2, (r, vh), e), ("loss", out.loss, (cfg.T,), f32),
+        ("total", out.total, (1,), f32), ("n_rows", out.n_rows, (1,), i32),
+        ("d_hidden", out.d_hidden, (cfg.T, cfg.H), e),
+        ("d_lm_head", out.d_lm_head, (vh, cfg.H), e),
+        ("d_markov_w1", out.d_markov_w1, (V, r), e),
+        ("d_markov_w2", out.d_markov_w2, (r, vh), e),
+        ("teacher.ids", teacher.ids, listed, i32),
+        ("teacher.logits", teacher.logits, listed, f32),
+        ("teacher.lse", teacher.lse, (cfg.T,), f32))
+    for t in tensors:
+        _checked(*t)
+    prev = prev if r > 0 else None
+    args = (_checked("hidden", hidden, (cfg.T, cfg.H), e), _checked("prev", prev, (cfg.T,), i32),
+            teacher.struct(), _checked("weights", weights, (cfg.T,), f32))
+    here = _on_this_gpu([t[0] for t in tensors] + ["hidden", "prev", "weights", "workspace"],
+                        *[t[1] for t in tensors], hidden, prev, weights, workspace)
+    _abi.check(_abi.dspark_distill_loss(cfg, head.struct(), *args, out.struct(),
+                                        *_room(workspace), _stream(stream, here)))
+
+
 def make_norm_config(T, H, dtype, eps=1e-6, residual_scale=1.0, weight_offset=0.0,
                      gate_span=1) -> _abi.dspark_norm_config:
     return _abi.dspark_norm_config(T=T, H=H,
@@ -396,3 +449,92 @@ def clip_grads(grads: GradList, max_norm, norm, workspace, stream=None) -> None:
     here = _on_this_gpu(("norm", "workspace"), norm, workspace)
     _abi.check(_abi.dspark_clip_grads(len(grads), grads.array, float(max_norm), at,
                                       *_room(workspace), _stream(stream, here)))
+
+
+# ------------------------------------------------------------------ tokens in and out
+def make_sample_config(T, V, dtype, temperature=1.0, top_k=0, top_p=1.0,
+                       min_p=0.0) -> _abi.dspark_sample_config:
+    return _abi.dspark_sample_config(T=T, V=V, ld=V,
+                                     dtype=_DT[dtype] if isinstance(dtype, str) else int(dtype),
+                                     top_k=int(top_k), temperature=float(temperature),
+                                     top_p=float(top_p), min_p=float(min_p))
+
+
+def _logit_rows(logits, T, V, dtype) -> int:
+    """The elements from a row of logits to the next; rows may lie apart, not their elements."""
+    if (logits.shape != (T, V) or logits.dtype is not dtype or (V > 1 and logits.stride(1) != 1)
+            or (T > 1 and logits.stride(0) < V)):
+        raise ValueError(f"logits: need a {dtype} tensor of shape {(T, V)} with dense rows, got "
+                         f"{logits.dtype} {tuple(logits.shape)} with strides {logits.stride()}")
+    return logits.stride(0) if T > 1 else V
+
+
+def sample(cfg, logits, uniform, tokens, logp=None, temperature=None, top_k=None, top_p=None,
+           min_p=None, stream=None) -> None:
+    """dspark_sample on torch tensors; raises DSparkError on a non-OK status.  ``temperature``,
+    ``top_k``, ``top_p``, ``min_p``: tensors with every row's own setting, in the config's
+    place."""
+    T, f32, i32 = (cfg.T,), torch.float32, torch.int32
+    ld = _logit_rows(logits, cfg.T, cfg.V, _TORCH_DT.get(cfg.dtype))
+    if ld != cfg.ld:
+        cfg = _abi.dspark_sample_config.from_buffer_copy(cfg)
+        cfg.ld = ld
+    args = (_checked("uniform", uniform, T, f32), _checked("tokens", tokens, T, i32),
+            _checked("logp", logp, T, f32))
+    own = (_checked("top_k", top_k, T, i32), _checked("temperature", temperature, T, f32),
+           _checked("top_p", top_p, T, f32), _checked("min_p", min_p, T, f32))
+    here = _on_this_gpu(("logits", "uniform", "tokens", "logp", "top_k", "temperature", "top_p",
+                         "min_p"), logits, uniform, tokens, logp, top_k, temperature, top_p,
+                        min_p)
+    rows = None if own == (None,) * 4 else _abi.dspark_sample_rows(*own)
+    _abi.check(_abi.dspark_sample(cfg, rows, logits.data_ptr(), *args, _stream(stream, here)))
+
+
+def top_logits(logits, ids, values, lse=None, stream=None) -> None:
+    """dspark_top_logits on torch tensors; raises DSparkError on a non-OK status.  The k of
+    ``ids`` and ``values`` [T, k] is how many are listed."""
+    dt = {v: k for k, v in _TORCH_DT.items()}
+    if logits.dim() != 2 or ids.dim() != 2 or logits.dtype not in dt:
+        raise ValueError("logits and ids: need matrices, logits of float32 or bfloat16")
+    (T, V), k = logits.shape, ids.shape[1]
+    ld = _logit_rows(logits, T, V, logits.dtype)
+    args = (_checked("ids", ids, (T, k), torch.int32),
+            _checked("values", values, (T, k), torch.float32),
+            _checked("lse", lse, (T,), torch.float32))
+    here = _on_this_gpu(("logits", "ids", "values", "lse"), logits, ids, values, lse)
+    _abi.check(_abi.dspark_top_logits(T, V, ld, dt[logits.dtype], k, logits.data_ptr(), *args,
+                                      _stream(stream, here)))
+
+
+def make_embed_config(T, V, H, dtype, scale=1.0) -> _abi.dspark_embed_config:
+    return _abi.dspark_embed_config(T=T, V=V, H=H,
+                                    dtype=_DT[dtype] if isinstance(dtype, str) else int(dtype),
+                                    scale=float(scale))
+
+
+def embed(cfg, table, ids, out, stream=None) -> None:
+    """dspark_embed on torch tensors; raises DSparkError on a non-OK status."""
+    e = _TORCH_DT.get(cfg.dtype)
+    args = (_checked("table", table, (cfg.V, cfg.H), e),
+            _checked("ids", ids, (cfg.T,), torch.int32), _checked("out", out, (cfg.T, cfg.H), e))
+    here = _on_this_gpu(("table", "ids", "out"), table, ids, out)
+    _abi.check(_abi.dspark_embed(cfg, *args, _stream(stream, here)))
+
+
+def embed_workspace_for(cfg, device="cuda") -> torch.Tensor:
+    n = _abi.dspark_embed_workspace_size(cfg)
+    if n == 0:
+        _abi.check(_abi.DSPARK_ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def embed_backward(cfg, ids, d_out, d_table, workspace, add=None, stream=None) -> None:
+    """dspark_embed_backward on torch tensors; raises DSparkError on a non-OK status."""
+    e = _TORCH_DT.get(cfg.dtype)
+    args = (_checked("ids", ids, (cfg.T,), torch.int32),
+            _checked("d_out", d_out, (cfg.T, cfg.H), e),
+            _checked("add", add, (cfg.V, cfg.H), e),
+            _checked("d_table", d_table, (cfg.V, cfg.H), e))
+    here = _on_this_gpu(("ids", "d_out", "add", "d_table", "workspace"), ids, d_out, add, d_table,
+                        workspace)
+    _abi.check(_abi.dspark_embed_backward(cfg, *args, *_room(workspace), _stream(stream, here)))

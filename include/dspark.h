@@ -495,6 +495,49 @@ dspark_status dspark_head_loss(const dspark_loss_config* cfg, const dspark_head*
                                const dspark_loss_outputs* out, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* What a teacher says of every row: its listed tokens (dspark_top_logits makes such a list). */
+typedef struct dspark_teacher {
+  const int32_t* ids;    /* device [T, k]: token ids; a negative one is absent */
+  const float* logits;   /* device [T, k] fp32: their logits; -infinity: absent */
+  const float* lse;      /* device [T] fp32: the log-sum-exp of scale * logits over the
+                            teacher's whole vocabulary, or NULL: over the listed tokens */
+  int32_t k;             /* listed tokens a row, 1 .. 256 */
+  float scale;           /* factor of the teacher's logits (1 / temperature); finite */
+} dspark_teacher;
+
+/* Bytes of device workspace dspark_distill_loss needs: dspark_head_loss's, and about 12 bytes
+   for each listed token; 0 on invalid input.  256-byte aligned; needs no initialisation. */
+size_t dspark_distill_loss_workspace_size(const dspark_loss_config* cfg,
+                                          const dspark_head* head,
+                                          const dspark_teacher* teacher,
+                                          const dspark_loss_outputs* out);
+
+/*
+ * dspark_distill_loss -- the divergence of the head from a teacher's listed tokens, with its
+ * gradients.  With z as for dspark_head_loss and log p = z - log sum_v exp z:
+ *
+ *   log q[t, k] = scale * logits[t, k] - L[t]
+ *   loss[t]     = sum_k q[t, k] (log q[t, k] - log p[t, ids[t, k]])
+ *
+ * Listed tokens that the head cannot emit (absent from d2t, or masked by lm_bias) are left out.
+ * L is the log-sum-exp of the ones that are not, so that their q sum to 1; or, with
+ * teacher->lse, that of the teacher's whole vocabulary: q are then the teacher's own
+ * probabilities, and the rest of them takes no part.  A row with no token left carries no loss:
+ * nothing of it is read into any result.  A token at or above V, or listed twice in a row, or
+ * a prev outside [0, V) on a row with a loss, drops the row and raises the error word.
+ *
+ * config, head, hidden, prev, weights, outputs (n_rows: rows with a loss), precision, workspace
+ * and capture are as for dspark_head_loss.  The listed tokens' logits are taken by fp32 dot
+ * products, and their entries of the logits' gradient by themselves, so that a loss near 0
+ * keeps its gradient.  In bf16 these entries are rounded to 8 bits before the products, with
+ * what the first listed token's lost given back to d_hidden and d_markov_w1.
+ */
+dspark_status dspark_distill_loss(const dspark_loss_config* cfg, const dspark_head* head,
+                                  const void* hidden, const int32_t* prev,
+                                  const dspark_teacher* teacher, const float* weights,
+                                  const dspark_loss_outputs* out, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* Sizes and knobs of dspark_block_norm and its gradient. */
 typedef struct dspark_norm_config {
   int32_t T;             /* rows (tokens), 1 .. 2^30 */
@@ -577,6 +620,119 @@ size_t dspark_clip_grads_workspace_size(int32_t count, const dspark_grad* grads)
 dspark_status dspark_clip_grads(int32_t count, const dspark_grad* grads, float max_norm,
                                 float* norm, void* workspace, size_t workspace_bytes,
                                 void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Tokens in and out: the drafter's input rows and their gradient, and the tokens of a
+ * target's logits.  dspark_sample draws the tokens that dspark_verify takes as `target`
+ * (a draft is then accepted exactly where it is what the target would have drawn, so the
+ * output is the target's own distribution); dspark_top_logits lists what a teacher says.
+ * (The pages verify greedily: the operators are this library's own.)
+ * ------------------------------------------------------------------------------- */
+
+/* Sizes and settings of dspark_sample. */
+typedef struct dspark_sample_config {
+  int32_t T;             /* rows, 1 .. 2^20 */
+  int32_t V;             /* tokens of a row, 1 .. 2^24 */
+  int64_t ld;            /* elements from a row of logits to the next, >= V */
+  int32_t dtype;         /* dspark_dtype of the logits */
+  int32_t top_k;         /* <= 0: off */
+  float temperature;     /* <= 0: the largest logit, whatever the filters say */
+  float top_p;           /* >= 1: off; <= 0: the largest */
+  float min_p;           /* <= 0: off; >= 1: those equal to the largest */
+} dspark_sample_config;
+
+/* Settings of single rows (device arrays [T]), each in its config value's place; or NULL. */
+typedef struct dspark_sample_rows {
+  const int32_t* top_k;
+  const float* temperature;
+  const float* top_p;
+  const float* min_p;
+} dspark_sample_rows;
+
+/*
+ * dspark_sample -- a token of every row of logits, by one given uniform number each.
+ *
+ * A row's order is by falling logit, equal ones by rising id.  With weights
+ * w = exp((z - max) / temperature), one after the other:
+ *   top_k  keeps the first top_k tokens of the order
+ *   top_p  keeps its shortest prefix whose weight is at least top_p of the weight kept so far
+ *   min_p  keeps the tokens with w >= min_p
+ * and the token is the first by id for which the weight of the kept tokens up to it exceeds
+ * uniform times the weight of all kept ones.
+ *
+ * logits  device [T, ld] dtype.  A logit of -infinity or NaN is never drawn; a row without any
+ *         other has token -1 and log-probability -infinity.  With +infinity in a row, only those
+ *         are drawn, all alike
+ * rows    host struct of device arrays, or NULL.  A row's NaN setting: temperature as 0, top_p
+ *         and min_p off
+ * uniform device [T] fp32 in [0, 1) (below, or NaN: 0; above: the last kept one
+ *         that has a weight)
+ * tokens  device [T] int32
+ * logp    device [T] fp32 or NULL: the token's log-probability among the kept ones
+ *
+ * Weights are cut to whole multiples of 2^-S of the largest, S = 62 - ceil(log2 V) (44 for
+ * 151936 tokens), and off by at most 2^-28 of themselves besides; their sums are exact.  Needs no workspace; calls may overlap.
+ * Can be captured into a CUDA graph.
+ */
+dspark_status dspark_sample(const dspark_sample_config* cfg, const dspark_sample_rows* rows,
+                            const void* logits, const float* uniform, int32_t* tokens,
+                            float* logp, void* stream);
+
+/*
+ * dspark_top_logits -- the k largest logits of every row, and the row's log-sum-exp.
+ *
+ * logits  device [T, ld] dtype, T in 1 .. 2^20, V in 1 .. 2^24, ld >= V
+ * k       1 .. min(V, 1024)
+ * ids     device [T, k] int32, values device [T, k] fp32: by falling logit, equal ones by rising
+ *         id.  -infinity and NaN are not listed: where fewer than k others are left, -1 and
+ *         -infinity stand (absent, for dspark_distill_loss)
+ * lse     device [T] fp32 or NULL: log sum exp of the row (NaN left out)
+ *
+ * Needs no workspace; calls may overlap.  Can be captured into a CUDA graph.
+ */
+dspark_status dspark_top_logits(int32_t T, int32_t V, int64_t ld, int32_t dtype, int32_t k,
+                                const void* logits, int32_t* ids, float* values, float* lse,
+                                void* stream);
+
+/* Sizes and settings of dspark_embed and its gradient. */
+typedef struct dspark_embed_config {
+  int32_t T;             /* rows (tokens), 1 .. 2^20 */
+  int32_t V;             /* rows of the table, 1 .. 2^24 */
+  int32_t H;             /* features, 1 .. 2^16 */
+  int32_t dtype;         /* dspark_dtype of every tensor */
+  float scale;           /* finite */
+} dspark_embed_config;
+
+/*
+ * dspark_embed -- out[t] = scale * table[ids[t]].
+ *
+ * table   device [V, H]      ids  device [T] int32; a row whose id is outside [0, V) is zeros
+ * out     device [T, H], rounded once; must not overlap the table
+ */
+dspark_status dspark_embed(const dspark_embed_config* cfg, const void* table,
+                           const int32_t* ids, void* out, void* stream);
+
+/* Bytes of device workspace dspark_embed_backward needs; 0 on invalid input.  256-byte
+   aligned; needs no initialisation. */
+size_t dspark_embed_workspace_size(const dspark_embed_config* cfg);
+
+/*
+ * dspark_embed_backward -- d_table[v] = add[v] + scale * sum of d_out[t] over ids[t] = v.
+ *
+ * ids     device [T] int32.  A negative id is no token; one at or above V is none either, and
+ *         raises the error word (dspark_device_status)
+ * d_out   device [T, H]
+ * add     device [V, H] or NULL (zeros): what the gradient is added to, as the gradient of a
+ *         tied lm_head.  May be d_table itself: then only rows that occur are read and written
+ * d_table device [V, H], overwritten; overlaps nothing else
+ *
+ * Sums are fp32, over a token's rows in their order (in parts, for tokens of many rows), and
+ * rounded once.  The same call gives the same bits.  Not reentrant on one workspace.  Can be
+ * captured into a CUDA graph.
+ */
+dspark_status dspark_embed_backward(const dspark_embed_config* cfg, const int32_t* ids,
+                                    const void* d_out, const void* add, void* d_table,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* dspark_status_string(int32_t status);
