@@ -475,6 +475,8 @@ struct Row {
   __device__ __forceinline__ int put(int v, unsigned take) {
     const int n = __popc(take);
     if (n == 0) return 0;
+    // (a list that runs over by far, of equal logits, is not worth its atomics)
+    if (!HELD && *(volatile uint32_t*)&sh.claim > kList) return n;
     uint32_t at = atomicAdd(of(&sh.claim, 0), (uint32_t)n);
     u64* list = of(sh.list, 0);
     for (; take && at < kList; take &= take - 1, ++at) {
@@ -522,7 +524,7 @@ struct Row {
   }
   // Lists the elements with lo <= key <= hi that `b` keeps.
   __device__ __forceinline__ void collect(uint32_t lo, uint32_t hi, const Border& b) {
-    const float z_lo = value_of(lo);
+    const float z_lo = lo > kNoKey ? value_of(lo) : -INFINITY;
     int n = 0;
     part.each([&](int v, const uint4& raw) {
       if (!(Vec<E>::top(raw) >= z_lo)) return;
@@ -619,6 +621,11 @@ struct Row {
   __device__ __noinline__ bool locate(u64 target, Border& b, uint32_t lo, uint32_t hi, u64 above,
                                       const Weights w) {
     const Border in = b;
+    // (the keys of bf16 logits differ in their high halves)
+    constexpr int kUnit = sizeof(E) == 2 ? 16 : 0;
+    const uint32_t least = lo, most = hi;
+    lo >>= kUnit;
+    hi >>= kUnit;
     const int per = kBins / size();
     sync();                            // (the list and its count have been read)
     for (;;) {
@@ -632,8 +639,9 @@ struct Row {
         Vec<E>::get(raw, z);
 #pragma unroll
         for (int j = 0; j < VE; ++j) {
-          const uint32_t k = key_of(z[j]);
-          const bool take = k >= lo && k <= hi && in.keeps(k, part.id(v, j));
+          const uint32_t full = key_of(z[j]), k = full >> kUnit;
+          const bool take = k >= lo && k <= hi && full >= least && full <= most &&
+                            in.keeps(full, part.id(v, j));
           const uint32_t bin = (hi - k) >> shift;
           const unsigned m = __ballot_sync(0xFFFFFFFFu, take);
           if (!m) continue;
@@ -706,7 +714,7 @@ struct Row {
       const uint32_t wide = (1u << shift) - 1;
       lo = hi - lo > wide ? hi - wide : lo;
       if (n <= kList) {
-        collect(lo, hi, in);
+        collect(max(least, lo << kUnit), min(most, (hi << kUnit) | ((1u << kUnit) - 1u)), in);
         sync();
         if (rank() == 0) {
           sort_list((int)n);
@@ -721,7 +729,8 @@ struct Row {
       }
       if (shift == 0) {
         // equal logits: the border is the `nth` of them by id
-        const u64 x1 = MASS ? w(value_of(hi)) : 1ull;
+        const uint32_t key = kUnit > 0 && !(hi & 0x8000u) ? (hi << kUnit) | 0xFFFFu : hi << kUnit;
+        const u64 x1 = MASS ? w(value_of(key)) : 1ull;
         const u64 nth = (target - above + x1 - 1) / x1;
         auto ones = [&](int v, const uint4& raw, u64 (&y)[VE]) {
           float z[VE];
@@ -729,14 +738,14 @@ struct Row {
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
             const uint32_t k = key_of(z[j]);
-            y[j] = k == hi && in.keeps(k, part.id(v, j));
+            y[j] = k == key && in.keeps(k, part.id(v, j));
           }
         };
         u64 first;
         const u64 own = own_sum(ones);
         row_sum(own, first);
         find(nth - 1, first, own, ones, [&](int id, u64) {
-          tell_border((u64)hi << 32 | (0xFFFFFFFFu - (uint32_t)id));
+          tell_border((u64)key << 32 | (0xFFFFFFFFu - (uint32_t)id));
         });
         b = told_border();
         return true;
