@@ -9,8 +9,8 @@
 // equal tokens of each chunk in registers: frequent tokens then cost no more than others.  A run
 // that ends in its chunk is written to the table; the parts of one that chunks share are
 // joined by a last kernel, in order.  Rows of the table that no token asks for are written
-// while one CTA sorts (up to kSortAll rows: each CTA finds out about its own rows of the table
-// by looking at every token), or by a bit map of the tokens that occur.
+// beside the sort and the sums, which both wait for their loads more than they use the memory:
+// by a bit map of the tokens, or before there is one by looking at every token.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -27,9 +27,11 @@ namespace {
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortAll = 16384;          // rows that one CTA sorts in its shared memory
 constexpr int kTile = 4096;              // rows of one CTA of the sort of more
-constexpr int kDigit = 8, kDigits = 1 << kDigit;
+constexpr int kDigitAll = 9;             // bits of a digit in one CTA's sort: two passes up to 2^18
+constexpr int kDigit = 8, kDigits = 1 << kDigit;                 // and in the other
 constexpr int kMaxChunk = 512;
 constexpr int kSumThreads = 256;
+constexpr int kFillRows = 64;            // rows of the table that one CTA beside the sums fills
 
 template <typename E, int VE>
 struct alignas(sizeof(E) * VE) Pack {
@@ -105,21 +107,22 @@ __device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s_warp) {
   return before + in - v;
 }
 
-// The places of R items a thread among the CTA's by their digit, equal digits in the items'
-// order: warp w holds items [32 R w, 32 R (w + 1)), item r of a lane is 32 r + lane of those.
-// cnt: [warps][kDigits]; afterwards place[r] + cnt[warp][digit] is an item's place.
-template <int R>
+// The places of R items a thread among the CTA's by their digit of D bits, equal digits in the
+// items' order: warp w holds items [32 R w, 32 R (w + 1)), item r of a lane is 32 r + lane of those.
+// cnt: [warps][2^D]; afterwards place[r] + cnt[warp][digit] is an item's place.
+template <int R, int D>
 __device__ __forceinline__ void rank_items(const uint32_t (&digit)[R], uint32_t (&place)[R],
                                            uint32_t* cnt, uint32_t* s_warp) {
+  constexpr int kOf = 1 << D;
   const int tid = threadIdx.x, lane = tid % 32;
-  uint32_t* mine = cnt + (tid / 32) * kDigits;
-  for (int i = tid; i < kSortWarps * kDigits; i += kSortThreads) cnt[i] = 0;
+  uint32_t* mine = cnt + (tid / 32) * kOf;
+  for (int i = tid; i < kSortWarps * kOf; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     // (items past the end have a digit of their own, and are not counted)
     const unsigned peers = __match_any_sync(0xFFFFFFFFu, digit[r]);
-    const bool in = digit[r] < kDigits;
+    const bool in = digit[r] < kOf;
     const uint32_t before = __popc(peers & ((1u << lane) - 1u));
     const uint32_t base = in ? mine[digit[r]] : 0u;
     __syncwarp();
@@ -128,19 +131,19 @@ __device__ __forceinline__ void rank_items(const uint32_t (&digit)[R], uint32_t 
     place[r] = base + before;
   }
   __syncthreads();
-  // counts become offsets, digit by digit and in each warp by warp: eight a thread
-  static_assert(kSortWarps * kDigits == 8 * kSortThreads, "eight counts a thread");
-  const int d = tid / 4, w0 = tid % 4 * 8;
-  uint32_t x[8], s = 0;
+  // counts become offsets, digit by digit and in each warp by warp: `each` a thread
+  constexpr int each = kSortWarps * kOf / kSortThreads, per = kSortWarps / each;
+  const int d = tid / per, w0 = tid % per * each;
+  uint32_t x[each], s = 0;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    x[q] = cnt[(w0 + q) * kDigits + d];
+  for (int q = 0; q < each; ++q) {
+    x[q] = cnt[(w0 + q) * kOf + d];
     s += x[q];
   }
   uint32_t at = block_before(s, s_warp);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    cnt[(w0 + q) * kDigits + d] = at;
+  for (int q = 0; q < each; ++q) {
+    cnt[(w0 + q) * kOf + d] = at;
     at += x[q];
   }
   __syncthreads();
@@ -160,7 +163,7 @@ __device__ void sort_all(const EmbedArgs& a, uint32_t* smem) {
     pos[r] = warp * 32 * R + r * 32 + lane;
     key[r] = (int)pos[r] < a.T ? sort_key(a, (int)pos[r]) : 0u;
   }
-  const int passes = (a.bits + kDigit - 1) / kDigit, width = (a.bits + passes - 1) / passes;
+  const int passes = (a.bits + kDigitAll - 1) / kDigitAll, width = (a.bits + passes - 1) / passes;
   for (int p = 0; p < passes; ++p) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -171,45 +174,64 @@ __device__ void sort_all(const EmbedArgs& a, uint32_t* smem) {
       }
       digit[r] = item < a.T ? key[r] >> (p * width) & ((1u << width) - 1u) : 1u << 20;
     }
-    rank_items<R>(digit, place, cnt, s_warp);
+    rank_items<R, kDigitAll>(digit, place, cnt, s_warp);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (digit[r] >= kDigits) continue;
-      const uint32_t to = cnt[warp * kDigits + digit[r]] + place[r];
+      if (digit[r] >> kDigitAll) continue;
+      const uint32_t to = cnt[(warp << kDigitAll) + digit[r]] + place[r];
       s_key[to] = key[r];
       s_pos[to] = pos[r];
     }
     __syncthreads();
   }
+  // the sorted list, and the bits of its tokens
+  for (int i = threadIdx.x; i < (a.V + 31) / 32; i += kSortThreads) a.there[i] = 0;
+  __syncthreads();
   for (int i = threadIdx.x; i < a.T; i += kSortThreads) {
-    a.key[0][i] = s_key[i];
+    const uint32_t k = s_key[i];
+    a.key[0][i] = k;
     a.pos[0][i] = s_pos[i];
+    if (k < (uint32_t)a.V && (i == 0 || s_key[i - 1] != k)) atomicOr(&a.there[k / 32], 1u << k % 32);
   }
 }
 
 // Row v of the table where no token asks for it: zeros, or what the gradient is added to.  By a
-// warp.
-template <typename E, int VE>
+// warp, 16 bytes at a time between the ends that are not.
+template <typename E>
 __device__ __forceinline__ void fill_row(const EmbedArgs& a, size_t v) {
-  using P = Pack<E, VE>;
-  const int per = a.H / VE, lane = threadIdx.x % 32;
-  P* to = reinterpret_cast<P*>(a.d_table) + v * per;
-  if (a.add) {
-    const P* from = reinterpret_cast<const P*>(a.add) + v * per;
-#pragma unroll 8
-    for (int c = lane; c < per; c += 32) to[c] = from[c];
-  } else {
-    P none;
+  constexpr int VE = 16 / sizeof(E);
+  const int lane = threadIdx.x % 32;
+  E* to = reinterpret_cast<E*>(a.d_table) + v * a.H;
+  const E* from = a.add ? reinterpret_cast<const E*>(a.add) + v * a.H : nullptr;
+  const bool alike = !from || ((uintptr_t)from - (uintptr_t)to) % 16 == 0;
+  const int head = alike ? min(a.H, (int)((16 - (uintptr_t)to % 16) % 16 / sizeof(E))) : a.H;
+  const int vecs = (a.H - head) / VE, tail = head + vecs * VE;
+  uint4* tv = reinterpret_cast<uint4*>(to + head);
+  if (from) {
+    const uint4* fv = reinterpret_cast<const uint4*>(from + head);
+    for (int c0 = lane; c0 < vecs; c0 += 32 * 8) {
+      uint4 x[8];
 #pragma unroll
-    for (int j = 0; j < VE; ++j) none.e[j] = rounded<E>(0.f);
+      for (int q = 0; q < 8; ++q)
+        if (c0 + 32 * q < vecs) x[q] = __ldcs(fv + c0 + 32 * q);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c0 + 32 * q < vecs) tv[c0 + 32 * q] = x[q];
+    }
+    for (int c = lane; c < head; c += 32) to[c] = from[c];
+    for (int c = tail + lane; c < a.H; c += 32) to[c] = from[c];
+  } else {
 #pragma unroll 4
-    for (int c = lane; c < per; c += 32) to[c] = none;
+    for (int c = lane; c < vecs; c += 32) tv[c] = make_uint4(0, 0, 0, 0);
+    for (int c = lane; c < head; c += 32) to[c] = rounded<E>(0.f);
+    for (int c = tail + lane; c < a.H; c += 32) to[c] = rounded<E>(0.f);
   }
 }
 
-// CTA 0 sorts the rows; the others each fill their part of the table's rows that do not occur.
-template <typename E, int VE, int R>
-__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_fill(const EmbedArgs a, int rows) {
+// CTA 0 sorts the rows; the others meanwhile fill the first ones of the table that do not occur,
+// `rows` each (whole words of bits).  They find out which by looking at every token.
+template <typename E, int R>
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort(const EmbedArgs a, int rows) {
   extern __shared__ uint32_t s_dyn[];
   pdl_wait();
   pdl_signal();
@@ -217,18 +239,17 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_fill(const EmbedAr
     sort_all<R>(a, s_dyn);
     return;
   }
-  const int tid = threadIdx.x, warp = tid / 32;
-  const int v0 = (blockIdx.x - 1) * rows, v1 = min(a.V, v0 + rows);      // (rows: whole words)
+  const int v0 = (blockIdx.x - 1) * rows, v1 = min(a.V, v0 + rows), tid = threadIdx.x;
   for (int i = tid; i < rows / 32; i += kSortThreads) s_dyn[i] = 0;
   __syncthreads();
-#pragma unroll 4
+#pragma unroll 8
   for (int t = tid; t < a.T; t += kSortThreads) {
     const int id = a.ids[t];
     if (id >= v0 && id < v1) atomicOr(&s_dyn[(id - v0) / 32], 1u << (id - v0) % 32);
   }
   __syncthreads();
-  for (int v = v0 + warp; v < v1; v += kSortWarps)
-    if (!(s_dyn[(v - v0) / 32] >> (v - v0) % 32 & 1u)) fill_row<E, VE>(a, (size_t)v);
+  for (int v = v0 + tid / 32; v < v1; v += kSortWarps)
+    if (!(s_dyn[(v - v0) / 32] >> (v - v0) % 32 & 1u)) fill_row<E>(a, (size_t)v);
 }
 
 // --- more rows than one CTA sorts
@@ -239,13 +260,6 @@ __global__ void __launch_bounds__(256) embed_mark(const EmbedArgs a) {
   a.key[1][t] = k;
   a.pos[1][t] = (uint32_t)t;
   if (k < (uint32_t)a.V) atomicOr(&a.there[k / 32], 1u << k % 32);
-}
-
-template <typename E, int VE>
-__global__ void __launch_bounds__(256) embed_fill(const EmbedArgs a) {
-  const int warps = gridDim.x * 8;
-  for (int v = blockIdx.x * 8 + threadIdx.x / 32; v < a.V; v += warps)
-    if (!(a.there[v / 32] >> v % 32 & 1u)) fill_row<E, VE>(a, (size_t)v);
 }
 
 // Counts of the digits at `shift` of tile blockIdx.x.
@@ -295,7 +309,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_place(const EmbedArgs a, i
     pos[r] = i < a.T ? a.pos[from][i] : 0u;
     digit[r] = i < a.T ? key[r] >> shift & ((1u << width) - 1u) : 1u << 20;
   }
-  rank_items<R>(digit, place, cnt, s_warp);
+  rank_items<R, kDigit>(digit, place, cnt, s_warp);
   if (tid < kDigits) first[tid] = cnt[tid];        // warp 0's: where the digit starts
   __syncthreads();
 #pragma unroll
@@ -310,84 +324,137 @@ __global__ void __launch_bounds__(kSortThreads) embed_place(const EmbedArgs a, i
 }
 
 // ------------------------------------------------------------------ sums
+// The table's row v from its sum, and `add`'s columns of it (NULL: none).
 template <typename E, int VE>
-__device__ __forceinline__ void put_sum(const EmbedArgs& a, size_t v, int c, const float (&s)[VE]) {
-  using P = Pack<E, VE>;
-  const size_t at = v * (a.H / VE) + c;
-  P o;
-  if (a.add) {
-    const P x = reinterpret_cast<const P*>(a.add)[at];
+__device__ __forceinline__ void put_sum(const EmbedArgs& a, size_t v, int c, const float (&s)[VE],
+                                        const Pack<E, VE>* add) {
+  Pack<E, VE> o;
 #pragma unroll
-    for (int j = 0; j < VE; ++j) o.e[j] = rounded<E>(fmaf(a.scale, s[j], to_f32(x.e[j])));
-  } else {
-#pragma unroll
-    for (int j = 0; j < VE; ++j) o.e[j] = rounded<E>(a.scale * s[j]);
-  }
-  reinterpret_cast<P*>(a.d_table)[at] = o;
+  for (int j = 0; j < VE; ++j)
+    o.e[j] = rounded<E>(add ? fmaf(a.scale, s[j], to_f32(add->e[j])) : a.scale * s[j]);
+  reinterpret_cast<Pack<E, VE>*>(a.d_table)[v * (a.H / VE) + c] = o;
 }
 
+// VE sums of the workspace, in vectors of four where there are as many.
 template <int VE>
 __device__ __forceinline__ void put_part(float* to, const float (&s)[VE]) {
+  if constexpr (VE == 1) {
+    *to = s[0];
+  } else {
 #pragma unroll
-  for (int j = 0; j < VE; ++j) to[j] = s[j];
+    for (int j = 0; j < VE; j += 4)
+      *reinterpret_cast<float4*>(to + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+  }
+}
+template <int VE>
+__device__ __forceinline__ void get_part(const float* from, float (&s)[VE]) {
+  if constexpr (VE == 1) {
+    s[0] = *from;
+  } else {
+#pragma unroll
+    for (int j = 0; j < VE; j += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(from + j);
+      s[j] = x.x; s[j + 1] = x.y; s[j + 2] = x.z; s[j + 3] = x.w;
+    }
+  }
 }
 
-// CTA (chunk, column block): a thread sums VE columns of the chunk's rows, run by run, eight
-// rows' loads in flight.
-template <typename E, int VE>
-__global__ void __launch_bounds__(kSumThreads) embed_sum(const EmbedArgs a, int buf) {
+// One chunk and column block: a thread sums VE columns of the chunk's rows, run by run, the
+// loads of several rows in flight.
+template <typename E, int VE, bool ADD>
+__device__ __forceinline__ void sum_chunk(const EmbedArgs& a, int buf, int chunk, int block,
+                                          uint32_t* s_key, uint32_t* s_pos) {
   using P = Pack<E, VE>;
-  pdl_wait();
-  pdl_signal();
-  __shared__ uint32_t s_key[kMaxChunk + 2], s_pos[kMaxChunk];
-  const int tid = threadIdx.x, chunk = blockIdx.x, i0 = chunk * a.chunk;
-  const int n = min(a.chunk, a.T - i0);
+  constexpr int kAt = VE == 1 ? 16 : ADD ? 4 : 8;
+  constexpr uint32_t kEnd = 1u << 31;                   // the run ends with this row
+  const int tid = threadIdx.x, i0 = chunk * a.chunk, size = min(a.chunk, a.T - i0);
   const uint32_t V = (uint32_t)a.V;
-  for (int i = tid; i < n + 2; i += kSumThreads) {      // with the neighbours before and after
+  for (int i = tid; i < size + 2; i += kSumThreads) {   // with the neighbours before and after
     const int at = i0 + i - 1;
     s_key[i] = at >= 0 && at < a.T ? a.key[buf][at] : V;
-    if (i < n) s_pos[i] = a.pos[buf][i0 + i];
   }
   __syncthreads();
   const uint32_t* key = s_key + 1;
-  const int per = a.H / VE, c = blockIdx.y * kSumThreads + tid;
+  for (int i = tid; i < size; i += kSumThreads) {
+    const bool last = i == size - 1 || key[i + 1] != key[i];
+    s_pos[i] = a.pos[buf][i0 + i] | (last ? kEnd : 0u);
+  }
+  // (rows with a token come first)
+  int n = 0;
+  if (key[size - 1] < V) {
+    n = size;
+  } else {
+    for (int hi = size; n < hi;) {
+      const int m = (n + hi) / 2;
+      if (key[m] < V) n = m + 1;
+      else hi = m;
+    }
+  }
+  __syncthreads();
+  const int per = a.H / VE, c = block * kSumThreads + tid;
   const bool in = c < per;
-  int tok[2] = {-1, -1};
+  const P* d = reinterpret_cast<const P*>(a.d_out) + (in ? c : 0);
+  const P* add = reinterpret_cast<const P*>(a.add) + (in ? c : 0);
+  bool first = true;                                    // of the chunk's runs
+  int tok0 = -1, tok1 = -1;
   float acc[VE] = {};
-  int start = 0;
-  const P* d = reinterpret_cast<const P*>(a.d_out);
-  for (int b = 0; b < n && key[b] < V; b += 8) {
-    P x[8];
+#pragma unroll 1
+  for (int b = 0; b < n; b += kAt) {
+    P x[kAt];
+    P y[ADD ? kAt : 1];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int i = b + q;
-      if (in && i < n && key[i] < V) x[q] = d[(size_t)s_pos[i] * per + c];
+    for (int q = 0; q < kAt; ++q) {
+      const int i = min(b + q, n - 1);
+      x[q] = d[(size_t)(s_pos[i] & ~kEnd) * per];
+      if (ADD && (s_pos[i] & kEnd)) y[q] = add[(size_t)key[i] * per];
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kAt; ++q) {
       const int i = b + q;
-      if (i >= n || key[i] >= V) break;
+      if (i >= n) continue;
 #pragma unroll
       for (int j = 0; j < VE; ++j) acc[j] += to_f32(x[q].e[j]);
-      const uint32_t k = key[i];
-      const bool last = i == n - 1;
-      if (!last && key[i + 1] == k) continue;
+      if (!(s_pos[i] & kEnd)) continue;
       // the run ends here, or goes on in the next chunk
-      const bool shared_before = start == 0 && key[-1] == k;
-      const bool shared_after = last && key[n] == k;
-      if (shared_before || shared_after) {
-        const int s = shared_before ? 0 : 1;
-        tok[s] = (int)k;
-        if (in) put_part<VE>(a.part + ((size_t)chunk * 2 + s) * a.H + (size_t)c * VE, acc);
-      } else if (in) {
-        put_sum<E, VE>(a, k, c, acc);
+      const uint32_t k = key[i];
+      const bool shared_before = first && key[-1] == k;
+      const bool shared_after = i == size - 1 && key[size] == k;
+      if (shared_before) tok0 = (int)k;
+      else if (shared_after) tok1 = (int)k;
+      if (in) {
+        if (shared_before || shared_after)
+          put_part<VE>(a.part + ((size_t)chunk * 2 + !shared_before) * a.H + (size_t)c * VE, acc);
+        else
+          put_sum<E, VE>(a, k, c, acc, ADD ? &y[ADD ? q : 0] : nullptr);
       }
 #pragma unroll
       for (int j = 0; j < VE; ++j) acc[j] = 0.f;
-      start = i + 1;
+      first = false;
     }
   }
-  if (tid < 2 && blockIdx.y == 0) a.part_tok[chunk * 2 + tid] = tok[tid];
+  if (tid == 0 && block == 0) {
+    a.part_tok[chunk * 2] = tok0;
+    a.part_tok[chunk * 2 + 1] = tok1;
+  }
+}
+
+// The sums, which wait for their loads, and between them CTAs that fill the table's other rows
+// from `v0` on, `fills` of them, which wait for nothing.
+template <typename E, int VE, bool ADD>
+__global__ void __launch_bounds__(kSumThreads, 4) embed_sum(const EmbedArgs a, int buf, int v0, int fills) {
+  pdl_wait();
+  pdl_signal();
+  __shared__ uint32_t s_key[kMaxChunk + 2], s_pos[kMaxChunk];
+  const long long b = blockIdx.x, all = gridDim.x;
+  const int before = (int)(b * fills / all);            // fill CTAs before this one
+  if ((int)((b + 1) * fills / all) > before) {
+    const int first = v0 + before * kFillRows, end = min(a.V, first + kFillRows);
+    for (int v = first + threadIdx.x / 32; v < end; v += kSumThreads / 32)
+      if (!(a.there[v / 32] >> v % 32 & 1u)) fill_row<E>(a, (size_t)v);
+    return;
+  }
+  const int i = (int)b - before, blocks = (a.H / VE + kSumThreads - 1) / kSumThreads;
+  sum_chunk<E, VE, ADD>(a, buf, i / blocks, i % blocks, s_key, s_pos);
 }
 
 // CTA (chunk, column block): the token whose run starts in this chunk and goes on in the next
@@ -402,19 +469,18 @@ __global__ void __launch_bounds__(kSumThreads) embed_join(const EmbedArgs a) {
   if (c >= per) return;
   float s[VE], e[VE];
   const float* p = a.part + (size_t)c * VE;
+  get_part<VE>(p + ((size_t)chunk * 2 + 1) * a.H, s);
 #pragma unroll
-  for (int j = 0; j < VE; ++j) {
-    s[j] = p[((size_t)chunk * 2 + 1) * a.H + j];
-    e[j] = 0.f;
-  }
+  for (int j = 0; j < VE; ++j) e[j] = 0.f;
   bool more = true;
   for (int q0 = chunk + 1; more && q0 < a.chunks; q0 += 4) {
     float x[4][VE];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       more = more && q0 + q < a.chunks && a.part_tok[(q0 + q) * 2] == v;
+      if (more) get_part<VE>(p + (size_t)(q0 + q) * 2 * a.H, x[q]);
 #pragma unroll
-      for (int j = 0; j < VE; ++j) x[q][j] = more ? p[(size_t)(q0 + q) * 2 * a.H + j] : 0.f;
+      for (int j = 0; j < VE; ++j) x[q][j] = more ? x[q][j] : 0.f;
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -427,7 +493,12 @@ __global__ void __launch_bounds__(kSumThreads) embed_join(const EmbedArgs a) {
   }
 #pragma unroll
   for (int j = 0; j < VE; ++j) s[j] += e[j];
-  put_sum<E, VE>(a, (size_t)v, c, s);
+  if (a.add) {
+    const Pack<E, VE> x = reinterpret_cast<const Pack<E, VE>*>(a.add)[(size_t)v * per + c];
+    put_sum<E, VE>(a, (size_t)v, c, s, &x);
+  } else {
+    put_sum<E, VE>(a, (size_t)v, c, s, nullptr);
+  }
 }
 
 bool by16(const EmbedArgs& a, int es) {
@@ -447,35 +518,41 @@ cudaError_t lookup(const EmbedArgs& a) {
   return launch_after(embed_rows<E, VE, 1>, dim3((unsigned)a.T, cols), threads, 0, a.stream, a);
 }
 
-template <typename E, int VE, int R>
-cudaError_t sort_fill(const EmbedArgs& a) {
-  const size_t smem = sizeof(uint32_t) * (2 * kSortThreads * R + kSortWarps * kDigits);
+// Sorts the rows by their token in one CTA; the other SMs fill what rows of the table they can in
+// the time that takes, up to row *filled.
+template <typename E, int R>
+cudaError_t sort_one(const EmbedArgs& a, bool fill, int* filled) {
+  const size_t smem = sizeof(uint32_t) * (2 * kSortThreads * R + (kSortWarps << kDigitAll));
   int sms = 0;
   cudaError_t e = device_sms(&sms);
-  if (e == cudaSuccess) e = raise_smem_limit((const void*)embed_sort_fill<E, VE, R>, smem);
+  if (e == cudaSuccess) e = raise_smem_limit((const void*)embed_sort<E, R>, smem);
   if (e != cudaSuccess) return e;
-  const bool fill = a.add != a.d_table;
-  // whole words of rows for each of the other CTAs, as many as their bits have room for
-  const int most = (int)(smem / 4) * 32;
-  const int ctas = std::max(sms - 1, (a.V + most - 1) / most);
-  const int rows = ((a.V + ctas - 1) / ctas + 31) / 32 * 32;
-  return launch_after(embed_sort_fill<E, VE, R>, 1 + (fill ? (a.V + rows - 1) / rows : 0),
-                      kSortThreads, smem, a.stream, a, rows);
+  // (580 MB take 100 us, and the sort of 16384 rows about 50: the sums beside the rest of a larger
+  // table then read while it is written.  The gradient of 151936 x 4096 bf16 from 16384 rows: 249
+  // us with 290 MB, 238 with 580, 240 with all of it beside the sort.)
+  const size_t bytes = (size_t)a.H * sizeof(E) * (a.add ? 2 : 1);
+  const int rows = (int)std::min((size_t)a.V, (size_t)580000000 / bytes);
+  const int most = (int)(smem / 4) * 32;                // (bits that there is room for)
+  const int each = std::max(32, std::min(most, ((rows + sms - 2) / std::max(1, sms - 1) + 31) / 32 * 32));
+  const int ctas = fill ? std::min(sms - 1, (rows + each - 1) / each) : 0;
+  *filled = std::min(a.V, ctas * each);
+  return launch_after(embed_sort<E, R>, 1 + ctas, kSortThreads, smem, a.stream, a, each);
 }
 
 template <typename E, int VE>
 cudaError_t backward(const EmbedArgs& a) {
   cudaError_t e = cudaMemsetAsync(a.ctrl, 0, 256, a.stream);
-  int buf = 0;
+  const bool fill = a.add != a.d_table;
+  int buf = 0, filled = 0;
   if (e == cudaSuccess && a.T <= kSortAll) {
-    e = a.T <= kSortThreads       ? sort_fill<E, VE, 1>(a)
-        : a.T <= 4 * kSortThreads ? sort_fill<E, VE, 4>(a)
-                                  : sort_fill<E, VE, 16>(a);
+    e = a.T <= kSortThreads       ? sort_one<E, 1>(a, fill, &filled)
+        : a.T <= 4 * kSortThreads ? sort_one<E, 4>(a, fill, &filled)
+        : a.T <= 8 * kSortThreads ? sort_one<E, 8>(a, fill, &filled)
+                                  : sort_one<E, 16>(a, fill, &filled);
   } else if (e == cudaSuccess) {
     e = cudaMemsetAsync(a.there, 0, ((size_t)a.V + 31) / 32 * 4, a.stream);
     if (e != cudaSuccess) return e;
     embed_mark<<<(a.T + 255) / 256, 256, 0, a.stream>>>(a);
-    if (a.add != a.d_table) embed_fill<E, VE><<<1216, 256, 0, a.stream>>>(a);
     const int tiles = (a.T + kTile - 1) / kTile;
     const int passes = (a.bits + kDigit - 1) / kDigit, width = (a.bits + passes - 1) / passes;
     int from = 1;
@@ -488,11 +565,12 @@ cudaError_t backward(const EmbedArgs& a) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  const int per = a.H / VE;
-  const dim3 grid((unsigned)a.chunks, (unsigned)((per + kSumThreads - 1) / kSumThreads));
-  e = launch_after(embed_sum<E, VE>, grid, kSumThreads, 0, a.stream, a, buf);
+  const unsigned blocks = (unsigned)((a.H / VE + kSumThreads - 1) / kSumThreads);
+  const int fills = fill ? (a.V - filled + kFillRows - 1) / kFillRows : 0;
+  e = launch_after(a.add ? embed_sum<E, VE, true> : embed_sum<E, VE, false>, (unsigned)a.chunks * blocks + (unsigned)fills, kSumThreads, 0,
+                   a.stream, a, buf, filled, fills);
   if (e == cudaSuccess && a.chunks > 1)
-    e = launch_after(embed_join<E, VE>, grid, kSumThreads, 0, a.stream, a);
+    e = launch_after(embed_join<E, VE>, dim3((unsigned)a.chunks, blocks), kSumThreads, 0, a.stream, a);
   return e;
 }
 
