@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
   float top = -INFINITY, sum = 0.f, ref = 0.f;
   // one CTA a row, and rows long enough: one pass does the rest too, where a look at a part of
   // the row tells what to expect
-  const bool ahead = !HELD && !greedy && part.share >= 3 * 32 * kRing && (K <= 256 || !(TOP || cut_k));
+  const bool ahead = !HELD && !greedy && !classes && part.share >= 3 * 32 * kRing && (K <= 256 || !(TOP || cut_k));
   Weights ahead_w = {};
   u64 ahead_sum = 0;
   uint32_t first = 0xFFFFFFFFu;                  // greedy: the lowest id of the maximum
@@ -977,9 +977,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
       row.put_count(n);
     } else {
       ahead_w.set(seen, tau, a.V);             // (nothing seen: far)
-      if (classes) {
-        part.each(look);
-      } else if (!ahead_w.far) {
+      if (!ahead_w.far) {
         part.each([&](int v, const uint4& raw) {
           if (Vec<E>::top(raw) > ahead_w.z_cap) ahead_sum >>= min(63, ahead_w.raise(Vec<E>::top(raw)));
           look(v, raw);
@@ -1235,6 +1233,19 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
         }
       }
       const float z_hi = value_of(hi_key), z_lo = value_of(lo_key);
+      // bf16: the range has few different logits, of which there may be very many (a step of 1/16
+      // from 8 on), and they are counted instead of listed
+      constexpr int kKeys = kThreads;
+      const uint32_t k_hi = hi_key >> 16;
+      const bool by_key = sizeof(E) == 2 && k_hi - (lo_key >> 16) < (uint32_t)kKeys;
+      uint32_t* key_n = reinterpret_cast<uint32_t*>(sh.list);
+      u64* key_w = sh.list + kKeys;
+      if (by_key) {
+        const uint32_t k = k_hi - min(k_hi, (uint32_t)tid);
+        key_n[tid] = 0;
+        key_w[tid] = w(value_of(k & 0x8000u ? k << 16 : k << 16 | 0xFFFFu));
+        __syncthreads();
+      }
       // the exact mass, that above the range, and the list of those in it
       u64 mass = 0;
       int n = 0;
@@ -1249,7 +1260,13 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
           if (z[j] > z_hi) above += x;
           else if (z[j] >= z_lo) take |= 1u << j;
         }
-        n += row.put(v, take);
+        if (!by_key) {
+          n += row.put(v, take);
+        } else if (take) {
+#pragma unroll
+          for (int j = 0; j < VE; ++j)
+            if (take >> j & 1) atomicAdd(&key_n[k_hi - (key_of(z[j]) >> 16)], 1u);
+        }
       });
       row.put_count(n);
       mass = warp_sum(mass);
@@ -1258,10 +1275,68 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
       above = row.row_sum(own_above, before);
       target = top_p_target(top_p, mass);
       n = (int)sh.count;
+      if constexpr (sizeof(E) == 2) if (by_key && above < target) {
+        if (rank != 0 && key_n[tid]) atomicAdd(row.of(&key_n[tid], 0), key_n[tid]);
+        if (rank == 0 && tid < size) *row.of(&sh.slot[row.phase % kSlots][0], tid) = {0, 0, 0, 0};
+        row.sync();
+        if (rank == 0) {
+          const u64 x = key_n[tid] * key_w[tid], left = target - above;
+          u64 all;
+          const u64 run = row.scan(x, all);
+          if (x > 0 && run < left && run + x >= left) {
+            const u64 nth = (left - run + key_w[tid] - 1) / key_w[tid];
+            for (int r = 0; r < size; ++r)
+              *row.of(&sh.slot[row.phase % kSlots][0], r) = {nth, 1, k_hi - (uint32_t)tid, 0};
+          }
+        }
+        row.sync();
+        const Slot s = row.told()[0];
+        if (s.b != 0) {
+          // the `nth` of the logits equal to `z_b` is the border: this warp's kept ones, and its id
+          found = true;
+          const u64 nth = s.a, w_b = key_w[k_hi - s.c];
+          const uint32_t key_b = s.c & 0x8000u ? s.c << 16 : s.c << 16 | 0xFFFFu;
+          const float z_b = value_of(key_b);
+          u64 kept_mass = 0;
+          uint32_t ties = 0;
+          part.each([&](int, const uint4& raw) {
+            if (!(Vec<E>::top(raw) >= z_b)) return;
+            float z[VE];
+            Vec<E>::get(raw, z);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+              ties += z[j] == z_b;
+              if (z[j] > z_b && z[j] <= z_hi) kept_mass += key_w[k_hi - (key_of(z[j]) >> 16)];
+            }
+          });
+          const u64 own_ties = warp_sum((u64)ties);
+          u64 ties_before;
+          row.row_sum(own_ties, ties_before);
+          row.find(nth - 1, ties_before, own_ties,
+                   [&](int, const uint4& raw, u64 (&y)[VE]) {
+                     float z[VE];
+                     Vec<E>::get(raw, z);
+#pragma unroll
+                     for (int j = 0; j < VE; ++j) y[j] = z[j] == z_b;
+                   },
+                   [&](int id, u64) {
+                     row.tell_border((u64)key_b << 32 | (0xFFFFFFFFu - (uint32_t)id));
+                   });
+          b = row.told_border();
+          if (w_b >= least) {
+            const u64 kept_ties = nth > ties_before ? min(nth - ties_before, own_ties) : 0ull;
+            const u64 own = own_above + warp_sum(kept_mass) + kept_ties * w_b;
+            const u64 all = row.row_sum(own, before);
+            row.find(draw_target(a.uniform[t], all), before, own, kept,
+                     [&](int id, u64 x) { write_token(a, t, id, x, all); });
+            return;
+          }
+        }
+      }
       // (exact: what the classes said was only where to look)
-      if (n > kList && above < target)
+      if (!by_key && n > kList && above < target)
         found = row.template locate<true>(target, b, lo_key, hi_key, above, w);
-      if (n <= kList && above < target) {
+      if (!by_key && n <= kList && above < target) {
         if (rank == 0) {
           row.sort_list(n);
           if (tid == 0) sh.claim = 0;
