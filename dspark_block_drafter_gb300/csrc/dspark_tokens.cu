@@ -49,6 +49,12 @@ static dspark_status validate_embed(const dspark_embed_config* c) {
   return DSPARK_OK;
 }
 
+// Whether two arrays share memory.
+static bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return p && q && a < b + m && b < a + n;
+}
+
 static EmbedArgs embed_args(const dspark_embed_config* c) {
   EmbedArgs a{};
   a.T = c->T; a.V = c->V; a.H = c->H; a.dtype = c->dtype;
@@ -150,6 +156,9 @@ dspark_status dspark_embed(const dspark_embed_config* cfg, const void* table,
   st = check_elements({table, out}, element(cfg->dtype));
   if (st == DSPARK_OK) st = check_elements({ids}, 4);
   if (st != DSPARK_OK) return st;
+  const size_t row = (size_t)cfg->H * element(cfg->dtype);
+  if (overlap(out, cfg->T * row, table, cfg->V * row))
+    return fail(DSPARK_ERR_INVALID_ARG, "out overlaps the table");
   EmbedArgs a = embed_args(cfg);
   a.table = table; a.ids = ids; a.out = out;
   a.stream = (cudaStream_t)stream;
@@ -174,6 +183,10 @@ dspark_status dspark_embed_backward(const dspark_embed_config* cfg, const int32_
   st = check_elements({d_out, add, d_table}, element(cfg->dtype));
   if (st == DSPARK_OK) st = check_elements({ids}, 4);
   if (st != DSPARK_OK) return st;
+  const size_t row = (size_t)cfg->H * element(cfg->dtype);
+  if (overlap(d_table, cfg->V * row, d_out, cfg->T * row) ||
+      (add != d_table && overlap(d_table, cfg->V * row, add, cfg->V * row)))
+    return fail(DSPARK_ERR_INVALID_ARG, "d_table overlaps d_out, or add without being it");
   EmbedArgs a = embed_args(cfg);
   const size_t need = plan_embed_workspace((char*)workspace, &a);
   if (!workspace || !aligned(workspace, kAlign))

@@ -671,7 +671,7 @@ typedef struct dspark_sample_rows {
  * logp    device [T] fp32 or NULL: the token's log-probability among the kept ones
  *
  * Weights are cut to whole multiples of 2^-S of the largest, S = 62 - ceil(log2 V) (44 for
- * 151936 tokens), and off by at most 2^-28 of themselves besides; their sums are exact.  Needs no workspace; calls may overlap.
+ * 151936 tokens), and off by at most 2^-27 of themselves besides; their sums are exact.  Needs no workspace; calls may overlap.
  * Can be captured into a CUDA graph.
  */
 dspark_status dspark_sample(const dspark_sample_config* cfg, const dspark_sample_rows* rows,

@@ -1,9 +1,9 @@
 """Sampling, top logits and the embedding on a GB300 against their fp64 definitions.
 
 A drawn token is the definition's unless a border lies within 2^-26 of the mass of what it is
-compared with: a weight is off by at most 2^-28 of itself, and so are sums of them and their
-ratios to 2^-27.  A log-probability is log1p of the ratio of the other tokens' mass to the
-token's: 2^-27 from the weights, three fp32 roundings of 2^-24 and log1pf's two steps of 2^-23,
+compared with: a weight is off by at most 2^-27 of itself, and so are sums of them and their
+ratios to 2^-26.  A log-probability is log1p of the ratio of the other tokens' mass to the
+token's: 2^-26 from the weights, three fp32 roundings of 2^-24 and log1pf's two steps of 2^-23,
 which together stay below 2^-20 of the result.  Besides, a weight is cut to units of 2^-S of the
 largest, S = 62 - ceil(log2 V): V weights lose less than V 2^-S of it in all, and as the kept mass
 M is no less than the largest weight, the log of the token's share x / M moves by at most
