@@ -78,15 +78,39 @@ template <typename E, bool HELD>
 __device__ __forceinline__ void draw_listed(const RowArgs& a, Row<E, HELD>& row, int t, int n,
                                             const Weights& w, float top_p, float min_p) {
   Shared& sh = row.sh;
+  const u64 least = min_p_weight(min_p, w(w.m));
+  if (n <= 32) {
+    // one warp, without barriers
+    if (threadIdx.x >= 32) return;
+    const int lane = threadIdx.x;
+    const u64 e = lane < n ? sh.list[lane] : 0ull;
+    const uint32_t id = 0xFFFFFFFFu - (uint32_t)e;
+    u64 x = w(value_of(lane < n ? (uint32_t)(e >> 32) : kNoKey));
+    x = lane < n ? x : 0ull;
+    u64 in = warp_scan(x), all = __shfl_sync(0xFFFFFFFFu, in, 31);
+    if (top_p < 1.f && in - x >= top_p_target(top_p, all)) x = 0;
+    if (x < least) x = 0;
+    all = warp_sum(x);
+    u64 run = 0;
+#pragma unroll 8
+    for (int o = 0; o < n; ++o) {
+      const u64 y = __shfl_sync(0xFFFFFFFFu, x, o);
+      run += __shfl_sync(0xFFFFFFFFu, id, o) < id ? y : 0ull;
+    }
+    const u64 target = draw_target(a.uniform[t], all);
+    if (target >= run && target < run + x) write_token(a, t, (int)id, x, all);
+    return;
+  }
   constexpr int kEach = Row<E, HELD>::kEach;
   __shared__ int s_n;
   u64 x[kEach], all;
   if (top_p < 1.f) {
+    const int each = row.list_each(n);
     u64 run = row.list_weights(n, w, [](u64 e) { return (uint32_t)(e >> 32); }, x, all);
     const u64 target = top_p_target(top_p, all);
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-      if (x[q] > 0 && run < target && run + x[q] >= target) s_n = (int)threadIdx.x * kEach + q + 1;
+      if (x[q] > 0 && run < target && run + x[q] >= target) s_n = (int)threadIdx.x * each + q + 1;
       run += x[q];
     }
     __syncthreads();
@@ -97,7 +121,6 @@ __device__ __forceinline__ void draw_listed(const RowArgs& a, Row<E, HELD>& row,
   __syncthreads();
   row.sort_list(n);
   u64 run = row.list_weights(n, w, [](u64 e) { return (uint32_t)e; }, x, all);
-  const u64 least = min_p_weight(min_p, w(w.m));
   if (least > 0) {
     u64 s = 0;
 #pragma unroll
@@ -107,11 +130,12 @@ __device__ __forceinline__ void draw_listed(const RowArgs& a, Row<E, HELD>& row,
     }
     run = row.scan(s, all);
   }
+  const int each = row.list_each(n);
   const u64 target = draw_target(a.uniform[t], all);
 #pragma unroll
   for (int q = 0; q < kEach; ++q) {
     if (target >= run && target < run + x[q])
-      write_token(a, t, (int)(0xFFFFFFFFu - (uint32_t)(sh.list[threadIdx.x * kEach + q] >> 32)), x[q],
+      write_token(a, t, (int)(0xFFFFFFFFu - (uint32_t)(sh.list[threadIdx.x * each + q] >> 32)), x[q],
                   all);
     run += x[q];
   }
@@ -638,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
           row.list_weights(kept_n, w, [](u64 e) { return (uint32_t)(e >> 32); }, x, all);
 #pragma unroll
           for (int q = 0; q < kOf; ++q) {
-            const int i = tid * kOf + q;
-            if (i >= kept_n) continue;
+            const int i = tid * row.list_each(kept_n) + q;
+            if (q >= row.list_each(kept_n) || i >= kept_n) continue;
             const int id = (int)(0xFFFFFFFFu - (uint32_t)sh.list[i]), r = id / per;
             const E* g = (const E*)a.logits + (long long)t * a.ld + r * per;
             const int lead = (int)((uintptr_t)g / sizeof(E) % VE);

@@ -154,9 +154,9 @@ struct Weights {
 // The classes of weights: 1/64 of an octave each, by rounding; the last takes the rest.  The
 // class never falls as the logit does, whatever is rounded.
 struct Classes {
-  float m, c;               // where the first one is, 64 log2(e) / temperature
+  float m, c;               // the maximum, 64 log2(e) / temperature
   __device__ __forceinline__ float step(float z) const {
-    return fmaxf(fminf(__fmul_rn(__fsub_rn(m, z), c), (float)(kBins - 1)), 0.f);
+    return fminf(__fmul_rn(__fsub_rn(m, z), c), (float)(kBins - 1));
   }
   static __device__ __forceinline__ int of(float y) {
     return __float_as_int(__fadd_rn(y, 12582912.f)) - 0x4B400000;
@@ -562,22 +562,26 @@ struct Row {
       }
   }
 
-  // Weights of this CTA's first n list entries, kEach a thread in order, and the sum before the
+  // Weights of this CTA's first n list entries, list_each(n) a thread in order, and the sum before the
   // thread's; key_at(entry) is an entry's order key.
   static constexpr int kEach = kList / kThreads;
   template <typename W, typename F>
   __device__ __forceinline__ u64 list_weights(int n, const W& w, F key_at, u64 (&x)[kEach],
                                               u64& all) {
     u64 s = 0;
+    const int each = list_each(n);
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-      const int i = threadIdx.x * kEach + q;
+      x[q] = 0;
+      if (q >= each) continue;
+      const int i = threadIdx.x * each + q;
       const u64 y = w(value_of(i < n ? key_at(sh.list[i]) : kNoKey));
       x[q] = i < n ? y : 0ull;
       s += x[q];
     }
     return scan(s, all);
   }
+  static __device__ __forceinline__ int list_each(int n) { return n <= kThreads ? 1 : kEach; }
   // The first entry with which the mass of the sorted list reaches `target`, by one thread:
   // found(index, mass before it, its own).
   template <typename W, typename F>
@@ -587,7 +591,7 @@ struct Row {
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
       if (x[q] > 0 && run < target && run + x[q] >= target)
-        found((int)threadIdx.x * kEach + q, run, x[q]);
+        found((int)threadIdx.x * list_each(n) + q, run, x[q]);
       run += x[q];
     }
   }
