@@ -227,14 +227,14 @@ struct Part {
       x[j] = a + j >= lead && a + j < lead + n ? g[a + j] : (E)-INFINITY;
     return *reinterpret_cast<const uint4*>(x);
   }
+  static __device__ __forceinline__ void copy16(uint32_t to, const uint4* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  }
   // Vector v to `to` in shared memory, without waiting for it.
   __device__ __forceinline__ void copy(int v, uint4* to) const {
     const int a = v * VE;
     if (a >= lead && a + VE <= lead + n)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                       (uint32_t)__cvta_generic_to_shared(to)),
-                   "l"(reinterpret_cast<const uint4*>(g) + v)
-                   : "memory");
+      copy16((uint32_t)__cvta_generic_to_shared(to), reinterpret_cast<const uint4*>(g) + v);
     else
       *to = load(v);
   }
@@ -269,24 +269,30 @@ struct Part {
       }
       return;
     }
+    // kRing / 2 pairs of vectors on their way; whole ones only (the first and the last of a row may
+    // not be)
+    constexpr uint32_t kSlot = kThreads * 16, kAll = kRing * kSlot;
     uint4* ring = held + threadIdx.x;
+    const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+    const int whole = min(v1, (lead + n) / VE);
 #pragma unroll
     for (int q = 0; q < kRing; ++q) {
-      if (v0 + 32 * q + lane < v1) copy(v0 + 32 * q + lane, ring + q * kThreads);
-      copied();
+      const int v = v0 + 32 * q + lane;
+      if (v < whole) copy(v, ring + q * kThreads);
+      if (q % 2) copied();
     }
+    const uint4* src = reinterpret_cast<const uint4*>(g) + v0 + 32 * kRing + lane;
+    uint32_t at = 0;
     // two at a time, so that their arithmetic overlaps
-    int at = 0;
-    for (int b = v0; b < v1; b += 64) {
-      arrived<kRing - 2>();
-      const int v = b + lane, far = v + 32 * kRing;
-      const uint4 x = v < v1 ? ring[at] : Vec<E>::none();
-      const uint4 y = v + 32 < v1 ? ring[at + kThreads] : Vec<E>::none();
-      if (far < v1) copy(far, ring + at);
+    for (int v = v0 + lane; v - lane < v1; v += 64, src += 64) {
+      arrived<kRing / 2 - 1>();
+      uint4 x = ring[at / 16], y = ring[(at + kSlot) / 16];
+      if (v >= whole) x = v < v1 ? load(v) : Vec<E>::none();
+      if (v + 32 >= whole) y = v + 32 < v1 ? load(v + 32) : Vec<E>::none();
+      if (v + 32 * kRing < whole) copy16(ring_s + at, src);
+      if (v + 32 * kRing + 32 < whole) copy16(ring_s + at + kSlot, src + 32);
       copied();
-      if (far + 32 < v1) copy(far + 32, ring + at + kThreads);
-      copied();
-      at = at == (kRing - 2) * kThreads ? 0 : at + 2 * kThreads;
+      at = (at + 2 * kSlot) % kAll;
       f(v, x);
       f(v + 32, y);
     }
