@@ -77,7 +77,7 @@ __device__ __forceinline__ u64 min_p_weight(float p, u64 top) {
 template <typename E, bool HELD>
 __device__ __forceinline__ void draw_listed(const RowArgs& a, Row<E, HELD>& row, int t, int n,
                                             const Weights& w, float top_p, float min_p) {
-  Shared& sh = row.sh;
+  auto& sh = row.sh;
   const u64 least = min_p_weight(min_p, w(w.m));
   if (n <= 32) {
     // one warp, without barriers
@@ -144,10 +144,12 @@ __device__ __forceinline__ void draw_listed(const RowArgs& a, Row<E, HELD>& row,
 template <typename E, bool TOP, bool HELD>
 __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
   extern __shared__ uint4 s_held[];
-  __shared__ Shared sh;
+  using R = Row<E, HELD>;
+  constexpr int kList = R::kList;
+  __shared__ typename R::Sh sh;
   constexpr int VE = Vec<E>::n;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  Row<E, HELD> row(sh);
+  R row(sh);
   const int rank = row.rank(), size = row.size(), t = blockIdx.x / size;
   const int per = ((a.V + size - 1) / size + VE - 1) / VE * VE;
   Part<E, HELD>& part = row.part;

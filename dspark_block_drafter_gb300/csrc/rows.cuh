@@ -24,7 +24,7 @@ namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048, kList = 2048;
+constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kNoKey = 0x007FFFFFu;       // the order key of -infinity
 constexpr int kSlots = 4;
@@ -43,13 +43,16 @@ struct Slot {
   uint32_t c, d;
 };
 
+// LIST: entries of a list.
+template <int LIST>
 struct Shared {
+  static constexpr int kList = LIST;
   union {
     struct {
       uint32_t cnt[kBins], lo[kBins], hi[kBins];
     } h;
     struct {
-      u64 list[kList];
+      u64 list[LIST];
       uint32_t mass[kBins];         // of this CTA's elements, in the first CTA then of all
     };
   };
@@ -325,11 +328,14 @@ __device__ __forceinline__ T warp_scan(T v) {              // inclusive
 template <typename E, bool HELD>
 struct Row {
   static constexpr int VE = Vec<E>::n;
-  Shared& sh;
+  // (a CTA that holds no part of its row has room for a longer list)
+  using Sh = Shared<HELD ? 2048 : 4096>;
+  static constexpr int kList = Sh::kList;
+  Sh& sh;
   Part<E, HELD> part;
   int phase;
 
-  __device__ __forceinline__ Row(Shared& s) : sh(s), phase(0) {}
+  __device__ __forceinline__ Row(Sh& s) : sh(s), phase(0) {}
   __device__ __forceinline__ int size() const {
     return HELD ? (int)cg::this_cluster().num_blocks() : 1;
   }
@@ -662,7 +668,7 @@ struct Row {
         const int i = threadIdx.x * each + q;
         if (q >= each || i >= per) continue;
         for (int r = 0; r < size(); ++r) {
-          const Shared* o = of(&sh, r);
+          const Sh* o = of(&sh, r);
           const int at = rank() * per + i;
           c[q] += o->h.cnt[at];
           if (MASS) x[q] += (u64)o->h.hi[at] << 32 | o->h.lo[at];
