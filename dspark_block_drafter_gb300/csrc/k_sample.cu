@@ -13,14 +13,14 @@
 // (76 KB of each for 151936 fp32 logits in 8, two CTAs a SM), read from memory once, and every
 // later pass is one over shared memory.  CTAs tell each other by stores into all of their shared
 // memories before a barrier of the cluster, and read only their own after it.  Many long rows:
-// one CTA each, which reads its row again for every pass (1.2 MB in flight of every SM's two
-// rows' passes keep the memory busy where barriers of clusters did not: a greedy token of 2048
-// fp32 rows 503 us held by clusters, 196 by single CTAs, 184 the floor).
+// one CTA each, which reads its row again for every pass (the 128 KB that two CTAs have in flight
+// keep the memory busy where barriers of clusters did not: a greedy token of 2048 fp32 rows 503 us
+// held by clusters, 198 by single CTAs, 184 the floor).
 //
 //   top_k, and the k largest: a list of what is not below the least of some groups' maxima; with
 //     at least k groups it holds the k largest.  Single CTAs look at a ninth of the row first and
 //     list what is not below a bound that some twice k will reach, in the pass that reads the
-//     row (the 64 largest of 2048 fp32 rows: 494 us in two passes, 326 in one).  One CTA sorts the
+//     row (the 64 largest of 2048 fp32 rows: 494 us in two passes, 300 in one).  One CTA sorts the
 //     list, and does the rest alone.
 //   nothing but a draw: single CTAs sum the weights in the pass that reads the row, in units that
 //     the look at its ninth gives, and rise by octaves where that was too low.
@@ -28,8 +28,7 @@
 //     (32-bit sums by shared memory atomics); then, in one pass, the exact mass, that of the
 //     classes surely kept, and a list of the few classes that the border may lie in, or for bf16
 //     the counts of their logits.  The draw takes its sums by warp from that pass.  (2048 fp32 rows,
-//     p 0.95: 1.39 ms, 107 instructions for 32 logits, at 2.6 a clock and SM: bound by their issue,
-//     as the weights take 24 of them.)
+//     p 0.95: 1.25 ms, 95 instructions for 32 logits, at 2.5 a clock and SM: bound by their issue.)
 //   Where a list does not do (more entries than it holds, many equal logits): histograms of the
 //     logits' order keys, 2048 bins at a time, with exact masses.
 #include <cuda_bf16.h>
@@ -351,9 +350,11 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
         if (s[r].c > kNoKey)
           total += __uint_as_float((uint32_t)s[r].a) *
                    fast_exp2(value_of(s[r].c) * kLog2e - top_ref);
-      if (!(total >= 0.f)) {
-        // a logit is no number, or infinite: the sum of those that are
-        const float m = value_of(key);
+      const float m = value_of(key);
+      const bool plain = fabsf(top_ref) < INFINITY && total > 0.f && total < INFINITY;
+      if (key > kNoKey && !plain) {
+        // a logit is no number, or so large that the reference is none: the sum of those that are,
+        // from their distances
         float s1 = 0.f;
         part.each([&](int v, const uint4& raw) {
           float z[VE];
@@ -378,9 +379,9 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
         for (int r = 0; r < size; ++r) total += __uint_as_float((uint32_t)o[r].a);
       }
       if (rank == 0 && tid == 0)
-        a.lse[t] = key <= kNoKey                ? -INFINITY
-                   : value_of(key) == INFINITY ? INFINITY
-                                               : (top_ref + log2f(total)) * 0.693147181f;
+        a.lse[t] = key <= kNoKey ? -INFINITY
+                   : plain       ? (top_ref + log2f(total)) * 0.693147181f
+                                 : m + logf(total);
     }
   }
   const Border every = {kNoKey, -1};             // all but -infinity

@@ -62,9 +62,13 @@ def draw(z, u, dtype="f32", pad=0, lead=0, rows=None, **settings):
     return x.double().cpu().numpy(), tokens.cpu().numpy(), logp.cpu().numpy()
 
 
-def check_draw(z, u, rows=None, most_near=0.02, **kw):
+def check_draw(z, u, rows=None, most_near=0.02, of=None, **kw):
+    """`of`: the call's rows and numbers, and which of them z and u are."""
     settings = {k: kw[k] for k in ("temperature", "top_k", "top_p", "min_p") if k in kw}
-    x, tokens, logp = draw(z, u, rows=rows, **kw)
+    if of is None:
+        x, tokens, logp = draw(z, u, rows=rows, **kw)
+    else:
+        x, tokens, logp = (r[of[2]] for r in draw(of[0], of[1], rows=rows, **kw))
     close = 0
     for t in range(len(z)):
         own = {k: float(np.float32(v)) for k, v in settings.items()}
@@ -85,6 +89,7 @@ def check_draw(z, u, rows=None, most_near=0.02, **kw):
 
 
 SETTINGS = [dict(), dict(temperature=0.7, top_k=20, top_p=0.8), dict(top_p=0.9), dict(top_k=50),
+            dict(top_p=0.95, min_p=0.05), dict(top_p=0.99, min_p=0.5),
             dict(min_p=0.05), dict(top_k=300, min_p=0.01, temperature=1.7), dict(top_k=1),
             dict(temperature=0.0, top_p=0.5), dict(top_p=0.0), dict(top_k=7, top_p=0.99, min_p=0.2)]
 
@@ -93,7 +98,8 @@ SETTINGS = [dict(), dict(temperature=0.7, top_k=20, top_p=0.8), dict(top_p=0.9),
 @pytest.mark.parametrize("T,V,dtype", [(1, 1, "f32"), (5, 2, "bf16"), (3, 7, "f32"), (9, 64, "bf16"),
                                        (40, 1000, "f32"), (17, 4099, "bf16"), (170, 5000, "f32"),
                                        (6, 32003, "bf16"), (3, 151936, "f32"),
-                                       (2, 151936, "bf16")])
+                                       (2, 151936, "bf16"), (2, 262144, "f32"), (1, 390001, "f32"),
+                                       (1, 780001, "bf16")])
 def test_sample(T, V, dtype, settings):
     rng = np.random.default_rng(T * V + len(settings))
     check_draw(_rows(rng, T, V, "zipf"), rng.uniform(size=T), dtype=dtype, **settings)
@@ -184,6 +190,67 @@ def test_sample_rows_apart(pad, lead, dtype):
         check_draw(z, u, dtype=dtype, pad=pad, lead=lead)
 
 
+def _many(rng, T, V, kind, some=9):
+    """Rows that are read by one CTA each: `some` different ones, over and over."""
+    return np.tile(_rows(rng, some, V, kind), (T // some + 1, 1))[:T]
+
+
+@pytest.mark.parametrize("settings", SETTINGS + [dict(top_k=200), dict(top_k=250, top_p=0.9)], ids=str)
+@pytest.mark.parametrize("T,V,dtype", [(64, 22001, "f32"), (64, 43003, "bf16"), (70, 49999, "f32"),
+                                       (66, 60001, "f32"), (64, 100003, "bf16"), (65, 151936, "bf16")])
+def test_sample_many_long_rows(T, V, dtype, settings):
+    rng = np.random.default_rng(V + len(settings))
+    z, u = _many(rng, T, V, "zipf"), rng.uniform(size=T)
+    check_draw(z[::7], u[::7], of=(z, u, slice(None, None, 7)), dtype=dtype, pad=1, **settings)
+
+
+@pytest.mark.parametrize("kind", ["flat", "wide", "equal", "few", "low"])
+@pytest.mark.parametrize("settings", [dict(), dict(top_p=0.6), dict(top_k=2500, top_p=0.5),
+                                      dict(top_k=30, top_p=0.7), dict(temperature=8.0, top_p=0.95),
+                                      dict(min_p=1.0), dict(temperature=0.01),
+                                      dict(top_p=0.9, min_p=0.5)], ids=str)
+@pytest.mark.parametrize("V,dtype", [(60001, "f32"), (100003, "bf16")])
+def test_sample_many_flat_and_tied_rows(kind, settings, V, dtype):
+    rng = np.random.default_rng(len(kind))
+    T = 64
+    z, u = _many(rng, T, V, kind), (rng.integers(0, V, T) + 0.5) / V
+    check_draw(z[::9], u[::9], of=(z, u, slice(None, None, 9)), dtype=dtype, **settings)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sample_many_masked_rows(dtype):
+    """What the first ninth of a row shows says nothing of the rest."""
+    rng = np.random.default_rng(11)
+    T, V = 64, 110001
+    z = _many(rng, T, V, "zipf", 16)
+    z[0] = -INF
+    z[1] = np.nan
+    z[2] = -INF
+    z[2, V - 1] = 2.0                                  # only the last is left
+    z[3, :V - 5] = -INF                                # only the last five
+    z[4, :V // 2] = np.nan
+    z[5, 90000] = INF
+    z[6] = np.arange(V) * 1e-3                         # rising: every part has a larger one
+    z[7] = -np.arange(V) * 1e-3
+    z[8] = np.finfo(np.float32).min
+    z[9, 1000:] -= 200.0                               # all of it in the first share
+    z[10, 7000::7] = -INF
+    u = rng.uniform(size=T)
+    for settings in (dict(), dict(top_k=3), dict(top_p=0.5), dict(top_k=40, top_p=0.3, min_p=0.1),
+                     dict(temperature=0.0), dict(temperature=3.0, top_p=0.9), dict(min_p=0.3)):
+        check_draw(z[:12], u[:12], of=(z, u, slice(0, 12)), dtype=dtype, **settings)
+    check_top(z[:64], 40, dtype, rows=range(12))
+    check_top(z[:64], 300, dtype, rows=range(12), lse=False)
+
+
+@pytest.mark.parametrize("k", [1, 64, 256, 1000])
+@pytest.mark.parametrize("V,dtype", [(25000, "f32"), (60001, "f32"), (100003, "bf16")])
+def test_top_logits_many_long_rows(V, dtype, k):
+    rng = np.random.default_rng(k)
+    check_top(_many(rng, 65, V, "zipf"), k, dtype, pad=3, rows=range(0, 65, 9))
+    check_top(_many(rng, 64, V, "few"), k, dtype, rows=range(0, 64, 20))
+
+
 @pytest.mark.parametrize("dtype,V", [("f32", 500_001), ("bf16", 900_007)])
 def test_sample_rows_that_no_cluster_holds(dtype, V):
     rng = np.random.default_rng(5)
@@ -192,7 +259,7 @@ def test_sample_rows_that_no_cluster_holds(dtype, V):
         check_draw(z, u, dtype=dtype, **settings)
 
 
-def check_top(z, k, dtype="f32", pad=0, lead=0, lse=True):
+def check_top(z, k, dtype="f32", pad=0, lead=0, lse=True, rows=None):
     from dspark_block_drafter_gb300 import torch_io as tio
     T, V = z.shape
     x = _tensor(z, dtype, pad, lead)
@@ -202,7 +269,7 @@ def check_top(z, k, dtype="f32", pad=0, lead=0, lse=True):
     tio.top_logits(x, ids, values, lse=sums)
     torch.cuda.synchronize()
     x = x.double().cpu().numpy()
-    for t in range(T):
+    for t in range(T) if rows is None else rows:
         i, v, s = to.top_row(x[t], k)
         assert np.array_equal(ids[t].cpu().numpy(), i)
         assert np.array_equal(values[t].double().cpu().numpy(), v)
@@ -334,6 +401,26 @@ def grad(T, V, H, dtype, scale=1.0, add=None, ids=None, kind="skewed", seed=0):
 @pytest.mark.parametrize("add", [None, "other", "same"])
 def test_embed_backward(T, V, H, dtype, add):
     grad(T, V, H, dtype, add=add)
+
+
+@pytest.mark.parametrize("lead", [1, 3, 4])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_embed_backward_alignments(dtype, lead):
+    """`add` and the table at different places within 16 bytes."""
+    from dspark_block_drafter_gb300 import torch_io as tio
+    T, V, H = 40, 300, 64
+    g = torch.Generator(device="cuda").manual_seed(lead)
+    ids = torch.randint(V, (T,), generator=g, device="cuda").int()
+    flat = [torch.randn(n * H + lead, generator=g, device="cuda").to(DT[dtype]) for n in (V, V, T)]
+    for moved in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0)):
+        add, table, d = (f[lead * m:lead * m + n * H].view(n, H)
+                         for f, m, n in zip(flat, moved, (V, V, T)))
+        cfg = tio.make_embed_config(T, V, H, dtype)
+        tio.embed_backward(cfg, ids, d, table, tio.embed_workspace_for(cfg), add=add)
+        want, mag = to.embed_backward(ids.cpu().numpy(), d.double().cpu().numpy(), V, 1.0,
+                                      add.double().cpu().numpy())
+        bound = OUT[dtype] * np.abs(want) + 36 * 2.0 ** -24 * mag * (1 + OUT[dtype])
+        assert np.all(np.abs(table.double().cpu().numpy() - want) <= bound)
 
 
 @pytest.mark.parametrize("kind", ["one", "all", "none"])
