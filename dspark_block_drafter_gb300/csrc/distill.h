@@ -33,8 +33,9 @@ constexpr int kDistillDone = 6;       // control word: row CTAs whose loss is wr
 
 cudaError_t launch_distill_targets(const DistillPlan& d);             // label, row, log_q, mass
 cudaError_t launch_distill_logits(const DistillPlan& d);              // z, w, after the loss's plan
-cudaError_t launch_distill_loss(const DistillPlan& d);                // losses and total
-// q's entries of the listed tokens among columns [v0, v1)
+// losses and total; with `entries` (one piece) q's entries of the listed tokens too
+cudaError_t launch_distill_loss(const DistillPlan& d, bool entries);
+// q's entries of the listed tokens among columns [v0, v1), after the losses without them
 cudaError_t launch_distill_entries(const DistillPlan& d, int v0, int v1);
 
 }  // namespace dspark

@@ -185,13 +185,13 @@ static cudaError_t run_loss(const LossPlan& p, const DistillPlan* d) {
   const bool keep = p.grads && p.pieces == 1;
   e = logits(p, 0, p.Vh, true, keep);
   if (e == cudaSuccess) e = launch_loss_rows(p, keep);
-  if (e == cudaSuccess && d) e = launch_distill_loss(*d);
+  if (e == cudaSuccess && d) e = launch_distill_loss(*d, keep);
   if (e != cudaSuccess || !p.grads) return e;
   for (int c = 0; c < p.pieces; ++c) {
     const int v0 = c * p.piece_cols, v1 = std::min(p.Vh, v0 + p.piece_cols);
     if (!keep) e = logits(p, v0, v1, false, true);
     if (e == cudaSuccess && !keep && !tc) e = launch_loss_dz_f32(p, v0, v1);
-    if (e == cudaSuccess && d) e = launch_distill_entries(*d, v0, v1);
+    if (e == cudaSuccess && d && !keep) e = launch_distill_entries(*d, v0, v1);
     if (e == cudaSuccess) e = grads(p, v0, v1, c == 0);
     if (e != cudaSuccess) return e;
   }

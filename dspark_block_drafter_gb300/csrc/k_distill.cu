@@ -175,9 +175,30 @@ __device__ __forceinline__ float minus_log_p(const DistillPlan& d, int i, int k,
   return j == d.p.lab[i] ? label_loss : lse - d.z[(size_t)i * d.k + k];
 }
 
-// One warp a compact row: its loss; the last CTA takes the total.  `d.z` then holds
-// log q - log p, and log p's own is not needed any more.
+// The entry of the logits' gradient at listed token k of compact row i, column j, where v0 <= j:
+// q columns start at v0.  x: log q - log p.
+template <typename E>
+__device__ __forceinline__ void put_entry(const LossPlan& p, int i, int j, int v0, float w, float mass,
+                                          float lq, float x, bool low) {
+  E* q = (E*)p.q + (size_t)i * p.ldq + (j - v0);
+  // (far below: as the difference, where expm1 could overflow)
+  const float g = w * (x > -1.f ? expf(lq) * (mass * expm1f(-x) + (mass - 1.f))
+                                : mass * expf(lq - x) - expf(lq));
+  if constexpr (sizeof(E) == 4) {
+    *q = g;
+  } else if (j == p.lab[i]) {
+    loss_put_label(p, i, low, q, g);
+  } else {
+    const __nv_bfloat16 b = __float2bfloat16(g);
+    *q = b;
+    if (low) q[kLossLow * p.ldq] = __float2bfloat16(g - __bfloat162float(b));
+  }
+}
+
+// One warp a compact row: its loss, and with ENTRIES (the vocabulary in one piece) its listed
+// entries; the last CTA takes the total.  `d.z` then holds log q - log p.
 constexpr int kLossThreads = 256;
+template <typename E, bool ENTRIES>
 __global__ void __launch_bounds__(kLossThreads) distill_loss(const DistillPlan d) {
   pdl_wait();
   pdl_signal();
@@ -188,14 +209,16 @@ __global__ void __launch_bounds__(kLossThreads) distill_loss(const DistillPlan d
   const int i = blockIdx.x * (kLossThreads / 32) + threadIdx.x / 32;
   if (i < n_tok) {
     const int t = p.tok[i];
-    const float lse = p.lse[i], nll = p.loss[t];
+    const float lse = p.lse[i], nll = p.loss[t], w = d.w[i], mass = d.mass[t];
+    const bool low = ENTRIES && sizeof(E) == 2 && loss_low(p, n_tok);
     Sum2 s;
     for (int k = lane; k < d.k; k += 32) {
       const int j = d.row[(size_t)t * d.k + k];
       if (j < 0) continue;
       const float lq = d.log_q[(size_t)t * d.k + k];
       const float x = lq + minus_log_p(d, i, k, j, lse, nll);
-      d.z[(size_t)i * d.k + k] = x;
+      if (ENTRIES) put_entry<E>(p, i, j, 0, w, mass, lq, x, low);
+      else d.z[(size_t)i * d.k + k] = x;
       const float q = expf(lq);
       // (0 log 0 is 0)
       s.add(q > 0.f || q != q ? q * x : 0.f);
@@ -227,26 +250,13 @@ __global__ void __launch_bounds__(256) distill_entries(const DistillPlan d, int 
   const int n_tok = (int)p.ctrl[kLossTok], lane = threadIdx.x % 32;
   const int i = blockIdx.x * 8 + threadIdx.x / 32;
   if (i >= n_tok) return;
-  const int t = p.tok[i], label = p.lab[i];
+  const int t = p.tok[i];
   const float w = d.w[i], mass = d.mass[t];
   const bool low = loss_low(p, n_tok);
-  E* q = (E*)p.q + (size_t)i * p.ldq;
   for (int k = lane; k < d.k; k += 32) {
     const int j = d.row[(size_t)t * d.k + k];
-    if (j < v0 || j >= v1) continue;
-    const float lq = d.log_q[(size_t)t * d.k + k], x = d.z[(size_t)i * d.k + k];
-    // (far below: as the difference, where expm1 could overflow)
-    const float g = x > -1.f ? expf(lq) * (mass * expm1f(-x) + (mass - 1.f))
-                             : mass * expf(lq - x) - expf(lq);
-    if constexpr (sizeof(E) == 4) {
-      q[j - v0] = w * g;
-    } else if (j == label) {
-      loss_put_label(p, i, low, q + (j - v0), w * g);
-    } else {
-      const __nv_bfloat16 b = __float2bfloat16(w * g);
-      q[j - v0] = b;
-      if (low) q[kLossLow * p.ldq + (j - v0)] = __float2bfloat16(w * g - __bfloat162float(b));
-    }
+    if (j >= v0 && j < v1)
+      put_entry<E>(p, i, j, v0, w, mass, d.log_q[(size_t)t * d.k + k], d.z[(size_t)i * d.k + k], low);
   }
 }
 
@@ -263,8 +273,12 @@ cudaError_t launch_distill_logits(const DistillPlan& d) {
   return launch_after(kernel, dim3((unsigned)d.p.T, y), kDotThreads, 0, d.p.stream, d);
 }
 
-cudaError_t launch_distill_loss(const DistillPlan& d) {
-  return launch_after(distill_loss, (unsigned)(d.p.T + 7) / 8, kLossThreads, 0, d.p.stream, d);
+cudaError_t launch_distill_loss(const DistillPlan& d, bool entries) {
+  const bool f32 = d.p.dtype == 0;
+  return launch_after(!entries ? distill_loss<float, false>
+                      : f32    ? distill_loss<float, true>
+                               : distill_loss<__nv_bfloat16, true>,
+                      (unsigned)(d.p.T + 7) / 8, kLossThreads, 0, d.p.stream, d);
 }
 
 cudaError_t launch_distill_entries(const DistillPlan& d, int v0, int v1) {
