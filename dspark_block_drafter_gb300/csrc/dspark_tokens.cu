@@ -72,12 +72,12 @@ static size_t plan_embed_workspace(char* ws, EmbedArgs* a) {
   };
   const size_t T = (size_t)a->T, parts = (size_t)a->chunks * 2;
   a->ctrl = take(64);
+  a->there = (uint8_t*)take(((size_t)a->V + 3) / 4);
   for (int i = 0; i < 2; ++i) {
     a->key[i] = take(T);
     a->pos[i] = take(T);
   }
   a->hist = take(embed_hist_words(*a));
-  a->there = take(((size_t)a->V + 31) / 32);
   a->part_tok = (int32_t*)take(parts);
   a->part = (float*)take(parts * a->H);
   return off;

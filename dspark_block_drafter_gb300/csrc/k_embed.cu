@@ -10,7 +10,7 @@
 // that ends in its chunk is written to the table; the parts of one that chunks share are
 // joined by a last kernel, in order.  Rows of the table that no token asks for are written
 // beside the sort and the sums, which both wait for their loads more than they use the memory:
-// by a bit map of the tokens, or before there is one by looking at every token.
+// by a map of the tokens, or before there is one by looking at every token.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -184,14 +184,12 @@ __device__ void sort_all(const EmbedArgs& a, uint32_t* smem) {
     }
     __syncthreads();
   }
-  // the sorted list, and the bits of its tokens
-  for (int i = threadIdx.x; i < (a.V + 31) / 32; i += kSortThreads) a.there[i] = 0;
-  __syncthreads();
+  // the sorted list, and its tokens' places in the map
   for (int i = threadIdx.x; i < a.T; i += kSortThreads) {
     const uint32_t k = s_key[i];
     a.key[0][i] = k;
     a.pos[0][i] = s_pos[i];
-    if (k < (uint32_t)a.V && (i == 0 || s_key[i - 1] != k)) atomicOr(&a.there[k / 32], 1u << k % 32);
+    if (k < (uint32_t)a.V) a.there[k] = 1;
   }
 }
 
@@ -259,7 +257,7 @@ __global__ void __launch_bounds__(256) embed_mark(const EmbedArgs a) {
   const uint32_t k = sort_key(a, t);
   a.key[1][t] = k;
   a.pos[1][t] = (uint32_t)t;
-  if (k < (uint32_t)a.V) atomicOr(&a.there[k / 32], 1u << k % 32);
+  if (k < (uint32_t)a.V) a.there[k] = 1;
 }
 
 // Counts of the digits at `shift` of tile blockIdx.x.
@@ -287,10 +285,15 @@ __global__ void __launch_bounds__(kSortThreads) embed_offsets(const EmbedArgs a,
 #pragma unroll 8
   for (int i = i0; i < i1; ++i) s += a.hist[i];
   uint32_t at = block_before(s, s_warp);
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t c = a.hist[i];
-    a.hist[i] = at;
-    at += c;
+  for (int i = i0; i < i1; i += 8) {
+    uint32_t c[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) c[q] = i + q < i1 ? a.hist[i + q] : 0u;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (i + q < i1) a.hist[i + q] = at;
+      at += c[q];
+    }
   }
 }
 
@@ -363,9 +366,9 @@ __device__ __forceinline__ void get_part(const float* from, float (&s)[VE]) {
 // loads of several rows in flight.
 template <typename E, int VE, bool ADD>
 __device__ __forceinline__ void sum_chunk(const EmbedArgs& a, int buf, int chunk, int block,
-                                          uint32_t* s_key, uint32_t* s_pos) {
+                                          uint32_t* s_key, uint32_t* s_pos, Pack<E, VE>* s_add) {
   using P = Pack<E, VE>;
-  constexpr int kAt = VE == 1 ? 16 : ADD ? 4 : 8;
+  constexpr int kAt = VE == 1 ? 16 : 8;
   constexpr uint32_t kEnd = 1u << 31;                   // the run ends with this row
   const int tid = threadIdx.x, i0 = chunk * a.chunk, size = min(a.chunk, a.T - i0);
   const uint32_t V = (uint32_t)a.V;
@@ -401,13 +404,20 @@ __device__ __forceinline__ void sum_chunk(const EmbedArgs& a, int buf, int chunk
 #pragma unroll 1
   for (int b = 0; b < n; b += kAt) {
     P x[kAt];
-    P y[ADD ? kAt : 1];
+    P y[ADD && VE == 1 ? kAt : 1];
 #pragma unroll
     for (int q = 0; q < kAt; ++q) {
       const int i = min(b + q, n - 1);
       x[q] = d[(size_t)(s_pos[i] & ~kEnd) * per];
-      if (ADD && (s_pos[i] & kEnd)) y[q] = add[(size_t)key[i] * per];
+      // (what runs are added to: by way of shared memory where registers are short)
+      if (ADD && VE == 1 && (s_pos[i] & kEnd)) y[q] = add[(size_t)key[i] * per];
+      if (ADD && VE > 1 && (s_pos[i] & kEnd))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(&s_add[q * kSumThreads + tid])),
+                     "l"(add + (size_t)key[i] * per)
+                     : "memory");
     }
+    if (ADD && VE > 1) asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
     for (int q = 0; q < kAt; ++q) {
       const int i = b + q;
@@ -425,7 +435,10 @@ __device__ __forceinline__ void sum_chunk(const EmbedArgs& a, int buf, int chunk
         if (shared_before || shared_after)
           put_part<VE>(a.part + ((size_t)chunk * 2 + !shared_before) * a.H + (size_t)c * VE, acc);
         else
-          put_sum<E, VE>(a, k, c, acc, ADD ? &y[ADD ? q : 0] : nullptr);
+          put_sum<E, VE>(a, k, c, acc,
+                         !ADD      ? nullptr
+                         : VE == 1 ? &y[ADD && VE == 1 ? q : 0]
+                                   : &s_add[q * kSumThreads + tid]);
       }
 #pragma unroll
       for (int j = 0; j < VE; ++j) acc[j] = 0.f;
@@ -445,52 +458,98 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum(const EmbedArgs a, i
   pdl_wait();
   pdl_signal();
   __shared__ uint32_t s_key[kMaxChunk + 2], s_pos[kMaxChunk];
+  __shared__ Pack<E, VE> s_add[ADD && VE > 1 ? 8 * kSumThreads : 1];
   const long long b = blockIdx.x, all = gridDim.x;
   const int before = (int)(b * fills / all);            // fill CTAs before this one
   if ((int)((b + 1) * fills / all) > before) {
     const int first = v0 + before * kFillRows, end = min(a.V, first + kFillRows);
     for (int v = first + threadIdx.x / 32; v < end; v += kSumThreads / 32)
-      if (!(a.there[v / 32] >> v % 32 & 1u)) fill_row<E>(a, (size_t)v);
+      if (!a.there[v]) fill_row<E>(a, (size_t)v);
     return;
   }
   const int i = (int)b - before, blocks = (a.H / VE + kSumThreads - 1) / kSumThreads;
-  sum_chunk<E, VE, ADD>(a, buf, i / blocks, i % blocks, s_key, s_pos);
+  sum_chunk<E, VE, ADD>(a, buf, i / blocks, i % blocks, s_key, s_pos, s_add);
 }
 
 // CTA (chunk, column block): the token whose run starts in this chunk and goes on in the next
-// ones.  The parts' rounding errors are carried along.
+// ones.  Long runs are summed in thirds by three groups of threads, with their rounding errors,
+// and the thirds are joined in order.  (A token in most of 16000 rows has some 300 parts: one
+// thread for all of a column's took 75 us.)
+constexpr int kJoinGroups = 3, kJoinThreads = kJoinGroups * kSumThreads;
+constexpr int kJoinLong = 12;            // parts of a long run
+template <int VE>
+__device__ __forceinline__ void add_part(float (&s)[VE], float (&e)[VE], const float (&x)[VE]) {
+#pragma unroll
+  for (int j = 0; j < VE; ++j) {
+    const float t = s[j] + x[j], y = t - s[j];
+    e[j] += (s[j] - (t - y)) + (x[j] - y);
+    s[j] = t;
+  }
+}
 template <typename E, int VE>
-__global__ void __launch_bounds__(kSumThreads) embed_join(const EmbedArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) embed_join(const EmbedArgs a) {
   pdl_wait();
   pdl_signal();
-  const int chunk = blockIdx.x, v = a.part_tok[chunk * 2 + 1];
+  __shared__ int s_end;
+  __shared__ float s_sum[(kJoinGroups - 1) * kSumThreads * VE * 2];
+  const int chunk = blockIdx.x, v = a.part_tok[chunk * 2 + 1], tid = threadIdx.x;
   if (v < 0) return;
-  const int per = a.H / VE, c = blockIdx.y * kSumThreads + threadIdx.x;
-  if (c >= per) return;
-  float s[VE], e[VE];
-  const float* p = a.part + (size_t)c * VE;
-  get_part<VE>(p + ((size_t)chunk * 2 + 1) * a.H, s);
+  // the first chunk after the run
+  int end = a.chunks;
+  for (int q0 = chunk + 1; q0 < a.chunks && end == a.chunks; q0 += kJoinThreads) {
+    __syncthreads();
+    if (tid == 0) s_end = a.chunks;
+    __syncthreads();
+    const int q = q0 + tid;
+    if (q < a.chunks && a.part_tok[q * 2] != v) atomicMin(&s_end, q);
+    __syncthreads();
+    end = s_end;
+  }
+  const int parts = end - chunk - 1, group = tid / kSumThreads, col = tid % kSumThreads;
+  const bool split = parts >= kJoinLong;
+  if (!split && group > 0) return;
+  const int groups = split ? kJoinGroups : 1;
+  const int q0 = chunk + 1 + (int)((long long)parts * group / groups);
+  const int q1 = chunk + 1 + (int)((long long)parts * (group + 1) / groups);
+  const int per = a.H / VE, c = blockIdx.y * kSumThreads + col;
+  const bool in = c < per;
+  float s[VE] = {}, e[VE] = {};
+  const float* p = a.part + (size_t)(in ? c : 0) * VE;
+  if (group == 0) get_part<VE>(p + ((size_t)chunk * 2 + 1) * a.H, s);
+  constexpr int kAt = VE == 8 ? 4 : 8;
+  for (int q = q0; q < q1; q += kAt) {
+    float x[kAt][VE];
 #pragma unroll
-  for (int j = 0; j < VE; ++j) e[j] = 0.f;
-  bool more = true;
-  for (int q0 = chunk + 1; more && q0 < a.chunks; q0 += 4) {
-    float x[4][VE];
+    for (int o = 0; o < kAt; ++o) get_part<VE>(p + (size_t)min(q + o, q1 - 1) * 2 * a.H, x[o]);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      more = more && q0 + q < a.chunks && a.part_tok[(q0 + q) * 2] == v;
-      if (more) get_part<VE>(p + (size_t)(q0 + q) * 2 * a.H, x[q]);
-#pragma unroll
-      for (int j = 0; j < VE; ++j) x[q][j] = more ? x[q][j] : 0.f;
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int o = 0; o < kAt; ++o)
+      if (q + o < q1) add_part<VE>(s, e, x[o]);
+  }
+  if (split) {
+    // (value by value, so that neighbours' lie in different banks)
+    float* mine = s_sum + (group - 1) * kSumThreads * VE * 2 + col;
+    if (group > 0) {
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
-        const float t = s[j] + x[q][j], y = t - s[j];
-        e[j] += (s[j] - (t - y)) + (x[q][j] - y);
-        s[j] = t;
+        mine[j * kSumThreads] = s[j];
+        mine[(VE + j) * kSumThreads] = e[j];
       }
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < kJoinGroups; ++g) {
+      const float* other = s_sum + (g - 1) * kSumThreads * VE * 2 + col;
+      float x[VE];
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        x[j] = other[j * kSumThreads];
+        e[j] += other[(VE + j) * kSumThreads];
+      }
+      add_part<VE>(s, e, x);
+    }
   }
+  if (!in) return;
 #pragma unroll
   for (int j = 0; j < VE; ++j) s[j] += e[j];
   if (a.add) {
@@ -541,7 +600,8 @@ cudaError_t sort_one(const EmbedArgs& a, bool fill, int* filled) {
 
 template <typename E, int VE>
 cudaError_t backward(const EmbedArgs& a) {
-  cudaError_t e = cudaMemsetAsync(a.ctrl, 0, 256, a.stream);
+  // (the map follows the control words)
+  cudaError_t e = cudaMemsetAsync(a.ctrl, 0, 256 + (size_t)a.V, a.stream);
   const bool fill = a.add != a.d_table;
   int buf = 0, filled = 0;
   if (e == cudaSuccess && a.T <= kSortAll) {
@@ -550,8 +610,6 @@ cudaError_t backward(const EmbedArgs& a) {
         : a.T <= 8 * kSortThreads ? sort_one<E, 8>(a, fill, &filled)
                                   : sort_one<E, 16>(a, fill, &filled);
   } else if (e == cudaSuccess) {
-    e = cudaMemsetAsync(a.there, 0, ((size_t)a.V + 31) / 32 * 4, a.stream);
-    if (e != cudaSuccess) return e;
     embed_mark<<<(a.T + 255) / 256, 256, 0, a.stream>>>(a);
     const int tiles = (a.T + kTile - 1) / kTile;
     const int passes = (a.bits + kDigit - 1) / kDigit, width = (a.bits + passes - 1) / passes;
@@ -570,7 +628,7 @@ cudaError_t backward(const EmbedArgs& a) {
   e = launch_after(a.add ? embed_sum<E, VE, true> : embed_sum<E, VE, false>, (unsigned)a.chunks * blocks + (unsigned)fills, kSumThreads, 0,
                    a.stream, a, buf, filled, fills);
   if (e == cudaSuccess && a.chunks > 1)
-    e = launch_after(embed_join<E, VE>, dim3((unsigned)a.chunks, blocks), kSumThreads, 0, a.stream, a);
+    e = launch_after(embed_join<E, VE>, dim3((unsigned)a.chunks, blocks), kJoinThreads, 0, a.stream, a);
   return e;
 }
 

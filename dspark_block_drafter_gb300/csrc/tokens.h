@@ -43,7 +43,7 @@ struct EmbedArgs {
   uint32_t* ctrl;
   uint32_t *key[2], *pos[2];         // [T] (token, row) pairs while and after they are sorted
   uint32_t* hist;                    // [bins][tiles] digit counts of the tiles of a sort
-  uint32_t* there;                   // [ceil(V / 32)] bit of every token that occurs
+  uint8_t* there;                    // [V] behind ctrl's 256 bytes: 1 for a token that occurs
   float* part;                       // [chunks][2][H] sums of tokens that chunks share
   int32_t* part_tok;                 // [chunks][2] their tokens, -1: none
   int bits, chunk, chunks;
