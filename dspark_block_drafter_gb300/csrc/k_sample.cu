@@ -15,7 +15,8 @@
 // memories before a barrier of the cluster, and read only their own after it.  Many long rows:
 // one CTA each, which reads its row again for every pass (the 128 KB that two CTAs have in flight
 // keep the memory busy where barriers of clusters did not: a greedy token of 2048 fp32 rows 503 us
-// held by clusters, 198 by single CTAs, 184 the floor).
+// held by clusters, 198 by single CTAs, 184 the floor).  Where their settings differ, the rows
+// that no list serves are begun first.
 //
 //   top_k, and the k largest: a list of what is not below the least of some groups' maxima; with
 //     at least k groups it holds the k largest.  Single CTAs look at a ninth of the row first and
@@ -73,8 +74,8 @@ __device__ __forceinline__ u64 min_p_weight(float p, u64 top) {
 
 // The first CTA alone: the draw from the list's n best entries, which hold the k first of the
 // row's order (k entries or all there are).
-template <typename E, bool HELD>
-__device__ __forceinline__ void draw_listed(const RowArgs& a, Row<E, HELD>& row, int t, int n,
+template <typename E, bool HELD, int NT>
+__device__ __forceinline__ void draw_listed(const RowArgs& a, Row<E, HELD, NT>& row, int t, int n,
                                             const Weights& w, float top_p, float min_p) {
   auto& sh = row.sh;
   const u64 least = min_p_weight(min_p, w(w.m));
@@ -100,7 +101,7 @@ __device__ __forceinline__ void draw_listed(const RowArgs& a, Row<E, HELD>& row,
     if (target >= run && target < run + x) write_token(a, t, (int)id, x, all);
     return;
   }
-  constexpr int kEach = Row<E, HELD>::kEach;
+  constexpr int kEach = Row<E, HELD, NT>::kEach, kThreads = NT;
   __shared__ int s_n;
   u64 x[kEach], all;
   if (top_p < 1.f) {
@@ -140,18 +141,18 @@ __device__ __forceinline__ void draw_listed(const RowArgs& a, Row<E, HELD>& row,
   }
 }
 
-template <typename E, bool TOP, bool HELD>
-__global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
+template <typename E, bool TOP, bool HELD, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
   extern __shared__ uint4 s_held[];
-  using R = Row<E, HELD>;
-  constexpr int kList = R::kList;
+  using R = Row<E, HELD, NT>;
+  constexpr int kList = R::kList, kThreads = NT, kWarps = NT / 32;
   __shared__ typename R::Sh sh;
   constexpr int VE = Vec<E>::n;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   R row(sh);
-  const int rank = row.rank(), size = row.size(), t = blockIdx.x / size;
+  const int rank = row.rank(), size = row.size(), t = HELD ? blockIdx.x / size : blockIdx.x % a.T;
   const int per = ((a.V + size - 1) / size + VE - 1) / VE * VE;
-  Part<E, HELD>& part = row.part;
+  auto& part = row.part;
   {
     part.i0 = min(a.V, rank * per);
     part.n = min(a.V, part.i0 + per) - part.i0;
@@ -181,6 +182,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
   const bool greedy = !TOP && (!(tau > 0.f) || K == 1);
   const bool cut_k = !greedy && K < a.V, cut_p = !TOP && !greedy && top_p < 1.f;
   const bool classes = cut_p && !cut_k;
+  // (a row that no list serves takes ten times as long as one that does: those are begun first)
+  if (!HELD && a.long_first && (!greedy && !cut_k) != (blockIdx.x < a.T)) return;
   if (tid == 0) {
     sh.count = sh.claim = 0;
     sh.least_id = 0xFFFFFFFFu;
@@ -251,11 +254,12 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
     const int some = min(part.v1, part.v0 + 32 * kRing);
     float best = -INFINITY;
     part.each(part.v0, some, [&](int, const uint4& x) { best = fmaxf(best, Vec<E>::top(x)); });
-    // half a warp's maxima
+    // 32 maxima: of warps, or of half ones
+    constexpr int kOfLanes = kWarps;
     float m = best;
 #pragma unroll
-    for (int o = 1; o < 16; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (lane % 16 == 0) sh.half_top[warp * 2 + lane / 16] = m;
+    for (int o = 1; o < kOfLanes; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (lane % kOfLanes == 0) sh.half_top[tid / kOfLanes] = m;
     __syncthreads();
     m = sh.half_top[lane];
     const float seen = warp_top(m);
@@ -660,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowArgs a) {
           const int kept_n = (int)sh.claim;
           if (kept_n == 0 && tid < size) *row.of(&sh.slot[phase % kSlots][0], tid) = {0, 0, 0, 0};
           // the kept entries' masses, for the warps that hold them
-          constexpr int kOf = Row<E, HELD>::kEach;
+          constexpr int kOf = R::kEach;
           u64 x[kOf], all;
           row.list_weights(kept_n, w, [](u64 e) { return (uint32_t)(e >> 32); }, x, all);
 #pragma unroll
@@ -735,23 +739,43 @@ cudaError_t launch_rows(const RowArgs& a) {
   while (c < kMaxCluster && (bytes(c) > 84 * 1024 || (a.T * c < 152 && a.V / c >= 4096))) c *= 2;
   const bool held = bytes(c) <= 196 * 1024 && (a.T < 64 || bytes(1) <= 84 * 1024);
   if (!held) c = 1;
-  const size_t smem = held ? bytes(c) : kRing * kThreads * 16;
-  auto pick = [&](auto e, auto top, auto in) {
-    return rows_kernel<typename decltype(e)::type, decltype(top)::value, decltype(in)::value>;
+  // Threads of a row that no cluster holds.  Two CTAs of 512 a SM overlap their barriers; where rows
+  // that no list serves are few, one of 1024 has its row sooner.  (p 0.9, 152 rows of 151936 fp32
+  // logits: 176 us with 512, 139 with 1024; 304 rows 248 and 273.  Rows of different settings, one
+  // in five such, bf16: 544 rows 257 and 196, 1024 rows 308 and 325.)
+  const bool own = a.row_temperature || a.row_top_p || a.row_top_k;
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  const bool many = !held && a.tokens &&
+                    (own ? a.T <= 4 * sms : a.T <= sms && a.top_k <= 0 && a.temperature > 0.f);
+  const int nt = many ? 1024 : 512;
+  const size_t smem = held ? bytes(c) : (size_t)kRing * nt * 16;
+  auto pick = [&](auto e, auto top, auto in, auto threads) {
+    return rows_kernel<typename decltype(e)::type, decltype(top)::value, decltype(in)::value,
+                       decltype(threads)::value>;
   };
   auto of_type = [&](auto e) {
     using Yes = std::true_type;
     using No = std::false_type;
-    return a.tokens ? (held ? pick(e, No{}, Yes{}) : pick(e, No{}, No{}))
-                    : (held ? pick(e, Yes{}, Yes{}) : pick(e, Yes{}, No{}));
+    using Some = std::integral_constant<int, 512>;
+    using Many = std::integral_constant<int, 1024>;
+    if (!a.tokens) return held ? pick(e, Yes{}, Yes{}, Some{}) : pick(e, Yes{}, No{}, Some{});
+    return held   ? pick(e, No{}, Yes{}, Some{})
+           : many ? pick(e, No{}, No{}, Many{})
+                  : pick(e, No{}, No{}, Some{});
   };
   void (*kernel)(RowArgs) =
       a.dtype == 0 ? of_type(std::common_type<float>{}) : of_type(std::common_type<__nv_bfloat16>{});
-  cudaError_t e = raise_smem_limit((const void*)kernel, smem);
+  e = raise_smem_limit((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.T * c);
-  cfg.blockDim = dim3(kThreads);
+  // rows of different settings: one CTA each for the long ones, then one each for the others (2048
+  // rows: 498 us instead of 577)
+  RowArgs r = a;
+  r.long_first = !held && own;
+  cfg.gridDim = dim3((unsigned)a.T * (r.long_first ? 2 : c));
+  cfg.blockDim = dim3((unsigned)nt);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
   cudaLaunchAttribute attr[1];
@@ -761,7 +785,7 @@ cudaError_t launch_rows(const RowArgs& a) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, r);
 }
 
 }  // namespace dspark

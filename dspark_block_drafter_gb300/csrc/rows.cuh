@@ -23,7 +23,6 @@ namespace {
 namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kNoKey = 0x007FFFFFu;       // the order key of -infinity
@@ -43,10 +42,10 @@ struct Slot {
   uint32_t c, d;
 };
 
-// LIST: entries of a list.
-template <int LIST>
+// LIST: entries of a list; NT: threads.
+template <int LIST, int NT>
 struct Shared {
-  static constexpr int kList = LIST;
+  static constexpr int kList = LIST, kWarps = NT / 32;
   union {
     struct {
       uint32_t cnt[kBins], lo[kBins], hi[kBins];
@@ -59,7 +58,7 @@ struct Shared {
   Slot slot[kSlots][kMaxCluster];
   u64 warp_sum[kWarps], extra[kWarps];
   uint32_t warp_key[kWarps], warp_top[kWarps];
-  float warp_f[kWarps], half_top[2 * kWarps];
+  float warp_f[kWarps], half_top[32];
   uint32_t count;                   // entries of the list, told to every CTA
   uint32_t claim;                   // entries that have a place in the first CTA's list
   uint32_t least_id;
@@ -212,9 +211,9 @@ struct Vec<__nv_bfloat16> {
 // HELD: they are in shared memory once they have been read; otherwise every pass reads them
 // from memory again, through a ring of kRing places for each thread.
 constexpr int kRing = 8;
-template <typename E, bool HELD>
+template <typename E, bool HELD, int NT>
 struct Part {
-  static constexpr int VE = Vec<E>::n;
+  static constexpr int VE = Vec<E>::n, kThreads = NT;
   const E* g;               // the 16-byte boundary at or before element i0
   uint4* held;              // the vectors in shared memory, or the ring
   int i0, n, lead, nv;      // lead: elements before i0 in the first vector
@@ -325,14 +324,14 @@ __device__ __forceinline__ T warp_scan(T v) {              // inclusive
 }
 
 // HELD: a cluster of `size` CTAs; otherwise one CTA.
-template <typename E, bool HELD>
+template <typename E, bool HELD, int NT>
 struct Row {
-  static constexpr int VE = Vec<E>::n;
+  static constexpr int VE = Vec<E>::n, kThreads = NT, kWarps = NT / 32;
   // (a CTA that holds no part of its row has room for a longer list)
-  using Sh = Shared<HELD ? 2048 : 4096>;
+  using Sh = Shared<HELD ? 2048 : 4096, NT>;
   static constexpr int kList = Sh::kList;
   Sh& sh;
-  Part<E, HELD> part;
+  Part<E, HELD, NT> part;
   int phase;
 
   __device__ __forceinline__ Row(Sh& s) : sh(s), phase(0) {}

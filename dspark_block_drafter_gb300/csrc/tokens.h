@@ -24,6 +24,7 @@ struct RowArgs {
   const float* uniform;
   int32_t* tokens;
   float* logp;
+  bool long_first;                   // (of the launch: two CTAs a row, see k_sample.cu)
   // the largest
   int k;
   int32_t* ids;

@@ -72,7 +72,7 @@ def check_draw(z, u, rows=None, most_near=0.02, of=None, **kw):
     close = 0
     for t in range(len(z)):
         own = {k: float(np.float32(v)) for k, v in settings.items()}
-        own.update({k: v[t] for k, v in (rows or {}).items()})
+        own.update({k: (v if of is None else v[of[2]])[t] for k, v in (rows or {}).items()})
         tok, lp, near = to.sample_row(x[t], np.float32(u[t]), **own)
         if near < NEAR:
             close += 1
@@ -197,7 +197,8 @@ def _many(rng, T, V, kind, some=9):
 
 @pytest.mark.parametrize("settings", SETTINGS + [dict(top_k=200), dict(top_k=250, top_p=0.9)], ids=str)
 @pytest.mark.parametrize("T,V,dtype", [(64, 22001, "f32"), (64, 43003, "bf16"), (70, 49999, "f32"),
-                                       (66, 60001, "f32"), (64, 100003, "bf16"), (65, 151936, "bf16")])
+                                       (66, 60001, "f32"), (64, 100003, "bf16"), (65, 151936, "bf16"),
+                                       (200, 50001, "f32")])
 def test_sample_many_long_rows(T, V, dtype, settings):
     rng = np.random.default_rng(V + len(settings))
     z, u = _many(rng, T, V, "zipf"), rng.uniform(size=T)
@@ -212,9 +213,23 @@ def test_sample_many_long_rows(T, V, dtype, settings):
 @pytest.mark.parametrize("V,dtype", [(60001, "f32"), (100003, "bf16")])
 def test_sample_many_flat_and_tied_rows(kind, settings, V, dtype):
     rng = np.random.default_rng(len(kind))
-    T = 64
-    z, u = _many(rng, T, V, kind), (rng.integers(0, V, T) + 0.5) / V
-    check_draw(z[::9], u[::9], of=(z, u, slice(None, None, 9)), dtype=dtype, **settings)
+    for T in (64, 160):                                # (one CTA a SM, two)
+        z, u = _many(rng, T, V, kind), (rng.integers(0, V, T) + 0.5) / V
+        check_draw(z[::19], u[::19], of=(z, u, slice(None, None, 19)), dtype=dtype, **settings)
+
+
+@pytest.mark.parametrize("T", [66, 700])
+@pytest.mark.parametrize("dtype,V", [("f32", 50001), ("bf16", 100003)])
+def test_sample_many_rows_of_different_settings(T, dtype, V):
+    rng = np.random.default_rng(T)
+    rows = dict(temperature=rng.choice([0.0, 0.7, 1.0, 2.0], T).astype(np.float32),
+                top_k=rng.choice([0, 1, 20, 300, V + 1], T).astype(np.int32),
+                top_p=rng.choice([0.5, 0.95, 1.0], T).astype(np.float32),
+                min_p=rng.choice([0.0, 0.1], T).astype(np.float32))
+    z, u, at = _many(rng, T, V, "zipf"), rng.uniform(size=T), slice(None, None, T // 33)
+    x, tokens, logp = draw(z, u, dtype, rows=rows)
+    assert np.all((tokens >= 0) & (tokens < V)) and np.all(logp <= 0)
+    check_draw(z[at], u[at], of=(z, u, at), dtype=dtype, rows=rows)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
