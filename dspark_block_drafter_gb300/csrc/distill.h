@@ -25,7 +25,8 @@ struct DistillPlan {
                              // rows' tokens, compact head rows once their logits are known
   float* log_q;              // [T][k]
   float* mass;               // [T] sum of q
-  float* z;                  // [Tp][k] logits of the listed tokens of the compact rows
+  float* z;                  // [Tp][k] logits of the listed tokens of the compact rows; with
+                             // several pieces -log p of them once it is known
   float* w;                  // [Tp] w_t of the compact rows (LossPlan::wrow has w_t times mass)
 };
 

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "common.cuh"
 #include "distill.h"
@@ -59,7 +60,8 @@ __global__ void __launch_bounds__(128) distill_targets(const DistillPlan d) {
     row[q] = j;
     if (j < 0) continue;
     none = false;
-    x[q] = d.scale * s;
+    // (a mask of the type's lowest value stays a number under a factor above 1)
+    x[q] = isfinite(s) ? fminf(fmaxf(d.scale * s, -FLT_MAX), FLT_MAX) : d.scale * s;
     top = x[q] == x[q] ? fmaxf(top, x[q]) : top;
     first = min(first, k);
   }
@@ -176,14 +178,15 @@ __device__ __forceinline__ float minus_log_p(const DistillPlan& d, int i, int k,
 }
 
 // The entry of the logits' gradient at listed token k of compact row i, column j, where v0 <= j:
-// q columns start at v0.  x: log q - log p.
+// q columns start at v0.
 template <typename E>
 __device__ __forceinline__ void put_entry(const LossPlan& p, int i, int j, int v0, float w, float mass,
-                                          float lq, float x, bool low) {
+                                          float lq, float minus_lp, bool low) {
   E* q = (E*)p.q + (size_t)i * p.ldq + (j - v0);
-  // (far below: as the difference, where expm1 could overflow)
+  // (far below, which log q of -infinity is too: as the difference, where expm1 could overflow)
+  const float x = lq + minus_lp;
   const float g = w * (x > -1.f ? expf(lq) * (mass * expm1f(-x) + (mass - 1.f))
-                                : mass * expf(lq - x) - expf(lq));
+                                : mass * expf(-minus_lp) - expf(lq));
   if constexpr (sizeof(E) == 4) {
     *q = g;
   } else if (j == p.lab[i]) {
@@ -196,7 +199,7 @@ __device__ __forceinline__ void put_entry(const LossPlan& p, int i, int j, int v
 }
 
 // One warp a compact row: its loss, and with ENTRIES (the vocabulary in one piece) its listed
-// entries; the last CTA takes the total.  `d.z` then holds log q - log p.
+// entries; the last CTA takes the total.  `d.z` then holds -log p.
 constexpr int kLossThreads = 256;
 template <typename E, bool ENTRIES>
 __global__ void __launch_bounds__(kLossThreads) distill_loss(const DistillPlan d) {
@@ -216,10 +219,10 @@ __global__ void __launch_bounds__(kLossThreads) distill_loss(const DistillPlan d
       const int j = d.row[(size_t)t * d.k + k];
       if (j < 0) continue;
       const float lq = d.log_q[(size_t)t * d.k + k];
-      const float x = lq + minus_log_p(d, i, k, j, lse, nll);
-      if (ENTRIES) put_entry<E>(p, i, j, 0, w, mass, lq, x, low);
-      else d.z[(size_t)i * d.k + k] = x;
-      const float q = expf(lq);
+      const float minus_lp = minus_log_p(d, i, k, j, lse, nll);
+      if (ENTRIES) put_entry<E>(p, i, j, 0, w, mass, lq, minus_lp, low);
+      else d.z[(size_t)i * d.k + k] = minus_lp;
+      const float q = expf(lq), x = lq + minus_lp;
       // (0 log 0 is 0)
       s.add(q > 0.f || q != q ? q * x : 0.f);
     }

@@ -39,7 +39,7 @@ def _near(got, want, bound, name):
 
 def run(T, H, V, r, k, dtype, form="full", n_emit=None, reduction="mean", loss_scale=1.0, pieces=0,
         weighted=False, ignored=0, grads="all", seed=0, lse=False, t_scale=1.0, lists="mixed",
-        poison=False, std=None, spread=3.0):
+        poison=False, std=None, spread=3.0, masked=None):
     from dspark_block_drafter_gb300 import torch_io as tio
     rng = np.random.default_rng(seed)
     n_emit = n_emit or V
@@ -69,6 +69,10 @@ def run(T, H, V, r, k, dtype, form="full", n_emit=None, reduction="mean", loss_s
             s[t, n:] = np.nan                     # (what an absent token brings is not read)
         for t in range(1, T, 5):
             s[t, rng.integers(0, k):] = -np.inf
+    if masked is not None:                        # (some tokens of a row, or all)
+        of = rng.uniform(size=(T, k)) < 0.4
+        of[T // 2] = True
+        s[of & np.isfinite(s)] = masked
     off = rng.permutation(T)[:ignored]
     ids[off] = -1
     prev = rng.integers(0, V, T).astype(np.int32)
@@ -146,6 +150,17 @@ CASES = [
     dict(T=100, H=64, V=1024, r=16, k=50, lse=True, std=3.0, weighted=True),
 ]
 
+
+
+@pytest.mark.parametrize("masked", [-3.4028234e38, -1e9, -1e4])
+@pytest.mark.parametrize("t_scale", [0.5, 1.0, 2.0])
+@pytest.mark.parametrize("dtype,pieces", [("f32", 0), ("f32", 3), ("bf16", 0), ("bf16", 3)])
+def test_listed_tokens_masked_by_a_number(masked, t_scale, dtype, pieces):
+    """Their q is 0 and their entry of the gradient Q p, not what log q - (log q - log p) leaves."""
+    for T in (9, 130):
+        out, o, _ = run(T, 64, 1000, 16, 20, dtype, masked=masked, t_scale=t_scale, pieces=pieces,
+                        std=0.3)
+        check(out, o, dtype)
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(f"{k}{v}" for k, v in c.items()))
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
