@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const EmbedArgs a) {
   }
   if (!in) return;
 #pragma unroll
-  for (int j = 0; j < VE; ++j) s[j] += e[j];
+  for (int j = 0; j < VE; ++j) s[j] += isfinite(s[j]) ? e[j] : 0.f;     // (inf - inf is in e)
   if (a.add) {
     const Pack<E, VE> x = reinterpret_cast<const Pack<E, VE>*>(a.add)[(size_t)v * per + c];
     put_sum<E, VE>(a, (size_t)v, c, s, &x);
@@ -625,8 +625,9 @@ cudaError_t backward(const EmbedArgs& a) {
   if (e != cudaSuccess) return e;
   const unsigned blocks = (unsigned)((a.H / VE + kSumThreads - 1) / kSumThreads);
   const int fills = fill ? (a.V - filled + kFillRows - 1) / kFillRows : 0;
-  e = launch_after(a.add ? embed_sum<E, VE, true> : embed_sum<E, VE, false>, (unsigned)a.chunks * blocks + (unsigned)fills, kSumThreads, 0,
-                   a.stream, a, buf, filled, fills);
+  e = launch_after(a.add ? embed_sum<E, VE, true> : embed_sum<E, VE, false>,
+                   (unsigned)a.chunks * blocks + (unsigned)fills, kSumThreads, 0, a.stream, a, buf,
+                   filled, fills);
   if (e == cudaSuccess && a.chunks > 1)
     e = launch_after(embed_join<E, VE>, dim3((unsigned)a.chunks, blocks), kJoinThreads, 0, a.stream, a);
   return e;

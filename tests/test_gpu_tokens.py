@@ -446,6 +446,25 @@ def test_embed_backward_tokens(kind, T, V):
     grad(T, V, 24, "bf16", kind=kind, add="same")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [50, 100, 5000])
+def test_embed_backward_infinities(T, dtype):
+    """A sum with an infinity is that infinity, in one chunk or over many; inf - inf is NaN."""
+    from dspark_block_drafter_gb300 import torch_io as tio
+    H = 8
+    d = torch.ones(T, H, device="cuda", dtype=DT[dtype])
+    d[T // 3, 1] = d[T // 2, 2] = d[T // 3, 3] = float("inf")
+    d[T // 2, 3] = d[T - 1, 4] = float("-inf")
+    d[0, 5] = float("nan")
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    table = torch.empty(3, H, device="cuda", dtype=DT[dtype])
+    cfg = tio.make_embed_config(T, 3, H, dtype)
+    tio.embed_backward(cfg, ids, d, table, tio.embed_workspace_for(cfg))
+    want = d.double().sum(0).to(DT[dtype])
+    assert torch.allclose(table[0], want, rtol=0, atol=0, equal_nan=True)
+    assert not table[1:].any()
+
+
 @pytest.mark.parametrize("T", [100, 20000])
 def test_embed_backward_tokens_outside(T):
     rng = np.random.default_rng(1)
