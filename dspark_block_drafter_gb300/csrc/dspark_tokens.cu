@@ -55,6 +55,27 @@ static bool overlap(const void* p, size_t n, const void* q, size_t m) {
   return p && q && a < b + m && b < a + n;
 }
 
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+// Refuses outputs that share memory with an input or with one another: rows of one launch are read
+// and written in no order.
+static dspark_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span& o : outs) {
+    for (const Span& i : ins)
+      if (overlap(o.p, o.n, i.p, i.n)) return fail(DSPARK_ERR_INVALID_ARG, "an output overlaps an input");
+    for (const Span& i : outs)
+      if (&i != &o && overlap(o.p, o.n, i.p, i.n))
+        return fail(DSPARK_ERR_INVALID_ARG, "two outputs overlap");
+  }
+  return DSPARK_OK;
+}
+static size_t rows_bytes(int32_t T, int32_t V, int64_t ld, int32_t dtype) {
+  return ((size_t)(T - 1) * (size_t)ld + (size_t)V) * element(dtype);
+}
+
 static EmbedArgs embed_args(const dspark_embed_config* c) {
   EmbedArgs a{};
   a.T = c->T; a.V = c->V; a.H = c->H; a.dtype = c->dtype;
@@ -108,6 +129,12 @@ dspark_status dspark_sample(const dspark_sample_config* cfg, const dspark_sample
   if (st == DSPARK_OK && rows)
     st = check_elements({rows->top_k, rows->temperature, rows->top_p, rows->min_p}, 4);
   if (st != DSPARK_OK) return st;
+  const size_t each = 4 * (size_t)cfg->T;
+  const dspark_sample_rows own = rows ? *rows : dspark_sample_rows{};
+  st = check_apart({{tokens, each}, {logp, each}},
+                   {{logits, rows_bytes(cfg->T, cfg->V, cfg->ld, cfg->dtype)}, {uniform, each},
+                    {own.top_k, each}, {own.temperature, each}, {own.top_p, each}, {own.min_p, each}});
+  if (st != DSPARK_OK) return st;
   RowArgs a{};
   a.T = cfg->T; a.V = cfg->V; a.ld = cfg->ld; a.dtype = cfg->dtype;
   a.logits = logits;
@@ -137,6 +164,10 @@ dspark_status dspark_top_logits(int32_t T, int32_t V, int64_t ld, int32_t dtype,
   st = check_elements({logits}, element(dtype));
   if (st == DSPARK_OK) st = check_elements({ids, values, lse}, 4);
   if (st != DSPARK_OK) return st;
+  const size_t each = 4 * (size_t)T;
+  st = check_apart({{ids, each * k}, {values, each * k}, {lse, each}},
+                   {{logits, rows_bytes(T, V, ld, dtype)}});
+  if (st != DSPARK_OK) return st;
   RowArgs a{};
   a.T = T; a.V = V; a.ld = ld; a.dtype = dtype;
   a.logits = logits;
@@ -157,8 +188,8 @@ dspark_status dspark_embed(const dspark_embed_config* cfg, const void* table,
   if (st == DSPARK_OK) st = check_elements({ids}, 4);
   if (st != DSPARK_OK) return st;
   const size_t row = (size_t)cfg->H * element(cfg->dtype);
-  if (overlap(out, cfg->T * row, table, cfg->V * row))
-    return fail(DSPARK_ERR_INVALID_ARG, "out overlaps the table");
+  st = check_apart({{out, cfg->T * row}}, {{table, cfg->V * row}, {ids, 4 * (size_t)cfg->T}});
+  if (st != DSPARK_OK) return st;
   EmbedArgs a = embed_args(cfg);
   a.table = table; a.ids = ids; a.out = out;
   a.stream = (cudaStream_t)stream;
@@ -184,9 +215,10 @@ dspark_status dspark_embed_backward(const dspark_embed_config* cfg, const int32_
   if (st == DSPARK_OK) st = check_elements({ids}, 4);
   if (st != DSPARK_OK) return st;
   const size_t row = (size_t)cfg->H * element(cfg->dtype);
-  if (overlap(d_table, cfg->V * row, d_out, cfg->T * row) ||
-      (add != d_table && overlap(d_table, cfg->V * row, add, cfg->V * row)))
-    return fail(DSPARK_ERR_INVALID_ARG, "d_table overlaps d_out, or add without being it");
+  st = check_apart({{d_table, cfg->V * row}},
+                   {{d_out, cfg->T * row}, {ids, 4 * (size_t)cfg->T},
+                    {add == d_table ? nullptr : add, cfg->V * row}});
+  if (st != DSPARK_OK) return st;
   EmbedArgs a = embed_args(cfg);
   const size_t need = plan_embed_workspace((char*)workspace, &a);
   if (!workspace || !aligned(workspace, kAlign))

@@ -671,8 +671,9 @@ typedef struct dspark_sample_rows {
  * logp    device [T] fp32 or NULL: the token's log-probability among the kept ones
  *
  * Weights are cut to whole multiples of 2^-S of the largest, S = 62 - ceil(log2 V) (44 for
- * 151936 tokens), and off by at most 2^-27 of themselves besides; their sums are exact.  Needs no workspace; calls may overlap.
- * Can be captured into a CUDA graph.
+ * 151936 tokens), and off by at most 2^-27 of themselves besides; their sums are exact.  tokens
+ * and logp overlap nothing else.  Needs no workspace; calls may run at once.  Can be captured into
+ * a CUDA graph.
  */
 dspark_status dspark_sample(const dspark_sample_config* cfg, const dspark_sample_rows* rows,
                             const void* logits, const float* uniform, int32_t* tokens,
@@ -688,7 +689,8 @@ dspark_status dspark_sample(const dspark_sample_config* cfg, const dspark_sample
  *         -infinity stand (absent, for dspark_distill_loss)
  * lse     device [T] fp32 or NULL: log sum exp of the row (NaN left out)
  *
- * Needs no workspace; calls may overlap.  Can be captured into a CUDA graph.
+ * The outputs overlap nothing else.  Needs no workspace; calls may run at once.  Can be captured
+ * into a CUDA graph.
  */
 dspark_status dspark_top_logits(int32_t T, int32_t V, int64_t ld, int32_t dtype, int32_t k,
                                 const void* logits, int32_t* ids, float* values, float* lse,
@@ -707,7 +709,7 @@ typedef struct dspark_embed_config {
  * dspark_embed -- out[t] = scale * table[ids[t]].
  *
  * table   device [V, H]      ids  device [T] int32; a row whose id is outside [0, V) is zeros
- * out     device [T, H], rounded once; must not overlap the table
+ * out     device [T, H], rounded once; overlaps nothing else
  */
 dspark_status dspark_embed(const dspark_embed_config* cfg, const void* table,
                            const int32_t* ids, void* out, void* stream);

@@ -41,7 +41,11 @@ def _sample(logits=0x1000, uniform=0x2000, tokens=0x3000, logp=None, rows=None, 
     (dict(logits=0x1002), I), (dict(logits=0x1001, dtype=1), I), (dict(uniform=0x2002), I),
     (dict(tokens=0x3001), I), (dict(logp=0x4002), I),
     (dict(rows=_abi.dspark_sample_rows(top_k=0x5002)), I),
-    (dict(rows=_abi.dspark_sample_rows(top_p=0x5001)), I)])
+    (dict(rows=_abi.dspark_sample_rows(top_p=0x5001)), I),
+    # (rows of logits: 0x1000 to 0x1640)
+    (dict(tokens=0x1000), I), (dict(tokens=0x163C), I), (dict(logp=0xFF4), I), (dict(tokens=0x200C), I),
+    (dict(logp=0x3000), I), (dict(logp=0x5000, rows=_abi.dspark_sample_rows(temperature=0x5000)), I),
+    (dict(tokens=0x5004, rows=_abi.dspark_sample_rows(top_k=0x5000)), I)])
 def test_sample_refusals(kw, status):
     assert _sample(**kw) == status
     assert ds.dspark_last_error()
@@ -51,7 +55,8 @@ def test_sample_refusals(kw, status):
     (dict(T=0), I), (dict(V=0), I), (dict(ld=99), I), (dict(dtype=3), I), (dict(k=0), I),
     (dict(k=101), I), (dict(k=1025, V=2000, ld=2000), U), (dict(T=(1 << 20) + 1), U),
     (dict(logits=None), I), (dict(ids=None), I), (dict(values=None), I), (dict(ids=0x2002), I),
-    (dict(lse=0x4001), I), (dict(logits=0x1001, dtype=1), I)])
+    (dict(lse=0x4001), I), (dict(logits=0x1001, dtype=1), I), (dict(ids=0x163C), I),
+    (dict(values=0x204C), I), (dict(lse=0x304C), I), (dict(lse=0x1000), I)])
 def test_top_logits_refusals(kw, status):
     c = dict(T=4, V=100, ld=100, dtype=0, k=5, logits=0x1000, ids=0x2000, values=0x3000, lse=None)
     c.update(kw)
@@ -82,7 +87,7 @@ def test_embed_call_refusals():
     for args in ((None, 0x2000, 0x3000), (0x100000, None, 0x3000), (0x100000, 0x2000, None),
                  (0x100002, 0x2000, 0x3000), (0x100000, 0x2001, 0x3000),
                  (0x100000, 0x2000, 0x100000), (0x100000, 0x2000, 0x100000 + 25600 - 4),
-                 (0x100000, 0x2000, 0x100000 - 1024 + 4)):
+                 (0x100000, 0x2000, 0x100000 - 1024 + 4), (0x100000, 0x2000, 0x200C)):
         assert ds.dspark_embed(c, *args) == I, args
     need = ds.dspark_embed_workspace_size(c)
     assert need > 0 and need % 256 == 0
@@ -90,7 +95,7 @@ def test_embed_call_refusals():
     for at, value, status in ((0, None, I), (1, None, I), (3, None, I), (0, 0x2002, I), (1, 0x3002, I),
                               (2, 0x200002, I), (3, 0x100001, I), (4, None, W), (4, 0x1000010, W),
                               (5, need - 1, W), (1, 0x100000, I), (1, 0x100000 + 25600 - 4, I),
-                              (2, 0x100004, I), (2, 0x100000 - 25600 + 4, I)):
+                              (2, 0x100004, I), (2, 0x100000 - 25600 + 4, I), (0, 0x100004, I)):
         args = list(ok)
         args[at] = value
         assert ds.dspark_embed_backward(c, *args) == status, (at, value)
