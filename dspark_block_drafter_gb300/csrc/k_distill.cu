@@ -50,9 +50,10 @@ __global__ void __launch_bounds__(128) distill_targets(const DistillPlan d) {
     if (k >= d.k) continue;
     const int id = d.ids[at + k];
     float s = d.logits[at + k];
-    bad |= id >= p.V;
-    // (a token of no probability is not listed; one that is not a number is, and tells)
-    const bool in = id >= 0 && id < p.V && !(s == -INFINITY);
+    // (a token of no probability is not listed, whatever its id; one that is not a number is, and
+    // tells)
+    const bool listed = id >= 0 && !(s == -INFINITY), in = listed && id < p.V;
+    bad |= listed && !in;
     s_id[warp][k] = in ? id : -1;
     if (!in) continue;
     int j = p.d2t ? loss_d2t_row(p.d2t, p.Vh, id) : id;

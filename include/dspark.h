@@ -498,7 +498,7 @@ dspark_status dspark_head_loss(const dspark_loss_config* cfg, const dspark_head*
 /* What a teacher says of every row: its listed tokens (dspark_top_logits makes such a list). */
 typedef struct dspark_teacher {
   const int32_t* ids;    /* device [T, k]: token ids; a negative one is absent */
-  const float* logits;   /* device [T, k] fp32: their logits; -infinity: absent */
+  const float* logits;   /* device [T, k] fp32: their logits; -infinity: absent, whatever the id */
   const float* lse;      /* device [T] fp32: the log-sum-exp of scale * logits over the
                             teacher's whole vocabulary, or NULL: over the listed tokens */
   int32_t k;             /* listed tokens a row, 1 .. 256 */

@@ -109,7 +109,7 @@ def distill_loss(hidden, lm_head, ids, logits, lse=None, t_scale=1.0, prev=None,
     s = np.asarray(logits, np.float64)
     for t in range(T):
         listed = [int(v) for v, x in zip(ids[t], s[t]) if v >= 0 and not x == -np.inf]
-        if any(v >= V for v in ids[t]) or len(set(listed)) < len(listed):
+        if any(v >= V for v in listed) or len(set(listed)) < len(listed):
             dropped += 1
             continue
         for j in range(k):
