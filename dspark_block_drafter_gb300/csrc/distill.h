@@ -1,6 +1,6 @@
 // Distillation of the head from a teacher's listed tokens: the call's plan and the host
 // launchers.  The products, the statistics and the sums over rows are the head loss's (loss.h),
-// with the first listed token of a row as its label; what the other listed tokens add is done
+// with the most probable listed token of a row as its label; what the other listed tokens add is done
 // by the kernels here.
 #pragma once
 
@@ -20,7 +20,7 @@ struct DistillPlan {
   const int32_t* ids;        // [T][k]
   const float *logits, *t_lse;        // [T][k], [T] or NULL
   // workspace
-  int32_t* label;            // [T] first listed token of the row, -1: none, V: refused
+  int32_t* label;            // [T] most probable listed token of the row, -1: none, V: refused
   int32_t* row;              // [T][k] head rows of the listed tokens, -1: absent; of the compact
                              // rows' tokens, compact head rows once their logits are known
   float* log_q;              // [T][k]

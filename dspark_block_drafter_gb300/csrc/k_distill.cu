@@ -4,15 +4,18 @@
 //   loss  = sum_k q_k (log q_k - log p_k),     d loss / d z_v = Q p_v - sum_k [v = id_k] q_k
 //
 // The gradient of the logits is the head loss's, times Q, but for the listed entries.  So the
-// head loss runs as it is (the row's first listed token as its label, Q times its weight), and
+// head loss runs as it is (the row's most probable listed token as its label, Q times its weight), and
 // the kernels here take the listed tokens' logits by dot products of their own, 64 of 151936
 // columns, in fp32 from the rows of the head (next to the three products of the whole head, 2%
 // of the time at 2048 rows), and write the listed entries of the gradient anew.
 //
 // A listed entry q (Q e^-x - 1), x = log q - log p, loses no digits where head and teacher
-// nearly agree: it is q (Q expm1(-x) + (Q - 1)).  In bf16 it is rounded to 8 bits like every
-// entry; with few rows the rounding is carried along (loss_low), otherwise that of the first
-// listed token is (LossPlan::qres).
+// nearly agree: it is q (Q expm1(-x) + (Q - 1)).  x itself is small where they are sure of one
+// token: as the label its -log p is the log1p of the other logits' weights, and its -log q the
+// log1p of the other listed tokens' (as differences of logits and log-sum-exps near 25, each is off
+// by 1e-6, more than such an entry).  In bf16 an entry is rounded to 8 bits like every other; with
+// few rows the rounding is carried along (loss_low), otherwise that of the label is
+// (LossPlan::qres).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -83,29 +86,34 @@ __global__ void __launch_bounds__(128) distill_targets(const DistillPlan d) {
     if (lane == 0) d.label[t] = bad ? p.V : -1;
     return;
   }
-  float lse;
+  // the label: the most probable one, the first of equals (where none is a number, the first)
+  int label = kMaxTargets;
+#pragma unroll
+  for (int q = kPerLane - 1; q >= 0; --q)
+    if (row[q] >= 0 && x[q] == top) label = lane + 32 * q;
+  label = __reduce_min_sync(0xFFFFFFFFu, label);
+  if (label == kMaxTargets) label = first;
+  float lse = 0.f;
   if (d.t_lse) {
     lse = d.t_lse[t];
   } else {
-    const float ref = top > -INFINITY ? top : 0.f;
+    // log q from the label's logit, the log-sum-exp of the others beside it
     float s = 0.f;
 #pragma unroll
     for (int q = 0; q < kPerLane; ++q)
-      if (row[q] >= 0) s += expf(x[q] - ref);
+      if (row[q] >= 0 && lane + 32 * q != label) s += expf(x[q] - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    lse = ref + logf(s);
-    // (log q from the reference, so that the sum's size costs it nothing)
-    top = logf(s);
+    s = log1pf(s);
 #pragma unroll
-    for (int q = 0; q < kPerLane; ++q) x[q] = (x[q] - ref) - top;
+    for (int q = 0; q < kPerLane; ++q) x[q] = (x[q] - top) - s;
   }
   float mass = 0.f;
 #pragma unroll
   for (int q = 0; q < kPerLane; ++q) {
     const int k = lane + 32 * q;
     if (k >= d.k) continue;
-    if (d.t_lse) x[q] -= lse;
+    x[q] -= lse;
     d.row[at + k] = row[q];
     d.log_q[at + k] = x[q];
     if (row[q] >= 0) mass += expf(x[q]);
@@ -113,7 +121,7 @@ __global__ void __launch_bounds__(128) distill_targets(const DistillPlan d) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xFFFFFFFFu, mass, o);
   if (lane == 0) {
-    d.label[t] = s_id[warp][first];
+    d.label[t] = s_id[warp][label];
     d.mass[t] = d.t_lse ? mass : (mass == mass ? 1.f : mass);
   }
 }

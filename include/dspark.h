@@ -528,9 +528,11 @@ size_t dspark_distill_loss_workspace_size(const dspark_loss_config* cfg,
  *
  * config, head, hidden, prev, weights, outputs (n_rows: rows with a loss), precision, workspace
  * and capture are as for dspark_head_loss.  The listed tokens' logits are taken by fp32 dot
- * products, and their entries of the logits' gradient by themselves, so that a loss near 0
- * keeps its gradient.  In bf16 these entries are rounded to 8 bits before the products, with
- * what the first listed token's lost given back to d_hidden and d_markov_w1.
+ * products, and their entries of the logits' gradient by themselves, each off by what its log q
+ * and log p are; the most probable listed token's by as little of themselves where both are
+ * near 0 (log q: without teacher->lse), so that a loss near 0 keeps its gradient.  In bf16 these
+ * entries are rounded to 8 bits before the products, with what the most probable listed token's
+ * lost given back to d_hidden and d_markov_w1.
  */
 dspark_status dspark_distill_loss(const dspark_loss_config* cfg, const dspark_head* head,
                                   const void* hidden, const int32_t* prev,
