@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
   const bool ahead = !HELD && !greedy && !classes && part.share >= 3 * 32 * kRing && (K <= 256 || !(TOP || cut_k));
   Weights ahead_w = {};
   u64 ahead_sum = 0;
+  int seen_octave = 0;
   uint32_t first = 0xFFFFFFFFu;                  // greedy: the lowest id of the maximum
   auto look = [&](int v, const uint4& x) {
     const float best = fmaxf(top, Vec<E>::top(x));
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
       row.put_count(n);
     } else {
       ahead_w.set(seen, tau, a.V);             // (nothing seen: far)
+      seen_octave = ahead_w.octave;
       if (!ahead_w.far) {
         part.each([&](int v, const uint4& raw) {
           if (Vec<E>::top(raw) > ahead_w.z_cap) ahead_sum >>= min(63, ahead_w.raise(Vec<E>::top(raw)));
@@ -630,7 +632,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
 #pragma unroll
                      for (int j = 0; j < VE; ++j) y[j] = z[j] == z_b;
                    },
-                   [&](int id, u64) {
+                   [&](int id, u64, u64) {
                      row.tell_border((u64)key_b << 32 | (0xFFFFFFFFu - (uint32_t)id));
                    });
           b = row.told_border();
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
             const u64 own = own_above + warp_sum(kept_mass) + kept_ties * w_b;
             const u64 all = row.row_sum(own, before);
             row.find(draw_target(a.uniform[t], all), before, own, kept,
-                     [&](int id, u64 x) { write_token(a, t, id, x, all); });
+                     [&](int id, u64 x, u64) { write_token(a, t, id, x, all); });
             return;
           }
         }
@@ -689,7 +691,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
             const u64 own = own_above + sh.extra[warp];
             const u64 all = row.row_sum(own, before);
             row.find(draw_target(a.uniform[t], all), before, own, kept,
-                     [&](int id, u64 x) { write_token(a, t, id, x, all); });
+                     [&](int id, u64 x, u64) { write_token(a, t, id, x, all); });
             return;
           }
         }
@@ -700,14 +702,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
     if (!found) row.template locate<true>(target, b, b.key, key, 0, w);
   }
   if (ahead && !cut_k && !cut_p && !(min_p > 0.f) && !ahead_w.far && !w.far) {
-    // from the sums of the one pass.  (A lane's may have lost a unit in every octave it rose:
-    // where the draw falls behind all of them, it is made anew.)
-    int down = w.octave - ahead_w.octave;
-    const u64 own = warp_sum(down < 64 ? ahead_sum >> max(0, down) : 0ull);
-    const u64 mass = row.row_sum(own, before);
+    // From the sums of the one pass.  Where the rest of the row had a larger logit (by an octave),
+    // they began in finer units, and hold up to one unit more for each weight, whose cut-off parts
+    // they add up: the exact mass, what lies before a token and the target are each less by 0 to
+    // V.  A token that holds the target by more than that on both sides is the exact sums' too;
+    // any other draw is made anew (and one that falls behind the last weight).
+    const int down = w.octave - ahead_w.octave;
+    const u64 own = warp_sum(down < 64 ? ahead_sum >> down : 0ull);
+    const u64 mass = row.row_sum(own, before), slack = w.octave > seen_octave ? (u64)a.V : 0ull;
     if (tid == 0) sh.least_id = 0;
     __syncthreads();
-    row.find(draw_target(a.uniform[t], mass), before, own, kept, [&](int id, u64 x) {
+    row.find(draw_target(a.uniform[t], mass), before, own, kept, [&](int id, u64 x, u64 past) {
+      if (past < slack || x - past <= slack) return;
       write_token(a, t, id, x, mass);
       sh.least_id = 1;
     });
@@ -721,7 +727,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
   };
   const u64 own = row.own_sum(drawn), mass = row.row_sum(own, before);
   row.find(draw_target(a.uniform[t], mass), before, own, drawn,
-           [&](int id, u64 x) { write_token(a, t, id, x, mass); });
+           [&](int id, u64 x, u64) { write_token(a, t, id, x, mass); });
 }
 
 }  // namespace

@@ -6,7 +6,9 @@
 // units.  Sums of them are exact in 64 bits, in any order and by atomics too, so that the same row
 // gives the same token however it is split, and a border of a long sum lies where the
 // definition has it.  (An fp32 sum of 151936 weights is off by some 1e-7 of itself: among as many
-// tokens, that is the next token in one row of a hundred.)
+// tokens, that is the next token in one row of a hundred.)  The one sum that is taken before the
+// largest is known is in finer units; a draw from it counts where that cannot matter, and is made
+// anew where it could (k_sample.cu).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -425,8 +427,8 @@ struct Row {
     });
     return warp_sum(s);
   }
-  // The first id at which the running sum exceeds `target`: found(id, x) is called by one
-  // thread of the cluster.
+  // The first id at which the running sum exceeds `target`: found(id, x, past) is called by one
+  // thread of the cluster; `past`: how far into this id's x the target lies.
   template <typename F, typename H>
   __device__ __forceinline__ void find(u64 target, u64 before, u64 own, F f, H found) {
     if (target < before || target >= before + own) return;
@@ -452,7 +454,7 @@ struct Row {
         run += x[j];
         if (!hit && left < run) {
           hit = true;
-          found(part.id(v, j), x[j]);
+          found(part.id(v, j), x[j], x[j] - (run - left));
         }
       }
     });
@@ -737,7 +739,7 @@ struct Row {
         u64 first;
         const u64 own = own_sum(ones);
         row_sum(own, first);
-        find(nth - 1, first, own, ones, [&](int id, u64) {
+        find(nth - 1, first, own, ones, [&](int id, u64, u64) {
           tell_border((u64)key << 32 | (0xFFFFFFFFu - (uint32_t)id));
         });
         b = told_border();

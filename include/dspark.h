@@ -673,9 +673,10 @@ typedef struct dspark_sample_rows {
  * logp    device [T] fp32 or NULL: the token's log-probability among the kept ones
  *
  * Weights are cut to whole multiples of 2^-S of the largest, S = 62 - ceil(log2 V) (44 for
- * 151936 tokens), and off by at most 2^-27 of themselves besides; their sums are exact.  tokens
- * and logp overlap nothing else.  Needs no workspace; calls may run at once.  Can be captured into
- * a CUDA graph.
+ * 151936 tokens), and off by at most 2^-27 of themselves besides.  The token is that of their exact
+ * sums, whatever the call's other rows; the mass that logp is made of may be V of those units too
+ * large.  tokens and logp overlap nothing else.  Needs no workspace; calls may run at once.  Can be
+ * captured into a CUDA graph.
  */
 dspark_status dspark_sample(const dspark_sample_config* cfg, const dspark_sample_rows* rows,
                             const void* logits, const float* uniform, int32_t* tokens,

@@ -110,8 +110,8 @@ def test_head_that_agrees_with_its_teacher_entry_by_entry(order, T, pieces, dtyp
 @pytest.mark.parametrize("T,pieces", [(24, 0), (24, 3), (100, 0), (100, 3)])
 @pytest.mark.parametrize("order", ["falling", "rising", "shuffled"])
 def test_head_that_agrees_with_a_sure_teacher(order, T, pieces, dtype):
-    """Head and teacher give one token nearly all: the gradient is of the size of what is left, wherever in
-    the list the token stands."""
+    """Head and teacher give one token nearly all: the gradient is of the size of what is left,
+    wherever in the list the token stands."""
     rng = np.random.default_rng(T + 1)
     H, V, k = 64, 512, 20
     W, h = _tensor(rng, V, H, std=0.3, dtype=dtype), _tensor(rng, T, H, dtype=dtype)
