@@ -108,13 +108,15 @@ struct Weights {
     far = !(fabsf(top * c_hi) < 60000.f) || !(c_hi > 1e-6f);
     shift = 32 - __clz(max(1, V - 1));          // ceil(log2 V): S = 62 - shift
     t_lane = kExp2[threadIdx.x % 32];
+    octave = 0;
     raise(top);
   }
   // makes room for a logit of `top`; the octaves that this took
   __device__ __forceinline__ int raise(float top) {
     const int was = octave;
-    // steps of 1/32 up to it, in whole octaves
-    octave = far ? 1 : ((__float2int_ru(__fmul_rn(top, c_hi) * 32.f) + 2) >> 5) + 1;
+    // steps of 1/32 up to it, in whole octaves (a row with one above 60000 is far, and what the
+    // weights before it made is not used)
+    octave = far ? 1 : ((__float2int_ru(fminf(__fmul_rn(top, c_hi), 65536.f) * 32.f) + 2) >> 5) + 1;
     magic = 393216.f - (float)octave;           // 1.5 * 2^18 - octave: a sum's low bits count 1/32
     z_low = far ? -100.f : ((float)octave - 100.f) / c_hi;
     z_cap = far ? INFINITY : top;
