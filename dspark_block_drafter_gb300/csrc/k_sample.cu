@@ -194,8 +194,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
   row.started();
 
   // the row, its maximum, and for the k largest its sum of exponentials: 2^(z log2(e) - ref), ref
-  // the rounded log2(e) times the running maximum
-  float top = -INFINITY, sum = 0.f, ref = 0.f;
+  // the rounded log2(e) times a logit that the running maximum is at most 11 above.  (A sum that
+  // takes every maximum as its reference is scaled, and rounded, at every vector of a rising row.)
+  float top = -INFINITY, ref = 0.f, near_to = -INFINITY;
+  LongSum sum;
   // one CTA a row, and rows long enough: one pass does the rest too, where a look at a part of
   // the row tells what to expect
   const bool ahead = !HELD && !greedy && !classes && part.share >= 3 * 32 * kRing && (K <= 256 || !(TOP || cut_k));
@@ -206,16 +208,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
   auto look = [&](int v, const uint4& x) {
     const float best = fmaxf(top, Vec<E>::top(x));
     if (TOP && a.lse) {
-      if (best > top) {
+      if (best > near_to) {
         const float r = best * kLog2e;
-        sum = top > -INFINITY ? sum * fast_exp2(ref - r) : 0.f;
+        sum.scale(near_to > -INFINITY ? fast_exp2(ref - r) : 0.f);
         ref = r;
+        near_to = best + 11.f;
       }
       float z[VE], s[4] = {};
       Vec<E>::get(x, z);
 #pragma unroll
       for (int j = 0; j < VE; ++j) s[j % 4] += fast_exp2(fmaf(z[j], kLog2e, -ref));
-      sum += (s[0] + s[1]) + (s[2] + s[3]);
+      sum.add((s[0] + s[1]) + (s[2] + s[3]), chain_ends(v));
     }
     if (!TOP && greedy && best > top) {
       float z[VE];
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
     float all = 0.f, cta_ref = 0.f;
     if (TOP && a.lse) {
       cta_ref = value_of(key) * kLog2e;
-      float s = top > -INFINITY ? sum * fast_exp2(ref - cta_ref) : 0.f;
+      float s = top > -INFINITY ? sum.value() * fast_exp2(ref - cta_ref) : 0.f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
       __syncthreads();
@@ -361,16 +364,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) rows_kernel(const RowArgs a) {
       if (key > kNoKey && !plain) {
         // a logit is no number, or so large that the reference is none: the sum of those that are,
         // from their distances
-        float s1 = 0.f;
+        LongSum own;
         part.each([&](int v, const uint4& raw) {
-          float z[VE];
+          float z[VE], s[4] = {};
           Vec<E>::get(raw, z);
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
             const float x = z[j] == m ? 0.f : fmaxf(z[j] - m, -150.f);
-            s1 += z[j] > -INFINITY ? fast_exp2(x * kLog2e) : 0.f;
+            s[j % 4] += z[j] > -INFINITY ? fast_exp2(x * kLog2e) : 0.f;
           }
+          own.add((s[0] + s[1]) + (s[2] + s[3]), chain_ends(v));
         });
+        float s1 = own.value();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
         __syncthreads();

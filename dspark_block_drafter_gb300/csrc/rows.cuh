@@ -80,6 +80,31 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// An fp32 sum of many values that is as good for many as for a few: chains of values, and the
+// chains' sums with their rounding errors (Knuth's two-sum).  A plain sum of 4000 equal values,
+// whose roundings go one way within an octave, was off by 5e-5 of itself.
+struct LongSum {
+  float sum = 0.f, err = 0.f, chain = 0.f;
+  __device__ __forceinline__ void add(float x, bool last) {
+    chain += x;
+    if (!last) return;
+    const float t = sum + chain, b = t - sum;
+    err += (sum - (t - b)) + (chain - b);
+    sum = t;
+    chain = 0.f;
+  }
+  __device__ __forceinline__ void scale(float x) {
+    sum *= x;
+    err *= x;
+    chain *= x;
+  }
+  __device__ __forceinline__ float value() const { return sum + (err + chain); }
+};
+// Whether a lane's vector v is the last of a chain of 32: alike in all lanes of its warp.
+__device__ __forceinline__ bool chain_ends(int v) {
+  return ((v - (int)(threadIdx.x % 32)) & 0x3E0) == 0x3E0;
+}
+
 // The border of the kept set.
 struct Border {
   uint32_t key;

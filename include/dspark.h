@@ -690,7 +690,8 @@ dspark_status dspark_sample(const dspark_sample_config* cfg, const dspark_sample
  * ids     device [T, k] int32, values device [T, k] fp32: by falling logit, equal ones by rising
  *         id.  -infinity and NaN are not listed: where fewer than k others are left, -1 and
  *         -infinity stand (absent, for dspark_distill_loss)
- * lse     device [T] fp32 or NULL: log sum exp of the row (NaN left out)
+ * lse     device [T] fp32 or NULL: log sum exp of the row (NaN left out), off by at most 2^-17 and
+ *         2^-22 of itself whatever V is (the roundings' sum; as a rule some 1e-7)
  *
  * The outputs overlap nothing else.  Needs no workspace; calls may run at once.  Can be captured
  * into a CUDA graph.
