@@ -713,7 +713,7 @@ typedef struct dspark_embed_config {
  * dspark_embed -- out[t] = scale * table[ids[t]].
  *
  * table   device [V, H]      ids  device [T] int32; a row whose id is outside [0, V) is zeros
- * out     device [T, H], rounded once; overlaps nothing else
+ * out     device [T, H]: the fp32 product, in bf16 rounded to it; overlaps nothing else
  */
 dspark_status dspark_embed(const dspark_embed_config* cfg, const void* table,
                            const int32_t* ids, void* out, void* stream);
@@ -732,9 +732,10 @@ size_t dspark_embed_workspace_size(const dspark_embed_config* cfg);
  *         tied lm_head.  May be d_table itself: then only rows that occur are read and written
  * d_table device [V, H], overwritten; overlaps nothing else
  *
- * Sums are fp32, over a token's rows in their order (in parts, for tokens of many rows), and
- * rounded once.  The same call gives the same bits.  Not reentrant on one workspace.  Can be
- * captured into a CUDA graph.
+ * Sums are fp32, over a token's rows in their order, in parts of at most max(32, ceil(T / 2432))
+ * rows that are joined with their rounding errors; scale times the sum (with add: fused with it) is
+ * rounded to fp32, and in bf16 that to bf16.  The same call gives the same bits.  Not reentrant on
+ * one workspace.  Can be captured into a CUDA graph.
  */
 dspark_status dspark_embed_backward(const dspark_embed_config* cfg, const int32_t* ids,
                                     const void* d_out, const void* add, void* d_table,
