@@ -24,17 +24,17 @@ def _draw(x, u, **settings):
     return tokens.cpu().numpy(), logp.double().cpu().numpy()
 
 
-def _same_token(z, u, dtype, temperature=1.0):
+def _same_token(z, u, dtype, **settings):
     """Of the first rows alone (held by clusters) and of all of them, 64 and 320 (one CTA each, of
     1024 and of 512 threads)."""
     x = torch.from_numpy(z.astype(np.float32)).cuda().to(DT[dtype])
     u = torch.from_numpy(u.astype(np.float32)).cuda()
     n = len(z)
-    want, lp = _draw(x, u, temperature=temperature)
+    want, lp = _draw(x, u, **settings)
     assert np.all((want >= 0) & (want < z.shape[1]))
     for T in (64, 320):
         at = torch.arange(T, device="cuda") % n
-        tokens, logp = _draw(x[at], u[at], temperature=temperature)
+        tokens, logp = _draw(x[at], u[at], **settings)
         assert np.array_equal(tokens, want[at.cpu().numpy()]), (T, np.sum(tokens[:n] != want))
         # (the other tokens' mass, in a sum that may be off by a unit a weight; log1p of its ratio
         # to the token's, as everywhere)
@@ -75,3 +75,15 @@ def test_draw_of_a_row_with_a_late_logit_of_any_size(dtype):
     z = np.random.default_rng(3).normal(size=(n, V))
     z[:, V - 1] = np.resize([np.inf, 3e38, 1e30, 1e9, 70000.0, 30000.0, 2000.0, 90.0], n)
     _same_token(z, np.random.default_rng(4).uniform(size=n), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("settings", [dict(temperature=0.8), dict(top_p=0.9), dict(top_p=0.999, min_p=0.01),
+                                      dict(min_p=0.05), dict(top_k=40, top_p=0.9), dict(top_k=3000)],
+                         ids=str)
+def test_draw_by_every_filter(settings, dtype):
+    rng = np.random.default_rng(len(settings))
+    n, V = 40, 150001
+    z = -rng.uniform(0.7, 2.2, (n, 1)) * np.log(rng.uniform(size=(n, V)) * V + 1) + 18
+    z += rng.normal(size=(n, V)) * 0.5
+    _same_token(z, rng.uniform(size=n), dtype, **settings)
